@@ -59,7 +59,20 @@ typedef enum {
    * otherwise); N a multiple of 16, A, B, C 16-byte aligned, and one tile's
    * panels within 32-bit byte offsets (tile_m*K, 128*N and tile_m*N*2 all
    * below 2^31) (PGEMM_ERR_UNSUPPORTED otherwise). */
-  PGEMM_FP8E4M3_B128_OUT_BF16 = 2
+  PGEMM_FP8E4M3_B128_OUT_BF16 = 2,
+  /* MXFP4: A and B of OCP e2m1 codes, two to a byte, the even k in the low
+   * nibble, with one e8m0 scale byte per 32 consecutive k.  Both operands run
+   * along K: A [M][K/2] bytes, B [N][K/2] bytes (a weight matrix as out x in),
+   * and C[m][n] = sum over k of a[m][k] * b[n][k].  a_scale [K/128][M][4],
+   * b_scale [K/128][N][4]: four consecutive bytes scale the four blocks of a
+   * row's 128 k.  value = e2m1(code) * 2^(byte - 127), byte 255 is NaN; fp32
+   * accumulate; C bf16 or fp32.  K must be a multiple of 128
+   * (PGEMM_ERR_INVALID otherwise; pmx_quant_run pads with zeros); A, B
+   * 16-byte and the scales 4-byte aligned, C aligned to its elements, and one
+   * tile's panels within 32-bit byte offsets (PGEMM_ERR_UNSUPPORTED
+   * otherwise); any M and N. */
+  PGEMM_MXFP4_OUT_BF16 = 3,
+  PGEMM_MXFP4_OUT_F32 = 4
 } pgemm_dtype;
 
 /* Tile schedulers.  T = number of output tiles, G = grid (programs), X = XCDs.
@@ -137,7 +150,8 @@ typedef enum {
 
 /* Optional per-call arguments; pass NULL for all defaults. */
 typedef struct {
-  int tile_m, tile_n, tile_k; /* 0 => default: bf16 256x256x64, fp8 256x256x128 */
+  int tile_m, tile_n, tile_k; /* 0 => default: bf16 256x256x64, fp8 256x256x128, MXFP4 by
+                                 the sizes (pgemm_plan_gemm reports it) */
   int group_size;             /* grouped order rows per group; 0 => 8 for the GEMM, 1 for the
                                  add (memory order: an add has no operand panels to keep in L2,
                                  and tiles side by side in a row spread over the memory channels) */
@@ -151,8 +165,8 @@ typedef struct {
   int claim_chunk;            /* tiles per work-stealing claim (consecutive in the counter's
                                  range); GEMM 1..64 or PGEMM_CLAIM_PAIRS, 0 => 1; add 1..U
                                  (tiles a program handles per step), 0 => U */
-  const uint8_t* a_scale;     /* fp8: device, e8m0 [K/128][M] */
-  const uint8_t* b_scale;     /* fp8: device, e8m0 [K/128][N] */
+  const uint8_t* a_scale;     /* fp8: device, e8m0 [K/128][M]; MXFP4: [K/128][M][4] */
+  const uint8_t* b_scale;     /* fp8: device, e8m0 [K/128][N]; MXFP4: [K/128][N][4] */
   unsigned debug_flags;       /* PGEMM_DEBUG_* */
   int straggler_program;      /* with PGEMM_DEBUG_STRAGGLER */
   int straggler_ns;           /* with PGEMM_DEBUG_STRAGGLER */
@@ -307,12 +321,12 @@ PGEMM_API pgemm_status padd_run(pgemm_config* cfg, const float* X, const float* 
  * by virtual id. */
 #define PGEMM_MAX_PROBLEMS 8
 typedef struct {
-  const void* A;   /* device, bf16 or e4m3 [M][K] */
-  const void* B;   /* device, bf16 or e4m3 [K][N] */
+  const void* A;   /* device, bf16 or e4m3 [M][K]; MXFP4 [M][K/2] */
+  const void* B;   /* device, bf16 or e4m3 [K][N]; MXFP4 [N][K/2] */
   void* C;         /* device, [M][N] of the dtype's output type */
   int64_t M, N, K;
-  const uint8_t* a_scale;  /* fp8: device, e8m0 [K/128][M]; otherwise ignored */
-  const uint8_t* b_scale;  /* fp8: device, e8m0 [K/128][N]; otherwise ignored */
+  const uint8_t* a_scale;  /* fp8: device, e8m0 [K/128][M]; MXFP4: [K/128][M][4]; otherwise ignored */
+  const uint8_t* b_scale;  /* fp8: device, e8m0 [K/128][N]; MXFP4: [K/128][N][4]; otherwise ignored */
 } pgemm_problem;
 
 PGEMM_API pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems, int count,
@@ -379,7 +393,8 @@ typedef enum {
   PGEMM_KERNEL_BF16_STAGED = 1,  /* bf16, register-staged (any shape and alignment) */
   PGEMM_KERNEL_FP8 = 2,          /* block-scaled fp8 */
   PGEMM_KERNEL_ADD = 3,          /* persistent add */
-  PGEMM_KERNEL_BF16_PINGPONG = 4 /* bf16, eight waves in ping-pong (PGEMM_PIPELINE_PINGPONG) */
+  PGEMM_KERNEL_BF16_PINGPONG = 4, /* bf16, eight waves in ping-pong (PGEMM_PIPELINE_PINGPONG) */
+  PGEMM_KERNEL_FP4 = 5            /* MXFP4 */
 } pgemm_kernel;
 
 /* Launch a call would make.  A persistent launch runs one program per
@@ -409,6 +424,97 @@ PGEMM_API pgemm_status pgemm_plan_gemm(pgemm_config* cfg, const void* A, const v
 PGEMM_API pgemm_status pgemm_plan_add(pgemm_config* cfg, const float* X, const float* Y, const float* C,
                             int64_t rows, int64_t cols, int tile_rows, int tile_cols,
                             pgemm_sched sched, const pgemm_args* args, pgemm_plan* out);
+
+/* ---- Operands of the block-scaled GEMMs ---------------------------------
+ * Entry points that make, undo and feed the quantised operands above.  All
+ * follow pgemm_run's rules: argument errors are reported before anything is
+ * enqueued (NULL pointers, negative sizes, row strides below the row's length,
+ * buffers that do not lie inside one device allocation of the config's
+ * device, overlaps not named as allowed: PGEMM_ERR_INVALID; type combinations
+ * not built: PGEMM_ERR_UNSUPPORTED), calls are asynchronous on hip_stream,
+ * allocate nothing and may be captured into a graph.  rows == 0 is a call
+ * with no rows (row buffers may then be NULL).  Buffers need the alignment
+ * of their elements only; 16-byte aligned rows take the wide accesses. */
+
+/* Element types of pmx_* and prms_* matrices. */
+#define PMX_F32 0
+#define PMX_BF16 1
+#define PMX_F16 2
+
+/* How a block's scale exponent follows from its largest magnitude amax (emax
+ * and top: the largest exponent and largest value of the element format, 2
+ * and 6 for e2m1, 8 and 448 for e4m3).
+ *  CEIL   the smallest e with amax <= top * 2^e: nothing saturates.
+ *  FLOOR  e = floor(log2(amax)) - emax (OCP Microscaling Formats v1.0, 6.3):
+ *         values past top * 2^e saturate to it.
+ * e is clamped to [-127, 127] and stored as the byte e + 127; a block of zeros
+ * has byte 0; a block with an infinity or a NaN has byte 255 (NaN) and zero
+ * codes, so all of its values are NaN. */
+#define PMX_SCALE_CEIL 0
+#define PMX_SCALE_FLOOR 1
+
+/* MXFP4 operand of a matrix X [rows][cols] (x_type, row stride ldx elements):
+ * code = e2m1(x * 2^-e), rounded to nearest, ties to even, blocks of 32.
+ *  transpose == 0  blocks along the columns: Q [rows][Kp/2], scale
+ *                  [Kp/128][rows][4] with Kp = cols rounded up to 128.
+ *  transpose == 1  blocks along the rows, the operand of X^T: Q [cols][Kp/2],
+ *                  scale [Kp/128][cols][4] with Kp = rows rounded up to 128
+ *                  (the contraction over tokens of a weight gradient).
+ * The padding up to Kp is written as zero codes; a block wholly in the padding
+ * has scale byte 0.  Q must be 4-byte and scale 4-byte aligned
+ * (PGEMM_ERR_UNSUPPORTED otherwise). */
+PGEMM_API pgemm_status pmx_quant_run(pgemm_config* cfg, const void* X, int x_type, int64_t rows, int64_t cols,
+                           int64_t ldx, int transpose, int rule, uint8_t* Q, uint8_t* scale,
+                           void* hip_stream);
+
+/* Y [rows][cols] (y_type, row stride ldy elements) = the values of an MXFP4
+ * operand Q [rows][Kp/2], scale [Kp/128][rows][4], Kp = cols rounded up to
+ * 128; rounded to nearest even where the type does not hold the value (past
+ * its range: infinity).  Same alignment as pmx_quant_run. */
+PGEMM_API pgemm_status pmx_dequant_run(pgemm_config* cfg, const uint8_t* Q, const uint8_t* scale, int64_t rows,
+                             int64_t cols, void* Y, int y_type, int64_t ldy, void* hip_stream);
+
+/* What prms_run writes to Y. */
+#define PRMS_OUT_SAME 0     /* [rows][cols] of X's type, row stride ldy */
+#define PRMS_OUT_FP8_B128 1 /* e4m3 [rows][Kp], y_scale [Kp/128][rows]: the A operand of
+                               PGEMM_FP8E4M3_B128_OUT_BF16 */
+#define PRMS_OUT_MXFP4 2    /* codes [rows][Kp/2], y_scale [Kp/128][rows][4]: an operand of
+                               PGEMM_MXFP4_OUT_* */
+
+/* Root-mean-square norm of rows, with the residual's addition before it and
+ * the quantisation of the next product's operand after it:
+ *   h = x + r, rounded to r_type and written to H    (R NULL: h = x, H NULL)
+ *   rstd = 1 / sqrt(mean(h^2) + eps), written to rstd (fp32 [rows]; may be NULL)
+ *   y = h * rstd * w, rounded once to the output's type (scale rule CEIL)
+ * X [rows][cols] x_type, R and H [rows][cols] r_type (x_type or PMX_F32), W
+ * [cols] w_type (x_type or PMX_F32); ld*: row strides in elements (ldy: of
+ * PRMS_OUT_SAME; the quantised forms are dense, Kp = cols rounded up to 128,
+ * padding zero).  The norm is taken of h as stored, in 64 bits, so y is the
+ * correctly rounded value of the formula.  H may be R, or X if the types and
+ * strides are the same, exactly (in place); Y may be X exactly under
+ * PRMS_OUT_SAME with the same stride.  Quantised Y and y_scale 4-byte (e4m3:
+ * Y 8-byte) aligned (PGEMM_ERR_UNSUPPORTED otherwise). */
+PGEMM_API pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx, const void* R, int r_type,
+                      int64_t ldr, const void* W, int w_type, double eps, int64_t rows, int64_t cols,
+                      void* H, int64_t ldh, int out, void* Y, int64_t ldy, uint8_t* y_scale, float* rstd,
+                      void* hip_stream);
+
+/* Gradients of prms_run, the rounding of its output taken as the identity:
+ *   g = w * dy, dx = dh + rstd * g - h * rstd^3 * sum(g * h) / cols
+ *   dw = sum over the rows of dy * h * rstd
+ * dY [rows][cols] y_type, H (the h of the forward), dH (the gradient that
+ * reaches h past the norm; may be NULL: none) and dX h_type (y_type or
+ * PMX_F32), W w_type (y_type or PMX_F32), rstd fp32 [rows] as prms_run wrote
+ * it, dW fp32 [cols] (may be NULL: not computed).  dX is the gradient of both
+ * x and r.  Sums in fp32 in an order that depends on the sizes only, so results
+ * repeat bit for bit.  dX may be dH exactly, or dY exactly if the types are
+ * the same (same stride).  The partial sums of dW live in the config's
+ * workspace (see pgemm_config_create): PGEMM_ERR_UNSUPPORTED if one row of
+ * cols floats does not fit there.  rows == 0 writes zeros to dW. */
+PGEMM_API pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_t ldy, const void* H,
+                           int h_type, int64_t ldh, const void* dH, int64_t ldd, const void* W, int w_type,
+                           const float* rstd, int64_t rows, int64_t cols, void* dX, int64_t ldx,
+                           float* dW, void* hip_stream);
 
 /* Static string for a status code. */
 PGEMM_API const char* pgemm_status_str(pgemm_status s);

@@ -1,5 +1,6 @@
-"""Persistent tiled GEMM and persistent 2-D add with tile schedulers, for
-AMD Instinct MI355X (gfx950).
+"""Persistent tiled GEMM and persistent 2-D add with tile schedulers, and the
+operators that make the block-scaled GEMMs' operands (MXFP4 quantisation, RMS
+norm with a quantised output), for AMD Instinct MI355X (gfx950).
 
 A thin Python binding over the C ABI of libpgemm.so (include/pgemm.h): the
 functions keep the C names, marshal torch device tensors (or raw device
@@ -29,10 +30,15 @@ DTYPES = {
     "bf16_out_f32": _abi.BF16_OUT_F32,
     "bf16_out_bf16": _abi.BF16_OUT_BF16,
     "fp8_b128_out_bf16": _abi.FP8E4M3_B128_OUT_BF16,
+    "mxfp4_out_bf16": _abi.MXFP4_OUT_BF16,
+    "mxfp4_out_f32": _abi.MXFP4_OUT_F32,
 }
+SCALE_RULES = {"ceil": _abi.PMX_SCALE_CEIL, "floor": _abi.PMX_SCALE_FLOOR}
+RMS_OUTPUTS = {"same": _abi.PRMS_OUT_SAME, "fp8_b128": _abi.PRMS_OUT_FP8_B128, "mxfp4": _abi.PRMS_OUT_MXFP4}
 
 __all__ = ["Config", "pgemm_run", "pgemm_run_noalloc", "pgemm_run_grouped", "padd_run", "padd_run_multi", "plan_gemm", "plan_add", "SCHEDULERS",
-           "DTYPES", "PgemmError", "status_str", "make_args"]
+           "pmx_quant_run", "pmx_dequant_run", "prms_run", "prms_grad_run", "mxfp4_bytes", "SCALE_RULES",
+           "RMS_OUTPUTS", "DTYPES", "PgemmError", "status_str", "make_args"]
 
 
 def _check(where, code):
@@ -53,17 +59,24 @@ def _torch_dtypes(names):
 
 # Element types the calls accept: operands per pgemm_dtype, outputs, adds.
 _OPERAND = {_abi.BF16_OUT_F32: ("bfloat16",), _abi.BF16_OUT_BF16: ("bfloat16",),
-            _abi.FP8E4M3_B128_OUT_BF16: ("uint8", "float8_e4m3fn")}
+            _abi.FP8E4M3_B128_OUT_BF16: ("uint8", "float8_e4m3fn"),
+            _abi.MXFP4_OUT_BF16: ("uint8", "float4_e2m1fn_x2"), _abi.MXFP4_OUT_F32: ("uint8", "float4_e2m1fn_x2")}
 _OUTPUT = {_abi.BF16_OUT_F32: ("float32",), _abi.BF16_OUT_BF16: ("bfloat16",),
-           _abi.FP8E4M3_B128_OUT_BF16: ("bfloat16",)}
-_SCALE = ("uint8",)
+           _abi.FP8E4M3_B128_OUT_BF16: ("bfloat16",),
+           _abi.MXFP4_OUT_BF16: ("bfloat16",), _abi.MXFP4_OUT_F32: ("float32",)}
+_SCALE = ("uint8", "float8_e8m0fnu")
 _F32 = ("float32",)
+_FP4 = ("uint8", "float4_e2m1fn_x2")
 
 
 def gemm_bytes(M: int, N: int, K: int, dtype) -> dict:
     """Bytes each buffer of a GEMM call spans: A [M][K], B [K][N], C [M][N]
-    and (block-scaled fp8) the scales [K/128][M] and [K/128][N]."""
+    and (block-scaled fp8) the scales [K/128][M] and [K/128][N]; MXFP4:
+    A [M][K/2], B [N][K/2] and the scales [K/128][M][4] and [K/128][N][4]."""
     d = _dtype(dtype)
+    if d in (_abi.MXFP4_OUT_BF16, _abi.MXFP4_OUT_F32):
+        return {"A": M * (K // 2), "B": N * (K // 2), "C": M * N * (2 if d == _abi.MXFP4_OUT_BF16 else 4),
+                "a_scale": (K // 128) * M * 4, "b_scale": (K // 128) * N * 4}
     esz = 1 if d == _abi.FP8E4M3_B128_OUT_BF16 else 2
     csz = 4 if d == _abi.BF16_OUT_F32 else 2
     out = {"A": M * K * esz, "B": K * N * esz, "C": M * N * csz}
@@ -316,7 +329,7 @@ def padd_run_multi(cfg: Config, problems, tile_rows: int, tile_cols: int, sched,
 def pgemm_run_grouped(cfg: Config, problems, dtype, sched, args=None, stream=None):
     """Several GEMMs C_g = A_g . B_g in one persistent launch; `problems` is a
     sequence of (A, B, C, M, N, K), or (A, B, C, M, N, K, a_scale, b_scale)
-    for block-scaled fp8."""
+    for block-scaled fp8 and MXFP4."""
     n = len(problems)
     arr = (_abi.pgemm_problem * max(n, 1))()
     for g, pr in enumerate(problems):
@@ -324,7 +337,9 @@ def pgemm_run_grouped(cfg: Config, problems, dtype, sched, args=None, stream=Non
         arr[g].A, arr[g].B, arr[g].C = _gemm_ptrs(A, B, C, M, N, K, dtype, None, f"[{g}]")
         arr[g].M, arr[g].N, arr[g].K = int(M), int(N), int(K)
         if len(pr) == 8:
-            nb = gemm_bytes(int(M), int(N), int(K), "fp8_b128_out_bf16")
+            nb = gemm_bytes(int(M), int(N), int(K), dtype)
+            if "a_scale" not in nb:  # the scales of an unscaled type are ignored
+                nb = {"a_scale": 0, "b_scale": 0}
             arr[g].a_scale = _ptr(pr[6], f"a_scale[{g}]", _SCALE, nb["a_scale"])
             arr[g].b_scale = _ptr(pr[7], f"b_scale[{g}]", _SCALE, nb["b_scale"])
     code = _abi.lib().pgemm_run_grouped(cfg.handle, arr, n, _dtype(dtype), _sched(sched),
@@ -332,3 +347,137 @@ def pgemm_run_grouped(cfg: Config, problems, dtype, sched, args=None, stream=Non
                                         _stream(stream, cfg.device))
     _check("pgemm_run_grouped", code)
 
+
+def mxfp4_bytes(rows: int, cols: int) -> dict:
+    """Bytes of an MXFP4 operand of a [rows][cols] matrix: codes Q [rows][Kp/2]
+    and scale [Kp/128][rows][4], Kp = cols rounded up to 128."""
+    kp = -(-cols // 128) * 128
+    return {"Q": rows * (kp // 2), "scale": (kp // 128) * rows * 4}
+
+
+_ELEM = {}
+
+
+def _elem(x, what, given=None):
+    """PMX_* element type of a tensor argument (raw pointers: `given`)."""
+    if isinstance(x, int):
+        if given is None:
+            raise ValueError(f"{what}: a raw pointer needs its element type")
+        return int(given)
+    if not _ELEM:
+        import torch
+        _ELEM.update({torch.float32: _abi.PMX_F32, torch.bfloat16: _abi.PMX_BF16, torch.float16: _abi.PMX_F16})
+    t = _ELEM.get(getattr(x, "dtype", None))
+    if t is None:
+        raise ValueError(f"{what}: expected a float32, bfloat16 or float16 tensor")
+    return t
+
+
+def _matrix(x, what, rows, cols, ld=None):
+    """(device pointer, row stride) of a [rows][cols] matrix: a 2-D tensor with
+    dense rows, a contiguous tensor of at least rows * cols elements, or a raw
+    pointer with its row stride `ld`."""
+    if isinstance(x, int):
+        return x, int(cols if ld is None else ld)
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch tensor or an int device pointer")
+    if ld is None and x.dim() == 2 and tuple(x.shape) == (rows, cols) and (x.stride(1) == 1 or cols == 1):
+        return _dev(x, what), int(x.stride(0)) if rows > 1 else cols
+    ld = cols if ld is None else int(ld)
+    need = ((rows - 1) * ld + cols if rows else 0) * x.element_size()
+    _check_tensor(x, what, None, need)
+    return _dev(x, what), ld
+
+
+def pmx_quant_run(cfg: Config, X, Q, scale, rows: int, cols: int, transpose=False, rule="ceil", ldx=None,
+                  x_type=None, stream=None):
+    """MXFP4 codes Q and scale bytes of X [rows][cols] (float32, bfloat16 or
+    float16), blocks of 32 along the columns, or with `transpose` along the
+    rows (the operand of X^T), asynchronous on `stream`.  rule: "ceil" (no value
+    saturates) or "floor" (OCP MX)."""
+    rows, cols = int(rows), int(cols)
+    t = _elem(X, "X", x_type)
+    nb = mxfp4_bytes(cols, rows) if transpose else mxfp4_bytes(rows, cols)
+    x, ld = _matrix(X, "X", rows, cols, ldx)
+    code = _abi.lib().pmx_quant_run(cfg.handle, x, t, rows, cols, ld, int(bool(transpose)),
+                                    SCALE_RULES[rule] if isinstance(rule, str) else int(rule),
+                                    _ptr(Q, "Q", _FP4, nb["Q"]), _ptr(scale, "scale", _SCALE, nb["scale"]),
+                                    _stream(stream, cfg.device))
+    _check("pmx_quant_run", code)
+
+
+def pmx_dequant_run(cfg: Config, Q, scale, Y, rows: int, cols: int, ldy=None, y_type=None, stream=None):
+    """Y [rows][cols] (float32, bfloat16 or float16) = the values of an MXFP4
+    operand (asynchronous on `stream`)."""
+    rows, cols = int(rows), int(cols)
+    t = _elem(Y, "Y", y_type)
+    nb = mxfp4_bytes(rows, cols)
+    y, ld = _matrix(Y, "Y", rows, cols, ldy)
+    code = _abi.lib().pmx_dequant_run(cfg.handle, _ptr(Q, "Q", _FP4, nb["Q"]),
+                                      _ptr(scale, "scale", _SCALE, nb["scale"]), rows, cols, y, t, ld,
+                                      _stream(stream, cfg.device))
+    _check("pmx_dequant_run", code)
+
+
+def prms_run(cfg: Config, X, W, Y, rows: int, cols: int, eps: float = 1e-6, R=None, H=None, out="same",
+             y_scale=None, rstd=None, stream=None):
+    """h = X + R (into H; without R, h = X), Y = h / sqrt(mean(h^2) + eps) * W
+    by rows (asynchronous on `stream`).  out: "same" (Y of X's type), "fp8_b128"
+    (Y e4m3 [rows][Kp], y_scale [Kp/128][rows]: the A operand of a block-scaled
+    fp8 GEMM) or "mxfp4" (Y codes [rows][Kp/2], y_scale [Kp/128][rows][4]), Kp =
+    cols rounded up to 128.  rstd (float32 [rows]) takes the rows' factors for
+    prms_grad_run.  H may be R (or X), Y (out="same") may be X."""
+    rows, cols = int(rows), int(cols)
+    o = RMS_OUTPUTS[out] if isinstance(out, str) else int(out)
+    xt, wt = _elem(X, "X"), _elem(W, "W")
+    x, ldx = _matrix(X, "X", rows, cols)
+    r = h = s = t = None
+    rt, ldr, ldh, ldy = xt, cols, cols, cols
+    if R is not None:
+        rt = _elem(R, "R")
+        r, ldr = _matrix(R, "R", rows, cols)
+    if H is not None:
+        if _elem(H, "H") != rt:
+            raise ValueError("H: must have the type of R")
+        h, ldh = _matrix(H, "H", rows, cols)
+    if o == _abi.PRMS_OUT_SAME:
+        if _elem(Y, "Y") != xt:
+            raise ValueError("Y: must have the type of X")
+        y, ldy = _matrix(Y, "Y", rows, cols)
+    else:
+        kp = -(-cols // 128) * 128
+        if o == _abi.PRMS_OUT_FP8_B128:
+            y = _ptr(Y, "Y", ("uint8", "float8_e4m3fn"), rows * kp)
+            nb = kp // 128 * rows
+        else:
+            y = _ptr(Y, "Y", _FP4, rows * kp // 2)
+            nb = kp // 128 * rows * 4
+        if y_scale is None:
+            raise ValueError("y_scale: a quantised output needs its scales")
+        s = _ptr(y_scale, "y_scale", _SCALE, nb)
+    if rstd is not None:
+        t = _ptr(rstd, "rstd", _F32, rows * 4)
+    code = _abi.lib().prms_run(cfg.handle, x, xt, ldx, r, rt, ldr, _ptr(W, "W", None, cols * (4 if wt == 0 else 2)), wt,
+                               float(eps), rows, cols, h, ldh, o, y, ldy, s, t, _stream(stream, cfg.device))
+    _check("prms_run", code)
+
+
+def prms_grad_run(cfg: Config, dY, H, W, rstd, dX, dW, rows: int, cols: int, dH=None, stream=None):
+    """Gradients of prms_run (asynchronous on `stream`): dX [rows][cols] of H's
+    type (the gradient of X and of R), dW float32 [cols] (None: not wanted).  H:
+    the forward's h; dH: the gradient that reaches h past the norm (None: none)."""
+    rows, cols = int(rows), int(cols)
+    yt, ht, wt = _elem(dY, "dY"), _elem(H, "H"), _elem(W, "W")
+    if _elem(dX, "dX") != ht or (dH is not None and _elem(dH, "dH") != ht):
+        raise ValueError("dX, dH: must have the type of H")
+    dy, ldy = _matrix(dY, "dY", rows, cols)
+    h, ldh = _matrix(H, "H", rows, cols)
+    dx, ldx = _matrix(dX, "dX", rows, cols)
+    dh, ldd = _matrix(dH, "dH", rows, cols) if dH is not None else (None, cols)
+    code = _abi.lib().prms_grad_run(cfg.handle, dy, yt, ldy, h, ht, ldh, dh, ldd,
+                                    _ptr(W, "W", None, cols * (4 if wt == 0 else 2)), wt,
+                                    _ptr(rstd, "rstd", _F32, rows * 4), rows, cols, dx, ldx,
+                                    _ptr(dW, "dW", _F32, cols * 4) if dW is not None else None,
+                                    _stream(stream, cfg.device))
+    _check("prms_grad_run", code)

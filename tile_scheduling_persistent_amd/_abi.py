@@ -13,7 +13,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpgemm.so
 # pgemm_status
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_DEVICE, ERR_OOM, ERR_LAUNCH = range(6)
 # pgemm_dtype
-BF16_OUT_F32, BF16_OUT_BF16, FP8E4M3_B128_OUT_BF16 = range(3)
+BF16_OUT_F32, BF16_OUT_BF16, FP8E4M3_B128_OUT_BF16, MXFP4_OUT_BF16, MXFP4_OUT_F32 = range(5)
 # pgemm_sched
 (SCHED_BLOCKED, SCHED_INTERLEAVED, SCHED_GROUPED, SCHED_WORK_STEALING, SCHED_BLOCKED_GROUPED,
  SCHED_STREAM_K, SCHED_WORK_STEALING_XCC) = range(7)
@@ -24,11 +24,16 @@ DEBUG_VALIDATE_ONLY = 0x20
 # pgemm_args.claim_chunk value for paired claims
 CLAIM_PAIRS = -1
 # pgemm_kernel
-KERNEL_BF16_LDS, KERNEL_BF16_STAGED, KERNEL_FP8, KERNEL_ADD, KERNEL_BF16_PINGPONG = range(5)
+KERNEL_BF16_LDS, KERNEL_BF16_STAGED, KERNEL_FP8, KERNEL_ADD, KERNEL_BF16_PINGPONG, KERNEL_FP4 = range(6)
 KERNEL_NAMES = {KERNEL_BF16_LDS: "bf16_lds", KERNEL_BF16_STAGED: "bf16_staged", KERNEL_FP8: "fp8",
-                KERNEL_ADD: "add", KERNEL_BF16_PINGPONG: "bf16_pingpong"}
+                KERNEL_ADD: "add", KERNEL_BF16_PINGPONG: "bf16_pingpong",
+                KERNEL_FP4: "fp4"}
 # pgemm_args.pipeline
 PIPELINE_DEFAULT, PIPELINE_FOUR_WAVE, PIPELINE_PINGPONG = 0, 1, 2
+# element types, scale rules and norm outputs of the pmx_* and prms_* calls
+PMX_F32, PMX_BF16, PMX_F16 = range(3)
+PMX_SCALE_CEIL, PMX_SCALE_FLOOR = range(2)
+PRMS_OUT_SAME, PRMS_OUT_FP8_B128, PRMS_OUT_MXFP4 = range(3)
 # pgemm_args.program_order
 ORDER_DEFAULT, ORDER_DISPATCH, ORDER_XCD_MAJOR = 0, 1, 2
 
@@ -133,6 +138,17 @@ def lib() -> ctypes.CDLL:
     L.pgemm_run_grouped.argtypes = [_cfg_p, ctypes.POINTER(pgemm_problem), ctypes.c_int, ctypes.c_int,
                                     ctypes.c_int, ctypes.POINTER(pgemm_args), ctypes.c_void_p]
     L.pgemm_run_grouped.restype = st
+    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    L.pmx_quant_run.argtypes = [_cfg_p, vp, i32, i64, i64, i64, i32, i32, vp, vp, vp]
+    L.pmx_quant_run.restype = st
+    L.pmx_dequant_run.argtypes = [_cfg_p, vp, vp, i64, i64, vp, i32, i64, vp]
+    L.pmx_dequant_run.restype = st
+    L.prms_run.argtypes = [_cfg_p, vp, i32, i64, vp, i32, i64, vp, i32, ctypes.c_double, i64, i64, vp, i64,
+                           i32, vp, i64, vp, vp, vp]
+    L.prms_run.restype = st
+    L.prms_grad_run.argtypes = [_cfg_p, vp, i32, i64, vp, i32, i64, vp, i64, vp, i32, vp, i64, i64, vp, i64,
+                                vp, vp]
+    L.prms_grad_run.restype = st
     L.pgemm_witness_enable.argtypes = [_cfg_p, ctypes.c_int64, ctypes.c_int]
     L.pgemm_witness_enable.restype = st
     L.pgemm_witness_read.argtypes = [_cfg_p, ctypes.POINTER(pgemm_witness), ctypes.c_void_p]

@@ -73,6 +73,7 @@ struct GemmParams {
   Witness w;
   int ngemm;          // several GEMMs: entries of gp in use (0: one problem, A..K above)
   GemmProblem gp[kMaxGemmProblems];
+  int out_f32;        // MXFP4: C is fp32 (otherwise bf16)
 };
 
 // Stream-K fix-up: the tiles whose slabs several programs shared are summed
@@ -109,6 +110,53 @@ struct AddParams {
   AddProblem prob[kMaxAddProblems];
 };
 
+// Operands of the block-scaled GEMMs (pmx_quant_run, pmx_dequant_run).
+struct QuantParams {
+  const void* X;   // [rows][cols], row stride ldx
+  int type;
+  int64_t rows, cols, ldx;
+  int transpose, rule;
+  uint8_t* Q;      // [lines][Kp/2], lines = rows (transpose: cols)
+  uint8_t* scale;  // [Kp/128][lines][4]
+};
+
+struct DequantParams {
+  const uint8_t* Q;      // [rows][Kp/2]
+  const uint8_t* scale;  // [Kp/128][rows][4]
+  int64_t rows, cols, ldy;
+  void* Y;
+  int type;
+};
+
+// The norm and its gradient (prms_run, prms_grad_run).
+constexpr int kRmsSame = 0, kRmsFp8 = 1, kRmsFp4 = 2;  // PRMS_OUT_*
+struct RmsParams {
+  const void* X;
+  const void* R;  // null: no residual
+  const void* W;
+  int x_type, r_type, w_type, out;
+  int64_t ldx, ldr, ldh, ldy, rows, cols;
+  double eps;
+  void* H;        // null without a residual
+  void* Y;
+  uint8_t* y_scale;
+  float* rstd;    // may be null
+};
+
+struct RmsGradParams {
+  const void* dY;
+  const void* H;
+  const void* dH;  // may be null
+  const void* W;
+  const float* rstd;
+  int y_type, h_type, w_type;
+  int64_t ldy, ldh, ldd, ldx, rows, cols;
+  void* dX;
+  float* dW;       // may be null
+  float* ws;       // [partials][cols] partial sums of dW
+  int partials;
+};
+
 // Launchers: return hipErrorInvalidValue when no kernel is built for the
 // requested tile shape.
 hipError_t launch_gemm_bf16(const GemmParams& p, int bm, int bn, int bk, bool out_bf16,
@@ -119,6 +167,11 @@ hipError_t launch_padd(const AddParams& p, int tr, int tc, bool vec, bool witnes
                        hipStream_t stream);
 hipError_t launch_padd_multi(const AddParams& p, int tr, int tc, bool vec, bool witness,
                              hipStream_t stream);
+hipError_t launch_quant(const QuantParams& p, hipStream_t stream);
+hipError_t launch_dequant(const DequantParams& p, hipStream_t stream);
+hipError_t launch_rms(const RmsParams& p, hipStream_t stream);
+int rms_grad_partials(int64_t rows);
+hipError_t launch_rms_grad(const RmsGradParams& p, hipStream_t stream);
 hipError_t launch_zero_i32(int* ptr, int n, hipStream_t stream);
 hipError_t launch_fill_i32(int* ptr, int n, int value, hipStream_t stream);
 bool gemm_bf16_tile_supported(int bm, int bn, int bk);
@@ -131,6 +184,11 @@ bool gemm_fp8_tile_supported(int bm, int bn, int bk);
 bool gemm_fp8_eligible(int bm, long long N, long long K);
 bool padd_tile_supported(int tr, int tc);
 int padd_tiles_per_step(int tr, int tc);
+
+bool gemm_fp4_tile_supported(int bm, int bn, int bk);
+bool gemm_fp4_eligible(int bm, int bn, long long M, long long N, long long K);
+void gemm_fp4_default_tile(long long M, long long N, long long K, int cus, int& bm, int& bn, int& bk);
+hipError_t launch_gemm_fp4(const GemmParams& p, int bm, int bn, bool witness, hipStream_t stream);
 
 // Launch shape of a kernel instance: threads and dynamic LDS per workgroup,
 // and how many such workgroups one CU holds at once (registers, LDS, waves).
@@ -154,6 +212,7 @@ KernelInfo info_gemm_bf16_lds(int bm, int bn, bool out_bf16);
 KernelInfo info_gemm_bf16_pp(bool out_bf16);
 hipError_t launch_gemm_bf16_pp(const GemmParams& p, bool out_bf16, bool witness, hipStream_t stream);
 KernelInfo info_gemm_fp8(int bm, int bn);
+KernelInfo info_gemm_fp4(int bm, int bn, bool grouped);
 KernelInfo info_padd(int tr, int tc, bool vec);
 
 // Resident workgroups per CU of `kern` (at least 1), after raising its

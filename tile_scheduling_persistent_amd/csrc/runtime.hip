@@ -119,6 +119,12 @@ size_t span_bytes(int64_t rows, int64_t cols, size_t esz) {
   return b > (unsigned __int128)SIZE_MAX ? SIZE_MAX : (size_t)b;
 }
 
+bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
+  const char* x = (const char*)a;
+  const char* y = (const char*)b;
+  return an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+
 bool validate_only(const pgemm_args* args) {
   return args && (args->debug_flags & PGEMM_DEBUG_VALIDATE_ONLY);
 }
@@ -292,13 +298,51 @@ struct GemmChoice {
   bool vec;  // register-staged kernel: 16-byte vector path
 };
 
-pgemm_status choose_gemm(int64_t M, int64_t N, int64_t K, pgemm_dtype dtype, pgemm_sched sched,
-                         const pgemm_args* args, const void* A, const void* B, const void* C, GemmChoice& ch) {
+bool is_fp4(pgemm_dtype dtype) { return dtype == PGEMM_MXFP4_OUT_BF16 || dtype == PGEMM_MXFP4_OUT_F32; }
+
+// Bytes of an operand of `rows` x K (MXFP4: two codes to a byte), of its
+// scales, and of C.
+size_t operand_bytes(pgemm_dtype dtype, int64_t rows, int64_t K) {
+  if (is_fp4(dtype)) return span_bytes(rows, K / 2, 1);
+  return span_bytes(rows, K, dtype == PGEMM_FP8E4M3_B128_OUT_BF16 ? 1 : 2);
+}
+size_t scale_bytes(pgemm_dtype dtype, int64_t rows, int64_t K) {
+  return span_bytes(K / 128, rows, is_fp4(dtype) ? 4 : 1);
+}
+size_t out_size(pgemm_dtype dtype) {
+  return dtype == PGEMM_BF16_OUT_F32 || dtype == PGEMM_MXFP4_OUT_F32 ? 4 : 2;
+}
+
+// MXFP4 operands as the kernel needs them (null pointers pass).
+bool fp4_aligned(const void* A, const void* B, const void* C, const void* sa, const void* sb, pgemm_dtype dtype) {
+  return aligned(A, 16) && aligned(B, 16) && aligned(C, out_size(dtype)) && aligned(sa, 4) && aligned(sb, 4);
+}
+
+pgemm_status choose_gemm(const pgemm_config* cfg, int64_t M, int64_t N, int64_t K, pgemm_dtype dtype,
+                         pgemm_sched sched, const pgemm_args* args, const void* A, const void* B, const void* C,
+                         GemmChoice& ch) {
   if (M < 1 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
     return PGEMM_ERR_INVALID;
   const bool fp8 = dtype == PGEMM_FP8E4M3_B128_OUT_BF16;
-  if (!fp8 && dtype != PGEMM_BF16_OUT_F32 && dtype != PGEMM_BF16_OUT_BF16)
+  if (!fp8 && !is_fp4(dtype) && dtype != PGEMM_BF16_OUT_F32 && dtype != PGEMM_BF16_OUT_BF16)
     return PGEMM_ERR_INVALID;
+  if (is_fp4(dtype)) {
+    if (K % 128 != 0) return PGEMM_ERR_INVALID;
+    pgk::gemm_fp4_default_tile(M, N, K, cfg->num_cus, ch.bm, ch.bn, ch.bk);
+    if (args && (args->tile_m || args->tile_n || args->tile_k)) {
+      ch.bm = args->tile_m;
+      ch.bn = args->tile_n;
+      ch.bk = args->tile_k;
+    }
+    if (ch.bm < 1 || ch.bn < 1 || ch.bk < 1) return PGEMM_ERR_INVALID;
+    ch.out_bf16 = dtype == PGEMM_MXFP4_OUT_BF16;
+    ch.vec = false;
+    ch.kernel = PGEMM_KERNEL_FP4;
+    if (!pgk::gemm_fp4_tile_supported(ch.bm, ch.bn, ch.bk) || !pgk::gemm_fp4_eligible(ch.bm, ch.bn, M, N, K) ||
+        !fp4_aligned(A, B, C, args ? args->a_scale : nullptr, args ? args->b_scale : nullptr, dtype))
+      return PGEMM_ERR_UNSUPPORTED;
+    return PGEMM_OK;
+  }
   ch.bm = 256;
   ch.bn = 256;
   ch.bk = fp8 ? 128 : 64;
@@ -342,6 +386,7 @@ pgemm_status choose_gemm(int64_t M, int64_t N, int64_t K, pgemm_dtype dtype, pge
 pgk::KernelInfo gemm_info(const GemmChoice& ch) {
   switch (ch.kernel) {
     case PGEMM_KERNEL_FP8: return pgk::info_gemm_fp8(ch.bm, ch.bn);
+    case PGEMM_KERNEL_FP4: return pgk::info_gemm_fp4(ch.bm, ch.bn, false);
     case PGEMM_KERNEL_BF16_LDS: return pgk::info_gemm_bf16_lds(ch.bm, ch.bn, ch.out_bf16);
     case PGEMM_KERNEL_BF16_PINGPONG: return pgk::info_gemm_bf16_pp(ch.out_bf16);
     default: return pgk::info_gemm_bf16(ch.bm, ch.bn, ch.bk, ch.out_bf16, ch.vec);
@@ -605,12 +650,6 @@ pgemm_status pgemm_config_destroy(pgemm_config* cfg) {
   return PGEMM_OK;
 }
 
-static bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
-  const char* x = (const char*)a;
-  const char* y = (const char*)b;
-  return an > 0 && bn > 0 && x < y + bn && y < x + an;
-}
-
 pgemm_status padd_run_multi(pgemm_config* cfg, const padd_problem* problems, int count,
                             int tile_rows, int tile_cols, pgemm_sched sched,
                             const pgemm_args* args, void* hip_stream) {
@@ -688,14 +727,23 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
                                pgemm_dtype dtype, pgemm_sched sched, const pgemm_args* args,
                                void* hip_stream) {
   if (!cfg || !problems || count < 1 || count > PGEMM_MAX_PROBLEMS) return PGEMM_ERR_INVALID;
-  const bool fp8 = dtype == PGEMM_FP8E4M3_B128_OUT_BF16;
-  if (!fp8 && dtype != PGEMM_BF16_OUT_F32 && dtype != PGEMM_BF16_OUT_BF16) return PGEMM_ERR_INVALID;
+  const bool fp8 = dtype == PGEMM_FP8E4M3_B128_OUT_BF16, fp4 = is_fp4(dtype), scaled = fp8 || fp4;
+  if (!scaled && dtype != PGEMM_BF16_OUT_F32 && dtype != PGEMM_BF16_OUT_BF16) return PGEMM_ERR_INVALID;
   if ((int)sched == PGEMM_SCHED_STREAM_K) return PGEMM_ERR_UNSUPPORTED;
   if (args && (args->debug_flags & PGEMM_DEBUG_REGISTER_STAGED)) return PGEMM_ERR_UNSUPPORTED;
   if (args && args->pipeline == PGEMM_PIPELINE_PINGPONG) return PGEMM_ERR_UNSUPPORTED;  // four-wave kernel only
   if (args && (args->pipeline < PGEMM_PIPELINE_DEFAULT || args->pipeline > PGEMM_PIPELINE_PINGPONG))
     return PGEMM_ERR_INVALID;
   int bm = 256, bn = 256, bk = fp8 ? 128 : 64;
+  if (fp4) {  // one tile for all: the default of the largest problem's sizes
+    int64_t M = 1, N = 1, K = 1;
+    for (int g = 0; g < count; ++g) {
+      M = std::max(M, problems[g].M);
+      N = std::max(N, problems[g].N);
+      K = std::max(K, problems[g].K);
+    }
+    pgk::gemm_fp4_default_tile(M, N, K, cfg->num_cus, bm, bn, bk);
+  }
   if (args && (args->tile_m || args->tile_n || args->tile_k)) {
     bm = args->tile_m;
     bn = args->tile_n;
@@ -703,25 +751,32 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
   }
   if (bm < 1 || bn < 1 || bk < 1) return PGEMM_ERR_INVALID;
   const int dev = cfg->device;
-  const size_t csz = dtype == PGEMM_BF16_OUT_F32 ? 4 : 2;
+  const size_t csz = out_size(dtype);
   pgk::GemmParams p;
   memset(&p, 0, sizeof(p));
   p.ngemm = count;
+  p.out_f32 = csz == 4;
   int64_t total = 0;
   for (int g = 0; g < count; ++g) {
     const pgemm_problem& q = problems[g];
     if (!q.A || !q.B || !q.C) return PGEMM_ERR_INVALID;
     if (q.M < 0 || q.N < 0 || q.K < 1 || q.M > 0x7fffffffLL || q.N > 0x7fffffffLL || q.K > 0x7fffffffLL)
       return PGEMM_ERR_INVALID;
-    const size_t qesz = fp8 ? 1 : 2;
-    if (!device_range(q.A, span_bytes(q.M, q.K, qesz), dev) || !device_range(q.B, span_bytes(q.K, q.N, qesz), dev) ||
+    if (!device_range(q.A, operand_bytes(dtype, q.M, q.K), dev) ||
+        !device_range(q.B, operand_bytes(dtype, q.N, q.K), dev) ||
         !device_range(q.C, span_bytes(q.M, q.N, csz), dev))
       return PGEMM_ERR_INVALID;
-    if (fp8) {
-      if (!q.a_scale || !q.b_scale || !device_range(q.a_scale, span_bytes(q.K / 128, q.M, 1), dev) ||
-          !device_range(q.b_scale, span_bytes(q.K / 128, q.N, 1), dev))
+    if (scaled) {
+      if (!q.a_scale || !q.b_scale || !device_range(q.a_scale, scale_bytes(dtype, q.M, q.K), dev) ||
+          !device_range(q.b_scale, scale_bytes(dtype, q.N, q.K), dev))
         return PGEMM_ERR_INVALID;
       if (q.K % 128 != 0) return PGEMM_ERR_INVALID;
+    }
+    if (fp4) {
+      if (!pgk::gemm_fp4_tile_supported(bm, bn, bk) || !pgk::gemm_fp4_eligible(bm, bn, q.M, q.N, q.K) ||
+          !fp4_aligned(q.A, q.B, q.C, q.a_scale, q.b_scale, dtype))
+        return PGEMM_ERR_UNSUPPORTED;
+    } else if (fp8) {
       if (!aligned(q.A, 16) || !aligned(q.B, 16) || !aligned(q.C, 16) ||
           !pgk::gemm_fp8_tile_supported(bm, bn, bk) || !pgk::gemm_fp8_eligible(bm, q.N, q.K))
         return PGEMM_ERR_UNSUPPORTED;
@@ -731,13 +786,13 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
     }
     // each C overlaps no operand and no other output
     const size_t cb = (size_t)q.M * q.N * csz;
-    const size_t esz = fp8 ? 1 : 2;
     for (int h = 0; h < count; ++h) {
       const pgemm_problem& o = problems[h];
-      if (overlaps(q.C, cb, o.A, (size_t)o.M * o.K * esz) || overlaps(q.C, cb, o.B, (size_t)o.K * o.N * esz))
+      if (overlaps(q.C, cb, o.A, operand_bytes(dtype, o.M, o.K)) ||
+          overlaps(q.C, cb, o.B, operand_bytes(dtype, o.N, o.K)))
         return PGEMM_ERR_INVALID;
-      if (fp8 && (overlaps(q.C, cb, o.a_scale, (size_t)(o.K / 128) * o.M) ||
-                  overlaps(q.C, cb, o.b_scale, (size_t)(o.K / 128) * o.N)))
+      if (scaled && (overlaps(q.C, cb, o.a_scale, scale_bytes(dtype, o.M, o.K)) ||
+                     overlaps(q.C, cb, o.b_scale, scale_bytes(dtype, o.N, o.K))))
         return PGEMM_ERR_INVALID;
       if (h != g && overlaps(q.C, cb, o.C, (size_t)o.M * o.N * csz)) return PGEMM_ERR_INVALID;
     }
@@ -746,8 +801,8 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
     a.A = q.A;
     a.B = q.B;
     a.C = q.C;
-    a.sa = fp8 ? q.a_scale : nullptr;
-    a.sb = fp8 ? q.b_scale : nullptr;
+    a.sa = scaled ? q.a_scale : nullptr;
+    a.sb = scaled ? q.b_scale : nullptr;
     a.M = (int)q.M;
     a.N = (int)q.N;
     a.K = (int)q.K;
@@ -769,7 +824,8 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
   DeviceGuard gd(dev);
   if (!gd.ok) return PGEMM_ERR_DEVICE;
   const pgk::KernelInfo ki =
-      fp8 ? pgk::info_gemm_fp8_grouped(bm, bn) : pgk::info_gemm_bf16_lds_grouped(bm, bn, csz == 2);
+      fp4 ? pgk::info_gemm_fp4(bm, bn, true)
+          : fp8 ? pgk::info_gemm_fp8_grouped(bm, bn) : pgk::info_gemm_bf16_lds_grouped(bm, bn, csz == 2);
   if (ki.threads == 0) return PGEMM_ERR_UNSUPPORTED;
   pgemm_status st = make_sched(cfg, sched, args, (int)total, 1, cfg->num_cus * ki.occupancy, true, p.s);
   if (st != PGEMM_OK) return st;
@@ -781,7 +837,8 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
   if (st != PGEMM_OK) return st;
   st = reset_counters(args, p.s, cfg->capacity, &cfg->counters_dirty, witness, stream);
   if (st != PGEMM_OK) return st;
-  hipError_t e = fp8 ? pgk::launch_gemm_fp8_grouped(p, bm, bn, witness, stream)
+  hipError_t e = fp4 ? pgk::launch_gemm_fp4(p, bm, bn, witness, stream)
+                 : fp8 ? pgk::launch_gemm_fp8_grouped(p, bm, bn, witness, stream)
                      : pgk::launch_gemm_bf16_lds_grouped(p, bm, bn, csz == 2, witness, stream);
   if (e == hipErrorInvalidValue) return PGEMM_ERR_UNSUPPORTED;
   return e == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
@@ -877,38 +934,32 @@ pgemm_status gemm_call(pgemm_config* cfg, const void* A, const void* B, void* C,
                        void* hip_stream, CallBuffers buf) {
   if (!A || !B || !C) return PGEMM_ERR_INVALID;
   GemmChoice ch;
-  pgemm_status st = choose_gemm(M, N, K, dtype, sched, args, A, B, C, ch);
+  pgemm_status st = choose_gemm(cfg, M, N, K, dtype, sched, args, A, B, C, ch);
   if (st != PGEMM_OK) return st;
-  const bool fp8 = ch.kernel == PGEMM_KERNEL_FP8;
-  if (fp8 && (!args || !args->a_scale || !args->b_scale)) return PGEMM_ERR_INVALID;
+  const bool fp8 = ch.kernel == PGEMM_KERNEL_FP8, fp4 = is_fp4(dtype), scaled = fp8 || fp4;
+  if (scaled && (!args || !args->a_scale || !args->b_scale)) return PGEMM_ERR_INVALID;
   const int bm = ch.bm, bn = ch.bn;
   const int dev = cfg->device;
-  const size_t esz = fp8 ? 1 : 2;
-  const size_t csz = dtype == PGEMM_BF16_OUT_F32 ? 4 : 2;
-  if (!device_range(A, span_bytes(M, K, esz), dev) || !device_range(B, span_bytes(K, N, esz), dev) ||
-      !device_range(C, span_bytes(M, N, csz), dev))
+  const size_t csz = out_size(dtype);
+  const size_t ab = operand_bytes(dtype, M, K), bb = operand_bytes(dtype, N, K), cb = span_bytes(M, N, csz);
+  if (!device_range(A, ab, dev) || !device_range(B, bb, dev) || !device_range(C, cb, dev)) return PGEMM_ERR_INVALID;
+  if (scaled && (!device_range(args->a_scale, scale_bytes(dtype, M, K), dev) ||
+                 !device_range(args->b_scale, scale_bytes(dtype, N, K), dev)))
     return PGEMM_ERR_INVALID;
-  if (fp8 && (!device_range(args->a_scale, span_bytes(K / 128, M, 1), dev) ||
-              !device_range(args->b_scale, span_bytes(K / 128, N, 1), dev)))
+  // C must not overlap A or B (MXFP4: nor the scales)
+  if (overlaps(C, cb, A, ab) || overlaps(C, cb, B, bb)) return PGEMM_ERR_INVALID;
+  if (fp4 && (overlaps(C, cb, args->a_scale, scale_bytes(dtype, M, K)) ||
+              overlaps(C, cb, args->b_scale, scale_bytes(dtype, N, K))))
     return PGEMM_ERR_INVALID;
-  // C must not overlap A or B
-  {
-    const char* c0 = (const char*)C;
-    const char* c1 = c0 + (size_t)M * N * csz;
-    const char* a0 = (const char*)A;
-    const char* a1 = a0 + (size_t)M * K * esz;
-    const char* b0 = (const char*)B;
-    const char* b1 = b0 + (size_t)K * N * esz;
-    if ((c0 < a1 && a0 < c1) || (c0 < b1 && b0 < c1)) return PGEMM_ERR_INVALID;
-  }
 
   pgk::GemmParams p;
   memset(&p, 0, sizeof(p));
   p.A = A;
   p.B = B;
   p.C = C;
-  p.sa = fp8 ? args->a_scale : nullptr;
-  p.sb = fp8 ? args->b_scale : nullptr;
+  p.sa = scaled ? args->a_scale : nullptr;
+  p.sb = scaled ? args->b_scale : nullptr;
+  p.out_f32 = csz == 4;
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
@@ -949,7 +1000,9 @@ pgemm_status gemm_call(pgemm_config* cfg, const void* A, const void* B, void* C,
   if (st != PGEMM_OK) return st;
 
   hipError_t e;
-  if (fp8)
+  if (fp4)
+    e = pgk::launch_gemm_fp4(p, ch.bm, ch.bn, witness, stream);
+  else if (fp8)
     e = sk ? pgk::launch_gemm_fp8_sk(p, ch.bm, ch.bn, stream)
            : pgk::launch_gemm_fp8(p, ch.bm, ch.bn, ch.bk, true, witness, stream);
   else if (sk)
@@ -1040,7 +1093,7 @@ pgemm_status pgemm_plan_gemm(pgemm_config* cfg, const void* A, const void* B, co
                              const pgemm_args* args, pgemm_plan* out) {
   if (!cfg || !out) return PGEMM_ERR_INVALID;
   GemmChoice ch;
-  pgemm_status st = choose_gemm(M, N, K, dtype, sched, args, A, B, C, ch);
+  pgemm_status st = choose_gemm(cfg, M, N, K, dtype, sched, args, A, B, C, ch);
   if (st != PGEMM_OK) return st;
   const int64_t npm = (M + ch.bm - 1) / ch.bm, npn = (N + ch.bn - 1) / ch.bn;
   if (npm > 0x7fffffffLL || npn > 0x7fffffffLL) return PGEMM_ERR_INVALID;
@@ -1074,6 +1127,160 @@ pgemm_status pgemm_plan_add(pgemm_config* cfg, const float* X, const float* Y, c
   if (st != PGEMM_OK) return st;
   fill_plan(s, ki, tile_rows, tile_cols, 0, PGEMM_KERNEL_ADD, out);
   return PGEMM_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// A strided matrix argument of the pmx_* / prms_* calls.
+constexpr int64_t kMaxDim = 0x7fffffffLL;
+
+size_t type_size(int type) { return type == PMX_F32 ? 4 : 2; }
+bool type_ok(int type) { return type == PMX_F32 || type == PMX_BF16 || type == PMX_F16; }
+
+// Bytes from the first element of a [rows][cols] matrix to its last.
+size_t matrix_bytes(int64_t rows, int64_t cols, int64_t ld, size_t esz) {
+  if (rows <= 0 || cols <= 0) return 0;
+  const unsigned __int128 b = ((unsigned __int128)(rows - 1) * (unsigned __int128)ld + (unsigned __int128)cols) * esz;
+  return b > (unsigned __int128)SIZE_MAX ? SIZE_MAX : (size_t)b;
+}
+
+// A buffer of `bytes` that starts on its elements' alignment and lies in one
+// allocation; an empty one is not looked at.
+bool buffer_ok(const void* p, size_t bytes, size_t align, int dev) {
+  return bytes == 0 || (p != nullptr && aligned(p, align) && device_range(p, bytes, dev));
+}
+
+int64_t padded(int64_t n) { return (n + 127) / 128 * 128; }
+
+}  // namespace
+
+extern "C" {
+
+pgemm_status pmx_quant_run(pgemm_config* cfg, const void* X, int x_type, int64_t rows, int64_t cols, int64_t ldx,
+                           int transpose, int rule, uint8_t* Q, uint8_t* scale, void* hip_stream) {
+  if (!cfg || !type_ok(x_type) || rows < 0 || cols < 1 || rows > kMaxDim || cols > kMaxDim || ldx < cols ||
+      (transpose != 0 && transpose != 1) || (rule != PMX_SCALE_CEIL && rule != PMX_SCALE_FLOOR))
+    return PGEMM_ERR_INVALID;
+  if (rows == 0) return PGEMM_OK;
+  const int64_t lines = transpose ? cols : rows, len = transpose ? rows : cols;
+  const size_t xb = matrix_bytes(rows, cols, ldx, type_size(x_type));
+  const size_t qb = span_bytes(lines, padded(len) / 2, 1), sb = span_bytes(padded(len) / 128, lines, 4);
+  const int dev = cfg->device;
+  if (!buffer_ok(X, xb, type_size(x_type), dev) || !buffer_ok(Q, qb, 1, dev) || !buffer_ok(scale, sb, 1, dev))
+    return PGEMM_ERR_INVALID;
+  if (overlaps(Q, qb, X, xb) || overlaps(scale, sb, X, xb) || overlaps(Q, qb, scale, sb)) return PGEMM_ERR_INVALID;
+  if (!aligned(Q, 4) || !aligned(scale, 4)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(dev);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::QuantParams p = {X, x_type, rows, cols, ldx, transpose, rule, Q, scale};
+  return pgk::launch_quant(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
+}
+
+pgemm_status pmx_dequant_run(pgemm_config* cfg, const uint8_t* Q, const uint8_t* scale, int64_t rows, int64_t cols,
+                             void* Y, int y_type, int64_t ldy, void* hip_stream) {
+  if (!cfg || !type_ok(y_type) || rows < 0 || cols < 1 || rows > kMaxDim || cols > kMaxDim || ldy < cols)
+    return PGEMM_ERR_INVALID;
+  if (rows == 0) return PGEMM_OK;
+  const size_t yb = matrix_bytes(rows, cols, ldy, type_size(y_type));
+  const size_t qb = span_bytes(rows, padded(cols) / 2, 1), sb = span_bytes(padded(cols) / 128, rows, 4);
+  const int dev = cfg->device;
+  if (!buffer_ok(Y, yb, type_size(y_type), dev) || !buffer_ok(Q, qb, 1, dev) || !buffer_ok(scale, sb, 1, dev))
+    return PGEMM_ERR_INVALID;
+  if (overlaps(Y, yb, Q, qb) || overlaps(Y, yb, scale, sb)) return PGEMM_ERR_INVALID;
+  if (!aligned(Q, 4) || !aligned(scale, 4)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(dev);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::DequantParams p = {Q, scale, rows, cols, ldy, Y, y_type};
+  return pgk::launch_dequant(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
+}
+
+pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx, const void* R, int r_type,
+                      int64_t ldr, const void* W, int w_type, double eps, int64_t rows, int64_t cols, void* H,
+                      int64_t ldh, int out, void* Y, int64_t ldy, uint8_t* y_scale, float* rstd,
+                      void* hip_stream) {
+  if (!cfg || !type_ok(x_type) || !type_ok(w_type) || rows < 0 || cols < 1 || rows > kMaxDim || cols > kMaxDim ||
+      ldx < cols || !(eps >= 0.0))
+    return PGEMM_ERR_INVALID;
+  if (out != PRMS_OUT_SAME && out != PRMS_OUT_FP8_B128 && out != PRMS_OUT_MXFP4) return PGEMM_ERR_INVALID;
+  const bool quant = out != PRMS_OUT_SAME;
+  if (!quant && ldy < cols) return PGEMM_ERR_INVALID;
+  if (rows > 0 && (R == nullptr) != (H == nullptr)) return PGEMM_ERR_INVALID;
+  if (R && (!type_ok(r_type) || ldr < cols || ldh < cols)) return PGEMM_ERR_INVALID;
+  if (!R) r_type = x_type;
+  if ((r_type != x_type && r_type != PMX_F32) || (w_type != x_type && w_type != PMX_F32)) return PGEMM_ERR_UNSUPPORTED;
+  if (rows == 0) return PGEMM_OK;
+  const int dev = cfg->device;
+  const size_t xs = type_size(x_type), rs = type_size(r_type), ws = type_size(w_type);
+  const int64_t kp = padded(cols);
+  const size_t xb = matrix_bytes(rows, cols, ldx, xs), wb = (size_t)cols * ws;
+  const size_t rb = R ? matrix_bytes(rows, cols, ldr, rs) : 0, hb = R ? matrix_bytes(rows, cols, ldh, rs) : 0;
+  const size_t yb = quant ? span_bytes(rows, out == PRMS_OUT_FP8_B128 ? kp : kp / 2, 1)
+                          : matrix_bytes(rows, cols, ldy, xs);
+  const size_t sb = quant ? span_bytes(kp / 128, rows, out == PRMS_OUT_FP8_B128 ? 1 : 4) : 0;
+  const size_t tb = rstd ? span_bytes(rows, 4, 1) : 0;
+  if (!buffer_ok(X, xb, xs, dev) || !buffer_ok(R, rb, rs, dev) || !buffer_ok(W, wb, ws, dev) ||
+      !buffer_ok(H, hb, rs, dev) || !buffer_ok(Y, yb, quant ? 1 : xs, dev) || !buffer_ok(y_scale, sb, 1, dev) ||
+      !buffer_ok(rstd, tb, 4, dev))
+    return PGEMM_ERR_INVALID;
+  // every output against every input and every other output; in place: H on R
+  // or X, Y on X
+  const bool h_on_r = H == R && ldh == ldr, h_on_x = H == X && ldh == ldx && r_type == x_type;
+  const bool y_on_x = !quant && Y == X && ldy == ldx;
+  if ((!h_on_r && overlaps(H, hb, R, rb)) || (!h_on_x && overlaps(H, hb, X, xb)) || overlaps(H, hb, W, wb) ||
+      (!y_on_x && overlaps(Y, yb, X, xb)) || overlaps(Y, yb, R, rb) || overlaps(Y, yb, W, wb) ||
+      overlaps(Y, yb, H, hb))
+    return PGEMM_ERR_INVALID;
+  const void* small[2] = {y_scale, rstd};
+  const size_t small_b[2] = {sb, tb};
+  for (int i = 0; i < 2; ++i)
+    if (overlaps(small[i], small_b[i], X, xb) || overlaps(small[i], small_b[i], R, rb) ||
+        overlaps(small[i], small_b[i], W, wb) || overlaps(small[i], small_b[i], H, hb) ||
+        overlaps(small[i], small_b[i], Y, yb))
+      return PGEMM_ERR_INVALID;
+  if (overlaps(y_scale, sb, rstd, tb)) return PGEMM_ERR_INVALID;
+  if (quant && (!aligned(Y, out == PRMS_OUT_FP8_B128 ? 8 : 4) || !aligned(y_scale, 4))) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(dev);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::RmsParams p = {X,   R,   W,   x_type, r_type, w_type, out, ldx, ldr, ldh,
+                            ldy, rows, cols, eps,   H,      Y,      y_scale, rstd};
+  return pgk::launch_rms(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
+}
+
+pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_t ldy, const void* H, int h_type,
+                           int64_t ldh, const void* dH, int64_t ldd, const void* W, int w_type, const float* rstd,
+                           int64_t rows, int64_t cols, void* dX, int64_t ldx, float* dW, void* hip_stream) {
+  if (!cfg || !type_ok(y_type) || !type_ok(h_type) || !type_ok(w_type) || rows < 0 || cols < 1 || rows > kMaxDim ||
+      cols > kMaxDim || ldy < cols || ldh < cols || ldx < cols || (dH && ldd < cols))
+    return PGEMM_ERR_INVALID;
+  if ((h_type != y_type && h_type != PMX_F32) || (w_type != y_type && w_type != PMX_F32)) return PGEMM_ERR_UNSUPPORTED;
+  const int dev = cfg->device;
+  const size_t ys = type_size(y_type), hs = type_size(h_type), ws = type_size(w_type);
+  const size_t yb = matrix_bytes(rows, cols, ldy, ys), hb = matrix_bytes(rows, cols, ldh, hs);
+  const size_t db = dH ? matrix_bytes(rows, cols, ldd, hs) : 0, xb = matrix_bytes(rows, cols, ldx, hs);
+  const size_t wb = (size_t)cols * ws, tb = span_bytes(rows, 4, 1), gb = dW ? (size_t)cols * 4 : 0;
+  if (!buffer_ok(dY, yb, ys, dev) || !buffer_ok(H, hb, hs, dev) || !buffer_ok(dH, db, hs, dev) ||
+      !buffer_ok(W, wb, ws, dev) || !buffer_ok(rstd, tb, 4, dev) || !buffer_ok(dX, xb, hs, dev) ||
+      !buffer_ok(dW, gb, 4, dev))
+    return PGEMM_ERR_INVALID;
+  const bool on_dy = dX == dY && ldx == ldy && y_type == h_type, on_dh = dX == dH && ldx == ldd;
+  if ((!on_dy && overlaps(dX, xb, dY, yb)) || (!on_dh && overlaps(dX, xb, dH, db)) || overlaps(dX, xb, H, hb) ||
+      overlaps(dX, xb, W, wb) || overlaps(dX, xb, rstd, tb) || overlaps(dX, xb, dW, gb) || overlaps(dW, gb, dY, yb) ||
+      overlaps(dW, gb, H, hb) || overlaps(dW, gb, dH, db) || overlaps(dW, gb, W, wb) || overlaps(dW, gb, rstd, tb))
+    return PGEMM_ERR_INVALID;
+  int partials = 0;
+  if (dW) {
+    partials = pgk::rms_grad_partials(rows);
+    const int64_t fit = (int64_t)(cfg->ws_bytes / ((size_t)cols * sizeof(float)));
+    if (fit < 1) return PGEMM_ERR_UNSUPPORTED;
+    if (partials > fit) partials = (int)fit;
+  }
+  DeviceGuard g(dev);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::RmsGradParams p = {dY,  H,   dH,  W,    rstd, y_type, h_type, w_type,  ldy,
+                                ldh, ldd, ldx, rows, cols, dX,     dW,     cfg->ws, partials};
+  return pgk::launch_rms_grad(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
 }
 
 }  // extern "C"
