@@ -118,6 +118,7 @@ struct QuantParams {
   int transpose, rule;
   uint8_t* Q;      // [lines][Kp/2], lines = rows (transpose: cols)
   uint8_t* scale;  // [Kp/128][lines][4]
+  int cus;         // compute units of the device
 };
 
 struct DequantParams {
@@ -126,6 +127,7 @@ struct DequantParams {
   int64_t rows, cols, ldy;
   void* Y;
   int type;
+  int cus;
 };
 
 // The norm and its gradient (prms_run, prms_grad_run).
@@ -141,6 +143,7 @@ struct RmsParams {
   void* Y;
   uint8_t* y_scale;
   float* rstd;    // may be null
+  int cus, xcds;  // compute units and XCDs of the device
 };
 
 struct RmsGradParams {
@@ -154,7 +157,8 @@ struct RmsGradParams {
   void* dX;
   float* dW;       // may be null
   float* ws;       // [partials][cols] partial sums of dW
-  int partials;
+  int partials;    // rows of ws
+  int cus;
 };
 
 // Launchers: return hipErrorInvalidValue when no kernel is built for the
@@ -170,7 +174,7 @@ hipError_t launch_padd_multi(const AddParams& p, int tr, int tc, bool vec, bool 
 hipError_t launch_quant(const QuantParams& p, hipStream_t stream);
 hipError_t launch_dequant(const DequantParams& p, hipStream_t stream);
 hipError_t launch_rms(const RmsParams& p, hipStream_t stream);
-int rms_grad_partials(int64_t rows);
+int rms_grad_partials(int64_t rows, int64_t cols, int cus);
 hipError_t launch_rms_grad(const RmsGradParams& p, hipStream_t stream);
 hipError_t launch_zero_i32(int* ptr, int n, hipStream_t stream);
 hipError_t launch_fill_i32(int* ptr, int n, int value, hipStream_t stream);

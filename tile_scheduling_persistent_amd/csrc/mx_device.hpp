@@ -106,53 +106,74 @@ __device__ __forceinline__ Vec8<T> vec8_pack(const float (&x)[8]) {
   return v;
 }
 
+// 16 bytes at an address aligned to `A` bytes: global memory accesses of any
+// alignment are single instructions here, so rows that start on odd elements
+// move as wide as aligned ones.
+template <int A>
+struct Quad;
+template <>
+struct Quad<4> {
+  typedef u32x4_d __attribute__((aligned(4))) type;
+};
+template <>
+struct Quad<2> {
+  typedef u32x4_d __attribute__((aligned(2))) type;
+};
+
 // Elements i .. i + 7 of a row that ends at `n` (elements past it zero).
-// WIDE: the row starts on a 16-byte address and n is a multiple of 8.
-template <int T, bool WIDE>
+template <int T>
 __device__ __forceinline__ Vec8<T> vec8_load(const void* row, int64_t i, int64_t n) {
   constexpr int esz = T == kTypeF32 ? 4 : 2;
   Vec8<T> v;
-  if (WIDE) {
-    const u32x4_d* p = reinterpret_cast<const u32x4_d*>(static_cast<const char*>(row) + i * esz);
 #pragma unroll
-    for (int q = 0; q < esz / 2; ++q) v.q[q] = i < n ? p[q] : u32x4_d{0, 0, 0, 0};
-    return v;
-  }
-  if (T == kTypeF32) {
+  for (int q = 0; q < esz / 2; ++q) v.q[q] = u32x4_d{0, 0, 0, 0};
+  if (i + 8 <= n) {
+    const auto* p = reinterpret_cast<const typename Quad<esz>::type*>(static_cast<const char*>(row) + i * esz);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v.q[e >> 2][e & 3] = i + e < n ? static_cast<const unsigned*>(row)[i + e] : 0u;
-  } else {
-    const unsigned short* p = static_cast<const unsigned short*>(row);
+    for (int q = 0; q < esz / 2; ++q) v.q[q] = p[q];
+  } else if (i < n) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const unsigned lo = i + 2 * e < n ? p[i + 2 * e] : 0u, hi = i + 2 * e + 1 < n ? p[i + 2 * e + 1] : 0u;
-      v.q[0][e] = lo | (hi << 16);
+    for (int e = 0; e < 7; ++e) {
+      if (i + e >= n) continue;
+      if (T == kTypeF32)
+        v.q[e >> 2][e & 3] = static_cast<const unsigned*>(row)[i + e];
+      else
+        v.q[0][e >> 1] |= (unsigned)static_cast<const unsigned short*>(row)[i + e] << (16 * (e & 1));
     }
   }
   return v;
 }
 
-template <int T, bool WIDE>
+template <int T>
 __device__ __forceinline__ void vec8_store(void* row, int64_t i, int64_t n, const Vec8<T>& v) {
   constexpr int esz = T == kTypeF32 ? 4 : 2;
-  if (WIDE) {
-    u32x4_d* p = reinterpret_cast<u32x4_d*>(static_cast<char*>(row) + i * esz);
-    if (i < n) {
+  if (i + 8 <= n) {
+    auto* p = reinterpret_cast<typename Quad<esz>::type*>(static_cast<char*>(row) + i * esz);
 #pragma unroll
-      for (int q = 0; q < esz / 2; ++q) p[q] = v.q[q];
+    for (int q = 0; q < esz / 2; ++q) p[q] = v.q[q];
+  } else if (i < n) {
+#pragma unroll
+    for (int e = 0; e < 7; ++e) {
+      if (i + e >= n) continue;
+      if (T == kTypeF32)
+        static_cast<unsigned*>(row)[i + e] = v.q[e >> 2][e & 3];
+      else
+        static_cast<unsigned short*>(row)[i + e] = (unsigned short)(v.q[0][e >> 1] >> (16 * (e & 1)));
     }
-    return;
   }
-  if (T == kTypeF32) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (i + e < n) static_cast<unsigned*>(row)[i + e] = v.q[e >> 2][e & 3];
-  } else {
-    unsigned short* p = static_cast<unsigned short*>(row);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (i + e < n) p[i + e] = (unsigned short)(v.q[0][e >> 1] >> (16 * (e & 1)));
-  }
+}
+
+// Largest over the 4 lanes of a quad, and over the 16 lanes of a row, in
+// every lane of it (data-parallel primitives: no LDS).
+__device__ __forceinline__ unsigned max_u32(unsigned a, unsigned b) { return a > b ? a : b; }
+__device__ __forceinline__ unsigned quad_max(unsigned m) {
+  m = max_u32(m, (unsigned)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));     // lanes 1 0 3 2
+  return max_u32(m, (unsigned)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));  // lanes 2 3 0 1
+}
+__device__ __forceinline__ unsigned row16_max(unsigned m) {
+  m = quad_max(m);
+  m = max_u32(m, (unsigned)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xf, 0xf, true));    // rotated by 4
+  return max_u32(m, (unsigned)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xf, 0xf, true)); // rotated by 8
 }
 
 // Largest magnitude of the eight, as fp32 bits.

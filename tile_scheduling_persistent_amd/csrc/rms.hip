@@ -1,176 +1,246 @@
 // Root-mean-square norm of rows with the residual's addition before it and
-// the quantisation of the next product's operand after it, and its gradient.
+// the quantisation of the next product's operand after it.
+//
+// One pass over the data: a row's h = x + r stays in registers between the sum
+// of squares and the output, and its blocks' scale exponents are found there
+// too.  Bound by memory; the arithmetic is in 64 bits (which gfx950 runs at
+// the rate of unpacked 32-bit operations), because the quantised outputs round
+// at borders: y in fp32 would now and then be on the other side of one, and a
+// scale byte off by one is a factor of two.
 #include "common.hpp"
-#include "mx_device.hpp"
+#include "rms_device.hpp"
 
 namespace pgk {
 namespace {
 
-constexpr int kThreads = 256;
-
-// y = h * rstd * w in 64 bits, as fp32 with the bits below the 20th of the
-// fraction folded into the last one (round to odd): whatever few bits the
-// result is rounded to next, it is rounded as from the 64-bit value.
+// y in 64 bits, as fp32 with the bits below the 20th of the fraction folded
+// into the last one (round to odd): whatever few bits the result is rounded to
+// next, it is rounded as from the 64-bit value.
 __device__ __forceinline__ float narrow_odd(double y) {
   const unsigned long long b = __builtin_bit_cast(unsigned long long, y);
   const unsigned lo = (unsigned)b, hi = (unsigned)(b >> 32);
   return (float)__builtin_bit_cast(double, (unsigned long long)(hi | (lo != 0u ? 1u : 0u)) << 32);
 }
 
-__device__ __forceinline__ float load_any(const void* p, int64_t i, int type) {
-  if (type == kTypeF32) return load_elem<kTypeF32>(p, i);
-  if (type == kTypeBF16) return load_elem<kTypeBF16>(p, i);
-  return load_elem<kTypeF16>(p, i);
-}
-__device__ __forceinline__ void store_any(void* p, int64_t i, int type, float v) {
-  if (type == kTypeF32)
-    store_elem<kTypeF32>(p, i, v);
-  else if (type == kTypeBF16)
-    store_elem<kTypeBF16>(p, i, v);
-  else
-    store_elem<kTypeF16>(p, i, v);
+// The row group of workgroup i: ranges of `chunk` consecutive ones go to the
+// workgroups of one XCD (which take every X-th index), because the scale bytes
+// of consecutive rows share lines of memory, which that XCD's L2 then writes
+// whole.
+__device__ __forceinline__ int64_t group_of(int64_t i, int64_t n, int X, int chunk) {
+  const int64_t per = (int64_t)X * chunk;
+  if (i >= n / per * per) return i;
+  const int64_t j = i / X, x = i - j * X;
+  return j / chunk * per + x * chunk + j % chunk;
 }
 
-// x rounded to the element type, as fp32.
-__device__ __forceinline__ float round_any(float x, int type) {
-  if (type == kTypeBF16) return (float)(__bf16)x;
-  if (type == kTypeF16) return (float)(_Float16)x;
-  return x;
+template <int WT>
+__device__ __forceinline__ void weights(const RmsParams& p, int64_t c, float (&w)[8]) {
+  vec8_f32<WT>(vec8_load<WT>(p.W, c, p.cols), w);
 }
 
-template <class T>
-__device__ __forceinline__ T block_sum(T v, T* s) {
-  const int t = threadIdx.x;
-  s[t] = v;
-  __syncthreads();
-  for (int n = kThreads / 2; n > 0; n >>= 1) {
-    if (t < n) s[t] += s[t + n];
-    __syncthreads();
+// h = x + r as it is stored (RT: its type), written to H where there is a
+// residual.
+template <int XT, int RT, bool RES>
+__device__ __forceinline__ void h_of(const RmsParams& p, int64_t row, int64_t c, const Vec8<XT>& x, const Vec8<RT>& r,
+                                     float (&h)[8]) {
+  vec8_f32<XT>(x, h);
+  if (RES) {
+    float a[8];
+    vec8_f32<RT>(r, a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] += h[e];
+    const Vec8<RT> s = vec8_pack<RT>(a);
+    vec8_store<RT>(static_cast<char*>(p.H) + row * p.ldh * (RT == kTypeF32 ? 4 : 2), c, p.cols, s);
+    vec8_f32<RT>(s, h);
   }
-  const T r = s[0];
-  __syncthreads();
-  return r;
 }
 
-// One workgroup per row.
-__global__ void __launch_bounds__(kThreads) rms_kernel(RmsParams p) {
-  __shared__ double red[kThreads];
-  const int64_t row = blockIdx.x;
-  const int64_t groups = (p.cols + 127) / 128;
-  auto h_at = [&](int64_t c) {
-    const float x = load_any(p.X, row * p.ldx + c, p.x_type);
-    return p.R ? round_any(x + load_any(p.R, row * p.ldr + c, p.r_type), p.r_type) : x;
-  };
-  double s = 0.0;
-  for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
-    const double h = h_at(c);
-    s += h * h;
+// Eight columns of the output.  Called by whole rows of 16 lanes.
+template <int XT, int OUT>
+__device__ __forceinline__ void put(const RmsParams& p, int64_t row, int64_t c, int64_t kp, const float (&h)[8],
+                                    const float (&w)[8], double rstd) {
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double v = (double)h[e] * (double)w[e] * rstd;
+    y[e] = OUT == kRmsSame && XT == kTypeF32 ? (float)v : narrow_odd(v);
   }
-  const double rstd = 1.0 / sqrt(block_sum(s, red) / (double)p.cols + p.eps);
-  if (threadIdx.x == 0 && p.rstd) p.rstd[row] = (float)rstd;
-  auto y_at = [&](int64_t c, float h) { return (double)h * rstd * (double)load_any(p.W, c, p.w_type); };
-  if (p.out == kRmsSame) {
-    for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
-      const float h = h_at(c);
-      const double y = y_at(c, h);
-      if (p.H) store_any(p.H, row * p.ldh + c, p.r_type, h);
-      store_any(p.Y, row * p.ldy + c, p.x_type, p.x_type == kTypeF32 ? (float)y : narrow_odd(y));
-    }
+  if (OUT == kRmsSame) {
+    vec8_store<XT>(static_cast<char*>(p.Y) + row * p.ldy * (XT == kTypeF32 ? 4 : 2), c, p.cols, vec8_pack<XT>(y));
     return;
   }
-  const int64_t nblk = p.out == kRmsFp8 ? groups : groups * 4;
-  const int len = p.out == kRmsFp8 ? 128 : 32;
-  for (int64_t b = threadIdx.x; b < nblk; b += kThreads) {
-    unsigned amax = 0;
-    for (int e = 0; e < len; ++e) {
-      const int64_t c = b * len + e;
-      if (c >= p.cols) break;
-      const unsigned v = __builtin_bit_cast(unsigned, narrow_odd(y_at(c, h_at(c)))) & 0x7fffffffu;
-      amax = v > amax ? v : amax;
-    }
-    const unsigned byte = p.out == kRmsFp8 ? scale_byte<E4M3>(amax, kRuleCeil) : scale_byte<E2M1>(amax, kRuleCeil);
+  if (c + 8 > p.cols) {  // the padding is zero whatever rstd is
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e >= p.cols) y[e] = 0.0f;
+  }
+  const Vec8<kTypeF32> v = vec8_pack<kTypeF32>(y);
+  const int lane16 = threadIdx.x & 15;
+  uint8_t* q = static_cast<uint8_t*>(p.Y);
+  if (OUT == kRmsFp8) {
+    const unsigned byte = scale_byte<E4M3>(row16_max(vec8_amax(v)), kRuleCeil);
     const float sc = scale_value(byte);
-    for (int e = 0; e < len; e += 8) {
-      float y[8];
-      for (int i = 0; i < 8; ++i) {
-        const int64_t c = b * len + e + i;
-        const float h = c < p.cols ? h_at(c) : 0.0f;
-        y[i] = c < p.cols && byte != 255u ? narrow_odd(y_at(c, h)) : 0.0f;
-        if (p.H && c < p.cols) store_any(p.H, row * p.ldh + c, p.r_type, h);
-      }
-      if (p.out == kRmsFp8) {
-        unsigned* q = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(p.Y) + row * groups * 128 + b * 128 + e);
-        for (int i = 0; i < 2; ++i) {
-          s16x2_d o = {0, 0};
-          o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, y[4 * i], y[4 * i + 1], sc, false);
-          o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, y[4 * i + 2], y[4 * i + 3], sc, true);
-          q[i] = byte == 255u ? 0u : __builtin_bit_cast(unsigned, o);
-        }
-      } else {
-        const unsigned o = vec8_e2m1(vec8_pack<kTypeF32>(y), sc);
-        *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(p.Y) + row * groups * 64 + b * 16 + e / 2) =
-            byte == 255u ? 0u : o;
-      }
+    u32x2_d o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s16x2_d t = {0, 0};
+      t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, y[4 * i], y[4 * i + 1], sc, false);
+      t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, y[4 * i + 2], y[4 * i + 3], sc, true);
+      o[i] = byte == 255u ? 0u : __builtin_bit_cast(unsigned, t);
     }
-    if (p.out == kRmsFp8)
-      p.y_scale[b * p.rows + row] = (uint8_t)byte;
-    else
-      p.y_scale[((b >> 2) * p.rows + row) * 4 + (b & 3)] = (uint8_t)byte;
+    *reinterpret_cast<u32x2_d*>(q + row * kp + c) = o;
+    if (lane16 == 0) p.y_scale[(c >> 7) * p.rows + row] = (uint8_t)byte;
+  } else {
+    const unsigned byte = scale_byte<E2M1>(quad_max(vec8_amax(v)), kRuleCeil);
+    const unsigned o = vec8_e2m1(v, scale_value(byte));
+    *reinterpret_cast<unsigned*>(q + row * (kp >> 1) + (c >> 1)) = byte == 255u ? 0u : o;
+    // the bytes of the row's four blocks of 32 as one word
+    unsigned word = byte << (8 * (lane16 >> 2));
+    word |= (unsigned)__builtin_amdgcn_update_dpp(0, (int)word, 0x124, 0xf, 0xf, true);
+    word |= (unsigned)__builtin_amdgcn_update_dpp(0, (int)word, 0x128, 0xf, 0xf, true);
+    if (lane16 == 0) reinterpret_cast<unsigned*>(p.y_scale)[(c >> 7) * p.rows + row] = word;
   }
 }
 
-// One workgroup per row: dx.
-__global__ void __launch_bounds__(kThreads) rms_dx_kernel(RmsGradParams p) {
-  __shared__ float red[kThreads];
-  const int64_t row = blockIdx.x;
-  const float r = p.rstd[row];
-  float s = 0.0f;
-  for (int64_t c = threadIdx.x; c < p.cols; c += kThreads)
-    s += load_any(p.dY, row * p.ldy + c, p.y_type) * load_any(p.W, c, p.w_type) * load_any(p.H, row * p.ldh + c, p.h_type);
-  const float k = r * r * r * (block_sum(s, red) / (float)p.cols);
-  for (int64_t c = threadIdx.x; c < p.cols; c += kThreads) {
-    const float g = load_any(p.dY, row * p.ldy + c, p.y_type) * load_any(p.W, c, p.w_type);
-    float v = r * g - load_any(p.H, row * p.ldh + c, p.h_type) * k;
-    if (p.dH) v += load_any(p.dH, row * p.ldd + c, p.h_type);
-    store_any(p.dX, row * p.ldx + c, p.h_type, v);
+// Rows held in registers: VPT vectors per thread.
+template <int XT, int RT, bool RES, int OUT, int VPT>
+__global__ void __launch_bounds__(kRmsMaxLanes) rms_kernel(RmsParams p, int L, int chunk) {
+  __shared__ double s_sum[2][16];
+  const int t = threadIdx.x & (L - 1), sub = threadIdx.x / L, per = blockDim.x / L;  // L <= 64: a power of two
+  const int t0 = L > 64 ? (int)threadIdx.x : t;
+  const int64_t kp = (p.cols + 127) / 128 * 128, n = (p.rows + per - 1) / per;
+  constexpr int xsz = XT == kTypeF32 ? 4 : 2, rsz = RT == kTypeF32 ? 4 : 2;
+  int turn = 0;
+  for (int64_t i = blockIdx.x; i < n; i += gridDim.x, turn ^= 1) {
+    const int64_t row = group_of(i, n, p.xcds, chunk) * per + (L > 64 ? 0 : sub);
+    const bool on = row < p.rows;
+    const int64_t at = on ? row : p.rows - 1;
+    Vec8<XT> x[VPT];
+    Vec8<RT> r[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int64_t c = ((int64_t)v * L + t0) * 8;
+      x[v] = vec8_load<XT>(static_cast<const char*>(p.X) + at * p.ldx * xsz, c, p.cols);
+      if (RES) r[v] = vec8_load<RT>(static_cast<const char*>(p.R) + at * p.ldr * rsz, c, p.cols);
+    }
+    float h[VPT][8];
+    double s = 0.0;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int64_t c = ((int64_t)v * L + t0) * 8;
+      h_of<XT, RT, RES>(p, at, on ? c : p.cols, x[v], r[v], h[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (double)h[v][e] * (double)h[v][e];
+    }
+    s = row_sum(s, L, s_sum, turn);
+    const double rstd = 1.0 / sqrt(s / (double)p.cols + p.eps);
+    if (!on) continue;
+    if (t0 == 0 && p.rstd) p.rstd[row] = (float)rstd;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int64_t c = ((int64_t)v * L + t0) * 8;
+      if (c >= kp) continue;
+      float w[8];
+      if (p.w_type == kTypeF32)
+        weights<kTypeF32>(p, c, w);
+      else
+        weights<XT>(p, c, w);
+      put<XT, OUT>(p, row, c, kp, h[v], w, rstd);
+    }
   }
 }
 
-// Partial sums of dw: program q adds the rows q, q + P, ...
-__global__ void __launch_bounds__(kThreads) rms_dw_kernel(RmsGradParams p) {
-  const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (c >= p.cols) return;
-  float s = 0.0f;
-  for (int64_t row = blockIdx.y; row < p.rows; row += p.partials)
-    s += load_any(p.dY, row * p.ldy + c, p.y_type) * (load_any(p.H, row * p.ldh + c, p.h_type) * p.rstd[row]);
-  p.ws[(int64_t)blockIdx.y * p.cols + c] = s;
+// Rows too long for that: a workgroup walks the row twice, the second time
+// from h as stored.
+template <int XT, int RT, bool RES, int OUT>
+__global__ void __launch_bounds__(kRmsMaxLanes) rms_long_kernel(RmsParams p) {
+  __shared__ double s_sum[2][16];
+  const int64_t kp = (p.cols + 127) / 128 * 128;
+  constexpr int xsz = XT == kTypeF32 ? 4 : 2, rsz = RT == kTypeF32 ? 4 : 2;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const char* xr = static_cast<const char*>(p.X) + row * p.ldx * xsz;
+    double s = 0.0;
+    for (int64_t c = threadIdx.x * 8; c < p.cols; c += kRmsMaxLanes * 8) {
+      Vec8<RT> r;
+      if (RES) r = vec8_load<RT>(static_cast<const char*>(p.R) + row * p.ldr * rsz, c, p.cols);
+      float h[8];
+      h_of<XT, RT, RES>(p, row, c, vec8_load<XT>(xr, c, p.cols), r, h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (double)h[e] * (double)h[e];
+    }
+    s = row_sum(s, kRmsMaxLanes, s_sum, turn);
+    const double rstd = 1.0 / sqrt(s / (double)p.cols + p.eps);
+    if (threadIdx.x == 0 && p.rstd) p.rstd[row] = (float)rstd;
+    for (int64_t c = threadIdx.x * 8; c < kp; c += kRmsMaxLanes * 8) {
+      float h[8], w[8];
+      if (RES)  // this thread's own stores
+        vec8_f32<RT>(vec8_load<RT>(static_cast<const char*>(p.H) + row * p.ldh * rsz, c, p.cols), h);
+      else
+        vec8_f32<XT>(vec8_load<XT>(xr, c, p.cols), h);
+      if (p.w_type == kTypeF32)
+        weights<kTypeF32>(p, c, w);
+      else
+        weights<XT>(p, c, w);
+      put<XT, OUT>(p, row, c, kp, h, w, rstd);
+    }
+  }
 }
 
-__global__ void __launch_bounds__(kThreads) rms_dw_sum_kernel(RmsGradParams p) {
-  const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (c >= p.cols) return;
-  float s = 0.0f;
-  for (int q = 0; q < p.partials; ++q) s += p.ws[(int64_t)q * p.cols + c];
-  p.dW[c] = s;
+constexpr int64_t kMaxGrid = 1 << 20;  // a grid's threads have to stay below 2^32
+
+template <int XT, int RT, bool RES, int OUT>
+void launch_typed(const RmsParams& p, hipStream_t stream) {
+  const int64_t kp = (p.cols + 127) / 128 * 128;
+  // rows whose scale bytes fill a 128-byte line
+  const int line = p.out == kRmsFp8 ? 128 : p.out == kRmsFp4 ? 32 : 1;
+  const bool few = p.rows <= p.cus;
+  const int vpt = few && kp <= 8 * kRmsMaxLanes ? 1 : 2;
+  if (kp > (int64_t)vpt * 8 * kRmsMaxLanes) {
+    const unsigned g = (unsigned)(p.rows < kMaxGrid ? p.rows : kMaxGrid);
+    hipLaunchKernelGGL((rms_long_kernel<XT, RT, RES, OUT>), dim3(g), dim3(kRmsMaxLanes), 0, stream, p);
+    return;
+  }
+  const RmsShape s = rms_shape(kp, vpt);
+  const int64_t n = (p.rows + s.rows - 1) / s.rows;
+  const dim3 grid((unsigned)(n < kMaxGrid ? n : kMaxGrid));
+  const int chunk = line > s.rows ? line / s.rows : 1;
+  if (vpt == 1)
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 1>), grid, dim3(s.threads), 0, stream, p, s.lanes, chunk);
+  else
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 2>), grid, dim3(s.threads), 0, stream, p, s.lanes, chunk);
+}
+
+template <int XT, int RT, bool RES>
+void launch_out(const RmsParams& p, hipStream_t stream) {
+  if (p.out == kRmsSame)
+    launch_typed<XT, RT, RES, kRmsSame>(p, stream);
+  else if (p.out == kRmsFp8)
+    launch_typed<XT, RT, RES, kRmsFp8>(p, stream);
+  else
+    launch_typed<XT, RT, RES, kRmsFp4>(p, stream);
+}
+
+template <int XT>
+void launch_res(const RmsParams& p, hipStream_t stream) {
+  if (!p.R)
+    launch_out<XT, XT, false>(p, stream);
+  else if (XT == kTypeF32 || p.r_type != kTypeF32)
+    launch_out<XT, XT, true>(p, stream);
+  else
+    launch_out<XT, kTypeF32, true>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_rms(const RmsParams& p, hipStream_t stream) {
   if (p.rows == 0) return hipSuccess;
-  hipLaunchKernelGGL(rms_kernel, dim3((unsigned)p.rows), dim3(kThreads), 0, stream, p);
-  return hipGetLastError();
-}
-
-int rms_grad_partials(int64_t rows) { return (int)(rows < 64 ? rows : 64); }
-
-hipError_t launch_rms_grad(const RmsGradParams& p, hipStream_t stream) {
-  const unsigned cb = (unsigned)((p.cols + kThreads - 1) / kThreads);
-  if (p.dW) {  // before dX, which may take dY's place
-    if (p.partials > 0) hipLaunchKernelGGL(rms_dw_kernel, dim3(cb, (unsigned)p.partials), dim3(kThreads), 0, stream, p);
-    hipLaunchKernelGGL(rms_dw_sum_kernel, dim3(cb), dim3(kThreads), 0, stream, p);
-  }
-  if (p.rows > 0) hipLaunchKernelGGL(rms_dx_kernel, dim3((unsigned)p.rows), dim3(kThreads), 0, stream, p);
+  if (p.x_type == kTypeF32)
+    launch_res<kTypeF32>(p, stream);
+  else if (p.x_type == kTypeBF16)
+    launch_res<kTypeBF16>(p, stream);
+  else
+    launch_res<kTypeF16>(p, stream);
   return hipGetLastError();
 }
 

@@ -1,0 +1,271 @@
+// Gradient of the RMS norm:
+//   g = w * dy, c = sum(g * h), dx = dh + rstd * g - h * rstd^3 * c / cols
+//   dw = sum over the rows of dy * h * rstd
+//
+// One pass over dy, h and dh gives both.  A workgroup walks a strided set of
+// rows; its threads own columns, so their shares of dw stay in registers
+// (fp32) over the whole walk and leave once, as one row of partial sums.  The
+// next row's loads go out before this row's sum is waited for.  A second
+// kernel adds the partial sums in a fixed order: results repeat bit for bit.
+// Bound by memory.
+#include "common.hpp"
+#include "rms_device.hpp"
+
+namespace pgk {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int YT, int HT, int VPT>
+struct GradRow {
+  Vec8<YT> dy[VPT];
+  Vec8<HT> h[VPT], dh[VPT];
+  float rstd;
+};
+
+template <int YT, int HT, int VPT>
+__device__ __forceinline__ void load_row(const RmsGradParams& p, int64_t row, int L, int t0,
+                                         GradRow<YT, HT, VPT>& g) {
+  constexpr int ysz = YT == kTypeF32 ? 4 : 2, hsz = HT == kTypeF32 ? 4 : 2;
+  g.rstd = p.rstd[row];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int64_t c = ((int64_t)v * L + t0) * 8;
+    g.dy[v] = vec8_load<YT>(static_cast<const char*>(p.dY) + row * p.ldy * ysz, c, p.cols);
+    g.h[v] = vec8_load<HT>(static_cast<const char*>(p.H) + row * p.ldh * hsz, c, p.cols);
+    if (p.dH) g.dh[v] = vec8_load<HT>(static_cast<const char*>(p.dH) + row * p.ldd * hsz, c, p.cols);
+  }
+}
+
+template <int YT>
+__device__ __forceinline__ void weights(const RmsGradParams& p, int64_t c, float (&w)[8]) {
+  if (p.w_type == kTypeF32)
+    vec8_f32<kTypeF32>(vec8_load<kTypeF32>(p.W, c, p.cols), w);
+  else
+    vec8_f32<YT>(vec8_load<YT>(p.W, c, p.cols), w);
+}
+
+// dx of eight columns; k = rstd^3 * c / cols.
+template <int YT, int HT>
+__device__ __forceinline__ void put_dx(const RmsGradParams& p, int64_t row, int64_t c, const float (&dy)[8],
+                                       const float (&h)[8], const Vec8<HT>& dh, const float (&w)[8], float rstd,
+                                       float k) {
+  float d[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    d[e] = rstd * (dy[e] * w[e]) - h[e] * k;
+    if (p.dH) d[e] += vec8_get(dh, e);
+  }
+  vec8_store<HT>(static_cast<char*>(p.dX) + row * p.ldx * (HT == kTypeF32 ? 4 : 2), c, p.cols, vec8_pack<HT>(d));
+}
+
+template <int YT, int HT, int VPT, int THREADS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS) rms_grad_kernel(RmsGradParams p, int L) {
+  __shared__ float s_sum[2][16];
+  __shared__ float s_dw[VPT == 1 ? kThreads * 8 : 1];
+  const int t0 = L > 64 ? (int)threadIdx.x : (int)threadIdx.x & (L - 1);
+  const int per = L > 64 ? 1 : kThreads / L, sub = L > 64 ? 0 : (int)threadIdx.x / L;
+  const int64_t n = (p.rows + per - 1) / per;
+  float acc[VPT][8] = {};
+  float w[VPT][8];
+  auto load_w = [&]() {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) weights<YT>(p, ((int64_t)v * L + t0) * 8, w[v]);
+  };
+  if (VPT == 1) load_w();
+  const float inv = 1.0f / (float)p.cols;
+  GradRow<YT, HT, VPT> now;
+  int64_t i = blockIdx.x;
+  auto row_at = [&](int64_t j) {
+    const int64_t row = j * per + sub;
+    return row < p.rows ? row : p.rows - 1;
+  };
+  if (AHEAD && i < n) load_row(p, row_at(i), L, t0, now);
+  int turn = 0;
+  for (; i < n; i += gridDim.x, turn ^= 1) {
+    const bool on = i * per + sub < p.rows;
+    const int64_t row = row_at(i);
+    GradRow<YT, HT, VPT> next;
+    if (AHEAD) {
+      if (i + gridDim.x < n) load_row(p, row_at(i + gridDim.x), L, t0, next);
+    } else {
+      load_row(p, row, L, t0, now);
+    }
+    if (VPT != 1) load_w();  // two vectors leave no registers to keep it in
+    const float r = now.rstd;
+    float c = 0.0f;
+    float dy[VPT][8], h[VPT][8];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      vec8_f32<YT>(now.dy[v], dy[v]);
+      vec8_f32<HT>(now.h[v], h[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c += dy[v][e] * w[v][e] * h[v][e];
+        if (on) acc[v][e] += dy[v][e] * (h[v][e] * r);
+      }
+    }
+    const float k = r * r * r * (row_sum(c, L, s_sum, turn) * inv);
+    if (on) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        put_dx<YT, HT>(p, row, ((int64_t)v * L + t0) * 8, dy[v], h[v], now.dh[v], w[v], r, k);
+    }
+    if (AHEAD) now = next;
+  }
+  if (!p.dW) return;
+  if (VPT == 1 && per > 1) {  // the rows the workgroup took side by side
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_dw[(sub * L + t0) * 8 + e] = acc[0][e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < L * 8; c += kThreads) {
+      float s = 0.0f;
+      for (int q = 0; q < per; ++q) s += s_dw[q * L * 8 + c];
+      if (c < p.cols) p.ws[(int64_t)blockIdx.x * p.cols + c] = s;
+    }
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    vec8_store<kTypeF32>(p.ws + (int64_t)blockIdx.x * p.cols, ((int64_t)v * L + t0) * 8, p.cols,
+                         vec8_pack<kTypeF32>(acc[v]));
+}
+
+// Rows too long for registers: dw and dx each in a pass of its own, dw first
+// because dx may take dy's or dh's place.
+template <int YT, int HT>
+__global__ void __launch_bounds__(kThreads) rms_grad_long_dw_kernel(RmsGradParams p) {
+  constexpr int ysz = YT == kTypeF32 ? 4 : 2, hsz = HT == kTypeF32 ? 4 : 2;
+  const int64_t step = (int64_t)gridDim.x * kThreads * 8;
+  for (int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8; c < p.cols; c += step) {
+    float acc[8] = {};
+    for (int64_t row = blockIdx.y; row < p.rows; row += p.partials) {
+      float dy[8], h[8];
+      vec8_f32<YT>(vec8_load<YT>(static_cast<const char*>(p.dY) + row * p.ldy * ysz, c, p.cols), dy);
+      vec8_f32<HT>(vec8_load<HT>(static_cast<const char*>(p.H) + row * p.ldh * hsz, c, p.cols), h);
+      const float r = p.rstd[row];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += dy[e] * (h[e] * r);
+    }
+    vec8_store<kTypeF32>(p.ws + (int64_t)blockIdx.y * p.cols, c, p.cols, vec8_pack<kTypeF32>(acc));
+  }
+}
+
+template <int YT, int HT>
+__global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_long_dx_kernel(RmsGradParams p) {
+  __shared__ float s_sum[2][16];
+  constexpr int ysz = YT == kTypeF32 ? 4 : 2, hsz = HT == kTypeF32 ? 4 : 2;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const char* yr = static_cast<const char*>(p.dY) + row * p.ldy * ysz;
+    const char* hr = static_cast<const char*>(p.H) + row * p.ldh * hsz;
+    const float r = p.rstd[row];
+    float s = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < p.cols; c += kRmsMaxLanes * 8) {
+      float dy[8], h[8], w[8];
+      vec8_f32<YT>(vec8_load<YT>(yr, c, p.cols), dy);
+      vec8_f32<HT>(vec8_load<HT>(hr, c, p.cols), h);
+      weights<YT>(p, c, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += dy[e] * w[e] * h[e];
+    }
+    const float k = r * r * r * (row_sum(s, kRmsMaxLanes, s_sum, turn) / (float)p.cols);
+    for (int64_t c = threadIdx.x * 8; c < p.cols; c += kRmsMaxLanes * 8) {
+      float dy[8], h[8], w[8];
+      Vec8<HT> dh;
+      vec8_f32<YT>(vec8_load<YT>(yr, c, p.cols), dy);
+      vec8_f32<HT>(vec8_load<HT>(hr, c, p.cols), h);
+      if (p.dH) dh = vec8_load<HT>(static_cast<const char*>(p.dH) + row * p.ldd * hsz, c, p.cols);
+      weights<YT>(p, c, w);
+      put_dx<YT, HT>(p, row, c, dy, h, dh, w, r, k);
+    }
+  }
+}
+
+// dw from the partial sums: 32 columns per workgroup, eight threads to a
+// column, each an eighth of the partial sums.
+__global__ void __launch_bounds__(kThreads) rms_dw_sum_kernel(RmsGradParams p) {
+  __shared__ float s_part[8][32];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < p.cols; c0 += (int64_t)gridDim.x * 32) {
+    const int64_t c = c0 + x;
+    float s = 0.0f;
+    if (c < p.cols) {
+#pragma unroll 8
+      for (int q = y; q < p.partials; q += 8) s += p.ws[(int64_t)q * p.cols + c];
+    }
+    s_part[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < p.cols) {
+      for (int q = 1; q < 8; ++q) s += s_part[q][x];
+      p.dW[c] = s;
+    }
+    __syncthreads();
+  }
+}
+
+constexpr int64_t kMaxGrid = 1 << 20;  // a grid's threads have to stay below 2^32
+
+// How the rows are walked.  Up to 8192 columns one vector per thread: a wide
+// row keeps 16 waves busy, which leaves each the registers for the next row's
+// loads.  Two vectors up to 16384, then the passes over long rows.
+struct GradPlan {
+  int vpt;  // 0: long rows
+  RmsShape s;
+  int grid;
+};
+GradPlan grad_plan(int64_t rows, int64_t cols, int cus) {
+  const int64_t kp = (cols + 127) / 128 * 128;
+  GradPlan g;
+  g.vpt = kp <= 8 * kRmsMaxLanes ? 1 : kp <= 16 * kRmsMaxLanes ? 2 : 0;
+  if (g.vpt == 0) {
+    g.s = {kRmsMaxLanes, kRmsMaxLanes, 1};
+    g.grid = (int)(rows < 64 ? rows : 64);
+    return g;
+  }
+  g.s = rms_shape(kp, g.vpt);
+  const int64_t n = (rows + g.s.rows - 1) / g.s.rows, most = (int64_t)cus * (kRmsMaxLanes / g.s.threads);
+  g.grid = (int)(n < most ? n : most);
+  return g;
+}
+
+template <int YT, int HT>
+void launch_typed(const RmsGradParams& p, hipStream_t stream) {
+  const GradPlan g = grad_plan(p.rows, p.cols, p.cus);
+  if (p.rows > 0 && g.vpt == 0) {
+    if (p.dW) {
+      const int64_t n = (p.cols + kThreads * 8 - 1) / (kThreads * 8);
+      const dim3 grid((unsigned)(n < 65536 ? n : 65536), (unsigned)p.partials);
+      hipLaunchKernelGGL((rms_grad_long_dw_kernel<YT, HT>), grid, dim3(kThreads), 0, stream, p);
+    }
+    const unsigned rows = (unsigned)(p.rows < kMaxGrid ? p.rows : kMaxGrid);
+    hipLaunchKernelGGL((rms_grad_long_dx_kernel<YT, HT>), dim3(rows), dim3(kRmsMaxLanes), 0, stream, p);
+  } else if (p.rows > 0) {
+    const dim3 grid((unsigned)(p.dW ? p.partials : g.grid)), threads(g.s.threads);
+    if (g.vpt == 1)
+      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 1, 1024, true>), grid, threads, 0, stream, p, g.s.lanes);
+    else
+      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 2, 1024, false>), grid, threads, 0, stream, p, g.s.lanes);
+  }
+  if (p.dW) {
+    const int64_t n = (p.cols + 31) / 32;
+    hipLaunchKernelGGL(rms_dw_sum_kernel, dim3((unsigned)(n < kMaxGrid ? n : kMaxGrid)), dim3(kThreads), 0, stream, p);
+  }
+}
+
+}  // namespace
+
+// Rows of partial sums a call leaves (0 rows: none).
+int rms_grad_partials(int64_t rows, int64_t cols, int cus) { return grad_plan(rows, cols, cus).grid; }
+
+hipError_t launch_rms_grad(const RmsGradParams& p, hipStream_t stream) {
+  if (p.y_type == kTypeF32)
+    launch_typed<kTypeF32, kTypeF32>(p, stream);
+  else if (p.y_type == kTypeBF16)
+    p.h_type == kTypeF32 ? launch_typed<kTypeBF16, kTypeF32>(p, stream) : launch_typed<kTypeBF16, kTypeBF16>(p, stream);
+  else
+    p.h_type == kTypeF32 ? launch_typed<kTypeF16, kTypeF32>(p, stream) : launch_typed<kTypeF16, kTypeF16>(p, stream);
+  return hipGetLastError();
+}
+
+}  // namespace pgk

@@ -1174,7 +1174,7 @@ pgemm_status pmx_quant_run(pgemm_config* cfg, const void* X, int x_type, int64_t
   if (!aligned(Q, 4) || !aligned(scale, 4)) return PGEMM_ERR_UNSUPPORTED;
   DeviceGuard g(dev);
   if (!g.ok) return PGEMM_ERR_DEVICE;
-  const pgk::QuantParams p = {X, x_type, rows, cols, ldx, transpose, rule, Q, scale};
+  const pgk::QuantParams p = {X, x_type, rows, cols, ldx, transpose, rule, Q, scale, cfg->num_cus};
   return pgk::launch_quant(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
 }
 
@@ -1192,7 +1192,7 @@ pgemm_status pmx_dequant_run(pgemm_config* cfg, const uint8_t* Q, const uint8_t*
   if (!aligned(Q, 4) || !aligned(scale, 4)) return PGEMM_ERR_UNSUPPORTED;
   DeviceGuard g(dev);
   if (!g.ok) return PGEMM_ERR_DEVICE;
-  const pgk::DequantParams p = {Q, scale, rows, cols, ldy, Y, y_type};
+  const pgk::DequantParams p = {Q, scale, rows, cols, ldy, Y, y_type, cfg->num_cus};
   return pgk::launch_dequant(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
 }
 
@@ -1244,7 +1244,7 @@ pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx,
   DeviceGuard g(dev);
   if (!g.ok) return PGEMM_ERR_DEVICE;
   const pgk::RmsParams p = {X,   R,   W,   x_type, r_type, w_type, out, ldx, ldr, ldh,
-                            ldy, rows, cols, eps,   H,      Y,      y_scale, rstd};
+                            ldy, rows, cols, eps,   H,      Y,      y_scale, rstd, cfg->num_cus, cfg->num_xcds};
   return pgk::launch_rms(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
 }
 
@@ -1271,7 +1271,7 @@ pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_
     return PGEMM_ERR_INVALID;
   int partials = 0;
   if (dW) {
-    partials = pgk::rms_grad_partials(rows);
+    partials = pgk::rms_grad_partials(rows, cols, cfg->num_cus);
     const int64_t fit = (int64_t)(cfg->ws_bytes / ((size_t)cols * sizeof(float)));
     if (fit < 1) return PGEMM_ERR_UNSUPPORTED;
     if (partials > fit) partials = (int)fit;
@@ -1279,7 +1279,7 @@ pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_
   DeviceGuard g(dev);
   if (!g.ok) return PGEMM_ERR_DEVICE;
   const pgk::RmsGradParams p = {dY,  H,   dH,  W,    rstd, y_type, h_type, w_type,  ldy,
-                                ldh, ldd, ldx, rows, cols, dX,     dW,     cfg->ws, partials};
+                                ldh, ldd, ldx, rows, cols, dX,     dW,     cfg->ws, partials, cfg->num_cus};
   return pgk::launch_rms_grad(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
 }
 
