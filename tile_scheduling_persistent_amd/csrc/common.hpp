@@ -192,7 +192,7 @@ int padd_tiles_per_step(int tr, int tc);
 bool gemm_fp4_tile_supported(int bm, int bn, int bk);
 bool gemm_fp4_eligible(int bm, int bn, long long M, long long N, long long K);
 void gemm_fp4_default_tile(long long M, long long N, long long K, int cus, int& bm, int& bn, int& bk);
-hipError_t launch_gemm_fp4(const GemmParams& p, int bm, int bn, bool witness, hipStream_t stream);
+hipError_t launch_gemm_fp4(const GemmParams& p, int bm, int bn, hipStream_t stream);
 
 // Launch shape of a kernel instance: threads and dynamic LDS per workgroup,
 // and how many such workgroups one CU holds at once (registers, LDS, waves).

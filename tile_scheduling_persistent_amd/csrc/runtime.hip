@@ -837,7 +837,7 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
   if (st != PGEMM_OK) return st;
   st = reset_counters(args, p.s, cfg->capacity, &cfg->counters_dirty, witness, stream);
   if (st != PGEMM_OK) return st;
-  hipError_t e = fp4 ? pgk::launch_gemm_fp4(p, bm, bn, witness, stream)
+  hipError_t e = fp4 ? pgk::launch_gemm_fp4(p, bm, bn, stream)
                  : fp8 ? pgk::launch_gemm_fp8_grouped(p, bm, bn, witness, stream)
                      : pgk::launch_gemm_bf16_lds_grouped(p, bm, bn, csz == 2, witness, stream);
   if (e == hipErrorInvalidValue) return PGEMM_ERR_UNSUPPORTED;
@@ -1001,7 +1001,7 @@ pgemm_status gemm_call(pgemm_config* cfg, const void* A, const void* B, void* C,
 
   hipError_t e;
   if (fp4)
-    e = pgk::launch_gemm_fp4(p, ch.bm, ch.bn, witness, stream);
+    e = pgk::launch_gemm_fp4(p, ch.bm, ch.bn, stream);
   else if (fp8)
     e = sk ? pgk::launch_gemm_fp8_sk(p, ch.bm, ch.bn, stream)
            : pgk::launch_gemm_fp8(p, ch.bm, ch.bn, ch.bk, true, witness, stream);
