@@ -138,7 +138,7 @@ struct RmsParams {
   const void* W;
   int x_type, r_type, w_type, out;
   int64_t ldx, ldr, ldh, ldy, rows, cols;
-  double eps;
+  double eps, inv_cols;
   void* H;        // null without a residual
   void* Y;
   uint8_t* y_scale;

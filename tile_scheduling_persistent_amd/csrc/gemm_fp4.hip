@@ -509,9 +509,9 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
 
 // ------------------------------------------------------------- a few rows
 //
-// A tile is 16 * SM rows by 16 * SN columns; wave w of the workgroup takes
-// every WAVES-th 256-deep unit of K: per B row 128 bytes, one line, as two
-// 16-byte loads per lane, DEPTH units in flight.  A comes from the caches.
+// A tile is 16 * SM rows by 16 * SN columns; each wave of the workgroup takes
+// a stretch of K in units of 256 (per B row 128 bytes, one line, as two
+// 16-byte loads per lane), DEPTH units in flight.  A comes from the caches.
 // The waves' sums meet in LDS.
 template <int SM, int SN, int DEPTH, bool GRP>
 __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmParams P) {
@@ -598,19 +598,20 @@ __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmPar
       }
     };
     f32x4 acc[SN][SM] = {};
-    const int units = (steps + 1) >> 1;
+    // the wave's units: a consecutive stretch, so that a row's lines are read
+    // one after the other
+    const int units = (steps + 1) >> 1, u0 = units * wave / waves, u1 = units * (wave + 1) / waves;
     Unit x[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
-      if (wave + d * waves < units) load(wave + d * waves, x[d]);
-    for (int u = wave; u < units; u += DEPTH * waves) {
+      if (u0 + d < u1) load(u0 + d, x[d]);
+    for (int u = u0; u < u1; u += DEPTH) {
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
-        const int ud = u + d * waves;
-        if (ud >= units) break;
+        if (u + d >= u1) break;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (ud * 2 + s >= steps) break;
+          if ((u + d) * 2 + s >= steps) break;
 #pragma unroll
           for (int j = 0; j < SN; ++j)
 #pragma unroll
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmPar
                                             __builtin_bit_cast(i32x4, x[d].a[s][i]), acc[j][i], (int)x[d].sb[s][j],
                                             (int)x[d].sa[s][i]);
         }
-        if (ud + DEPTH * waves < units) load(ud + DEPTH * waves, x[d]);
+        if (u + DEPTH + d < u1) load(u + DEPTH + d, x[d]);
       }
     }
 #pragma unroll

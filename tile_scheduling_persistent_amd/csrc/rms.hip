@@ -33,6 +33,18 @@ __device__ __forceinline__ int64_t group_of(int64_t i, int64_t n, int X, int chu
   return j / chunk * per + x * chunk + j % chunk;
 }
 
+// 1 / sqrt(x) to the last bit or two: the approximate instruction and two
+// Newton steps, a third of the instructions of a square root and a division,
+// which every wave of a row would run.  Zero and infinity as the instruction
+// has them.
+__device__ __forceinline__ double inv_sqrt(double x) {
+  const double r0 = __builtin_amdgcn_rsq(x);
+  double r = r0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = r + r * (0.5 - 0.5 * x * r * r);
+  return x > 0.0 && x < __builtin_inf() ? r : r0;
+}
+
 template <int WT>
 __device__ __forceinline__ void weights(const RmsParams& p, int64_t c, float (&w)[8]) {
   vec8_f32<WT>(vec8_load<WT>(p.W, c, p.cols), w);
@@ -104,15 +116,14 @@ __device__ __forceinline__ void put(const RmsParams& p, int64_t row, int64_t c, 
 
 // Rows held in registers: VPT vectors per thread.
 template <int XT, int RT, bool RES, int OUT, int VPT>
-__global__ void __launch_bounds__(kRmsMaxLanes) rms_kernel(RmsParams p, int L, int chunk) {
+__global__ void __launch_bounds__(VPT == 1 ? kRmsMaxLanes : kRmsMaxLanes / 2) rms_kernel(RmsParams p, int L, int chunk) {
   __shared__ double s_sum[2][16];
-  const int t = threadIdx.x & (L - 1), sub = threadIdx.x / L, per = blockDim.x / L;  // L <= 64: a power of two
-  const int t0 = L > 64 ? (int)threadIdx.x : t;
+  const int per = (int)blockDim.x / L, sub = (int)threadIdx.x / L, t0 = (int)threadIdx.x - sub * L;
   const int64_t kp = (p.cols + 127) / 128 * 128, n = (p.rows + per - 1) / per;
   constexpr int xsz = XT == kTypeF32 ? 4 : 2, rsz = RT == kTypeF32 ? 4 : 2;
   int turn = 0;
   for (int64_t i = blockIdx.x; i < n; i += gridDim.x, turn ^= 1) {
-    const int64_t row = group_of(i, n, p.xcds, chunk) * per + (L > 64 ? 0 : sub);
+    const int64_t row = group_of(i, n, p.xcds, chunk) * per + sub;
     const bool on = row < p.rows;
     const int64_t at = on ? row : p.rows - 1;
     Vec8<XT> x[VPT];
@@ -133,7 +144,7 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_kernel(RmsParams p, int L, i
       for (int e = 0; e < 8; ++e) s += (double)h[v][e] * (double)h[v][e];
     }
     s = row_sum(s, L, s_sum, turn);
-    const double rstd = 1.0 / sqrt(s / (double)p.cols + p.eps);
+    const double rstd = inv_sqrt(s * p.inv_cols + p.eps);
     if (!on) continue;
     if (t0 == 0 && p.rstd) p.rstd[row] = (float)rstd;
 #pragma unroll
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_long_kernel(RmsParams p) {
       for (int e = 0; e < 8; ++e) s += (double)h[e] * (double)h[e];
     }
     s = row_sum(s, kRmsMaxLanes, s_sum, turn);
-    const double rstd = 1.0 / sqrt(s / (double)p.cols + p.eps);
+    const double rstd = inv_sqrt(s * p.inv_cols + p.eps);
     if (threadIdx.x == 0 && p.rstd) p.rstd[row] = (float)rstd;
     for (int64_t c = threadIdx.x * 8; c < kp; c += kRmsMaxLanes * 8) {
       float h[8], w[8];
@@ -194,21 +205,23 @@ void launch_typed(const RmsParams& p, hipStream_t stream) {
   const int64_t kp = (p.cols + 127) / 128 * 128;
   // rows whose scale bytes fill a 128-byte line
   const int line = p.out == kRmsFp8 ? 128 : p.out == kRmsFp4 ? 32 : 1;
-  const bool few = p.rows <= p.cus;
-  const int vpt = few && kp <= 8 * kRmsMaxLanes ? 1 : 2;
-  if (kp > (int64_t)vpt * 8 * kRmsMaxLanes) {
+  // A row's reduction and its 1 / sqrt are work per wave, so few waves per row
+  // where rows fill the device; for a handful, as many as there are.
+  const int vpt = p.rows <= p.cus && kp <= 8 * kRmsMaxLanes ? 1 : 4;
+  if (kp > 16384) {
     const unsigned g = (unsigned)(p.rows < kMaxGrid ? p.rows : kMaxGrid);
     hipLaunchKernelGGL((rms_long_kernel<XT, RT, RES, OUT>), dim3(g), dim3(kRmsMaxLanes), 0, stream, p);
     return;
   }
-  const RmsShape s = rms_shape(kp, vpt);
-  const int64_t n = (p.rows + s.rows - 1) / s.rows;
+  const int L = rms_lanes(kp, vpt), per = L < 256 ? 256 / L : 1;
+  const dim3 threads(L * per);
+  const int64_t n = (p.rows + per - 1) / per;
   const dim3 grid((unsigned)(n < kMaxGrid ? n : kMaxGrid));
-  const int chunk = line > s.rows ? line / s.rows : 1;
+  const int chunk = line > per ? line / per : 1;
   if (vpt == 1)
-    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 1>), grid, dim3(s.threads), 0, stream, p, s.lanes, chunk);
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 1>), grid, threads, 0, stream, p, L, chunk);
   else
-    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 2>), grid, dim3(s.threads), 0, stream, p, s.lanes, chunk);
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 4>), grid, threads, 0, stream, p, L, chunk);
 }
 
 template <int XT, int RT, bool RES>

@@ -59,12 +59,11 @@ __device__ __forceinline__ void put_dx(const RmsGradParams& p, int64_t row, int6
   vec8_store<HT>(static_cast<char*>(p.dX) + row * p.ldx * (HT == kTypeF32 ? 4 : 2), c, p.cols, vec8_pack<HT>(d));
 }
 
-template <int YT, int HT, int VPT, int THREADS, bool AHEAD>
-__global__ void __launch_bounds__(THREADS) rms_grad_kernel(RmsGradParams p, int L) {
+template <int YT, int HT, int VPT, bool AHEAD>
+__global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_kernel(RmsGradParams p, int L) {
   __shared__ float s_sum[2][16];
-  __shared__ float s_dw[VPT == 1 ? kThreads * 8 : 1];
-  const int t0 = L > 64 ? (int)threadIdx.x : (int)threadIdx.x & (L - 1);
-  const int per = L > 64 ? 1 : kThreads / L, sub = L > 64 ? 0 : (int)threadIdx.x / L;
+  __shared__ float s_dw[VPT == 1 ? kRmsMaxLanes * 8 : 1];
+  const int per = (int)blockDim.x / L, sub = (int)threadIdx.x / L, t0 = (int)threadIdx.x - sub * L;
   const int64_t n = (p.rows + per - 1) / per;
   float acc[VPT][8] = {};
   float w[VPT][8];
@@ -118,7 +117,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(RmsGradParams p, int 
 #pragma unroll
     for (int e = 0; e < 8; ++e) s_dw[(sub * L + t0) * 8 + e] = acc[0][e];
     __syncthreads();
-    for (int c = threadIdx.x; c < L * 8; c += kThreads) {
+    for (int c = threadIdx.x; c < L * 8; c += blockDim.x) {
       float s = 0.0f;
       for (int q = 0; q < per; ++q) s += s_dw[q * L * 8 + c];
       if (c < p.cols) p.ws[(int64_t)blockIdx.x * p.cols + c] = s;
@@ -182,50 +181,57 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_long_dx_kernel(RmsGradP
   }
 }
 
-// dw from the partial sums: 32 columns per workgroup, eight threads to a
-// column, each an eighth of the partial sums.
-__global__ void __launch_bounds__(kThreads) rms_dw_sum_kernel(RmsGradParams p) {
-  __shared__ float s_part[8][32];
+// dw from the partial sums: 32 columns per workgroup, 32 threads to a column,
+// so that the few hundred rows of partial sums are a handful of loads each.
+__global__ void __launch_bounds__(1024) rms_dw_sum_kernel(RmsGradParams p) {
+  __shared__ float s_part[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < p.cols; c0 += (int64_t)gridDim.x * 32) {
     const int64_t c = c0 + x;
     float s = 0.0f;
     if (c < p.cols) {
 #pragma unroll 8
-      for (int q = y; q < p.partials; q += 8) s += p.ws[(int64_t)q * p.cols + c];
+      for (int q = y; q < p.partials; q += 32) s += p.ws[(int64_t)q * p.cols + c];
     }
     s_part[y][x] = s;
     __syncthreads();
+    // eight sums of four, then of two eight times over
+    if (y < 8) s_part[y][x] = (s + s_part[y + 8][x]) + (s_part[y + 16][x] + s_part[y + 24][x]);
+    __syncthreads();
     if (y == 0 && c < p.cols) {
-      for (int q = 1; q < 8; ++q) s += s_part[q][x];
-      p.dW[c] = s;
+      for (int q = 1; q < 8; ++q) s_part[0][x] += s_part[q][x];
+      p.dW[c] = s_part[0][x];
     }
     __syncthreads();
   }
 }
 
+constexpr int kWorkgroupsPerCu = 1;
 constexpr int64_t kMaxGrid = 1 << 20;  // a grid's threads have to stay below 2^32
 
 // How the rows are walked.  Up to 8192 columns one vector per thread: a wide
 // row keeps 16 waves busy, which leaves each the registers for the next row's
-// loads.  Two vectors up to 16384, then the passes over long rows.
+// loads; several shorter rows go side by side in one workgroup, so that the
+// partial sums of dw stay one row per workgroup.  Two vectors up to 16384
+// columns, then the passes over long rows.
 struct GradPlan {
   int vpt;  // 0: long rows
-  RmsShape s;
-  int grid;
+  int lanes, threads, grid;
 };
 GradPlan grad_plan(int64_t rows, int64_t cols, int cus) {
   const int64_t kp = (cols + 127) / 128 * 128;
   GradPlan g;
   g.vpt = kp <= 8 * kRmsMaxLanes ? 1 : kp <= 16 * kRmsMaxLanes ? 2 : 0;
   if (g.vpt == 0) {
-    g.s = {kRmsMaxLanes, kRmsMaxLanes, 1};
+    g.lanes = g.threads = kRmsMaxLanes;
     g.grid = (int)(rows < 64 ? rows : 64);
     return g;
   }
-  g.s = rms_shape(kp, g.vpt);
-  const int64_t n = (rows + g.s.rows - 1) / g.s.rows, most = (int64_t)cus * (kRmsMaxLanes / g.s.threads);
-  g.grid = (int)(n < most ? n : most);
+  g.lanes = rms_lanes(kp, g.vpt);
+  const int per = g.vpt == 1 ? kRmsMaxLanes / g.lanes : 1;
+  g.threads = per * g.lanes;
+  const int64_t n = (rows + per - 1) / per;
+  g.grid = (int)(n < kWorkgroupsPerCu * cus ? n : kWorkgroupsPerCu * cus);
   return g;
 }
 
@@ -241,15 +247,15 @@ void launch_typed(const RmsGradParams& p, hipStream_t stream) {
     const unsigned rows = (unsigned)(p.rows < kMaxGrid ? p.rows : kMaxGrid);
     hipLaunchKernelGGL((rms_grad_long_dx_kernel<YT, HT>), dim3(rows), dim3(kRmsMaxLanes), 0, stream, p);
   } else if (p.rows > 0) {
-    const dim3 grid((unsigned)(p.dW ? p.partials : g.grid)), threads(g.s.threads);
+    const dim3 grid((unsigned)(p.dW ? p.partials : g.grid)), threads(g.threads);
     if (g.vpt == 1)
-      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 1, 1024, true>), grid, threads, 0, stream, p, g.s.lanes);
+      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 1, true>), grid, threads, 0, stream, p, g.lanes);
     else
-      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 2, 1024, false>), grid, threads, 0, stream, p, g.s.lanes);
+      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 2, false>), grid, threads, 0, stream, p, g.lanes);
   }
   if (p.dW) {
     const int64_t n = (p.cols + 31) / 32;
-    hipLaunchKernelGGL(rms_dw_sum_kernel, dim3((unsigned)(n < kMaxGrid ? n : kMaxGrid)), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL(rms_dw_sum_kernel, dim3((unsigned)(n < kMaxGrid ? n : kMaxGrid)), dim3(1024), 0, stream, p);
   }
 }
 

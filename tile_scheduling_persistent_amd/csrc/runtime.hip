@@ -1244,7 +1244,7 @@ pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx,
   DeviceGuard g(dev);
   if (!g.ok) return PGEMM_ERR_DEVICE;
   const pgk::RmsParams p = {X,   R,   W,   x_type, r_type, w_type, out, ldx, ldr, ldh,
-                            ldy, rows, cols, eps,   H,      Y,      y_scale, rstd, cfg->num_cus, cfg->num_xcds};
+                            ldy, rows, cols, eps,   1.0 / (double)cols, H,      Y,      y_scale, rstd, cfg->num_cus, cfg->num_xcds};
   return pgk::launch_rms(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
 }
 
