@@ -27,7 +27,10 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr int kFmtE2M1 = 4;  // f8f6f4 operand format code of e2m1
@@ -53,11 +56,19 @@ __device__ __forceinline__ f32x4 mfma_scaled(i32x4 a, i32x4 b, f32x4 c, int sa, 
                                                           kFmtE2M1, OPSEL_A, sa, OPSEL_B, sb);
 }
 
-// Columns c .. c + 3 (fp32) or c .. c + 7 (bf16) of a row of C that ends at n.
+template <int OPSEL_A, int OPSEL_B>
+__device__ __forceinline__ f32x16 mfma_scaled32(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
+                                                         i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, c, kFmtE2M1,
+                                                         kFmtE2M1, OPSEL_A, sa, OPSEL_B, sb);
+}
+
 // Rows of C start on any element; stores of any alignment are single
-// instructions.
+// instructions.  Columns c .. c + 3 of a row of C that ends at n:
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef unsigned u32_a2 __attribute__((aligned(2)));
 __device__ __forceinline__ void store_f32x4(float* row, int64_t c, int64_t n, f32x4 v) {
   if (c + 4 <= n) {
     *reinterpret_cast<u32x4_a4*>(row + c) = __builtin_bit_cast(u32x4, v);
@@ -67,13 +78,34 @@ __device__ __forceinline__ void store_f32x4(float* row, int64_t c, int64_t n, f3
       if (c + e < n) row[c + e] = v[e];
   }
 }
-__device__ __forceinline__ void store_bf16x8(unsigned short* row, int64_t c, int64_t n, u32x4 v) {
-  if (c + 8 <= n) {
-    *reinterpret_cast<u32x4_a2*>(row + c) = v;
+// W (2 or 4) columns at p, those before `left`.
+template <int W>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[W], int64_t left) {
+  if (left >= W) {
+    if constexpr (W == 4)
+      *reinterpret_cast<u32x4_a4*>(p) = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+    else
+      *reinterpret_cast<u32x2_a4*>(p) = __builtin_bit_cast(u32x2, f32x2{v[0], v[1]});
   } else {
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (c + e < n) row[c + e] = (unsigned short)(v[e >> 1] >> (16 * (e & 1)));
+    for (int e = 0; e < W - 1; ++e)
+      if (e < left) p[e] = v[e];
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_row(unsigned short* p, const float (&v)[W], int64_t left) {
+  unsigned o[W / 2];
+#pragma unroll
+  for (int e = 0; e < W / 2; ++e) o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  if (left >= W) {
+    if constexpr (W == 4)
+      *reinterpret_cast<u32x2_a2*>(p) = u32x2{o[0], o[1]};
+    else
+      *reinterpret_cast<u32_a2*>(p) = o[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < W - 1; ++e)
+      if (e < left) p[e] = (unsigned short)(o[e >> 1] >> (16 * (e & 1)));
   }
 }
 
@@ -100,18 +132,47 @@ template <int BM, int BN, int NST_>
 struct Shape {
   static constexpr int NST = NST_;
   static constexpr int TM = BM / 2, TN = BN / 2;
-  static constexpr int SM = TM / 16, SN = TN / 16;
+  static constexpr int SM = TM / 32, SN = TN / 32;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int SA_BYTES = BM * 8, SB_BYTES = BN * 8;  // two groups of words
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static constexpr int LDS_BYTES = NST * STAGE + 16;  // + first tile, next tile [2]
   static constexpr int NA = BM / 32, NB = BN / 32;    // 1 KB operand loads per wave per slab
-  static constexpr int NSA = BM / 128, NSB = BN / 128;  // 256-byte scale loads per wave per slab
-  static constexpr int NL = NA + NB + NSA + NSB;
-  static constexpr int NMF = SM * SN;                 // MFMAs per 128-deep step
-  static constexpr int NRD = SM + SN + SM / 4 + SN / 4;
-  static_assert(SM % 4 == 0 && SN % 4 == 0, "scale bytes gathered four blocks at a time");
+  static constexpr int NL = NA + NB + 1;              // + one 1 KB load of scale words
+  static constexpr int NMF = 2 * SM * SN;             // MFMAs per 128-deep step
+  static constexpr int NRD = 2 * SM + 2 * SN + 2;     // LDS reads per 128-deep step
+  static_assert((SM == 2 || SM == 4) && (SN == 2 || SN == 4), "a row's scale words in one LDS read");
   static_assert(BM % 128 == 0 && BN % 128 == 0 && NA % 2 == 0 && NB % 2 == 0, "whole loads per wave");
+};
+
+// LDS layout of an operand.  Block i of a wave's BLOCKS 32-row blocks is made
+// of the rows l * BLOCKS + i (l = 0 .. 31) of the wave's half.  Eight
+// consecutive rows, 128 bytes each, are a 1 KB chunk; within it rows of one
+// block stand together, and a row's 16-byte pieces are permuted by l >> 1.
+// So a ds_read_b128, served 16 lanes (16 consecutive l of one block and
+// piece) at a time, meets all 16 slots of a 256-byte window.
+template <int BLOCKS>
+__device__ __forceinline__ int slot_row(int slot) {  // row of a slot of the chunk
+  return BLOCKS == 4 ? 4 * (slot & 1) + (slot >> 1) : 2 * (slot & 3) + (slot >> 2);
+}
+template <int BLOCKS>
+__device__ __forceinline__ int row_slot(int l) {  // bytes to row l of block 0 (block i: + i * 1024 / BLOCKS)
+  return BLOCKS == 4 ? (l >> 1) * 1024 + (l & 1) * 128 : (l >> 2) * 1024 + (l & 3) * 128;
+}
+// The part of l >> 1 (mod 8) that the chunk's index gives.
+template <int BLOCKS>
+__device__ __forceinline__ constexpr unsigned piece_flip(int chunk) {
+  return BLOCKS == 4 ? (unsigned)chunk & 7u : 2u * ((unsigned)chunk & 3u);
+}
+
+// The scale words of one row of each of the wave's blocks.
+template <int BLOCKS>
+struct Words {
+  typedef u32x4 type;
+};
+template <>
+struct Words<2> {
+  typedef u32x2 type;
 };
 
 template <int BM, int BN, int NST, bool GRP>
@@ -121,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   constexpr int SM = S::SM, SN = S::SN;
   // Of a period's 2 * NMF MFMA positions, the loads take the first SPREAD, and
   // the next step's LDS reads the first RSPREAD of each step's.
-  constexpr int SPREAD = NL > NMF ? 2 * NMF : NMF;
+  constexpr int SPREAD = NST > 2 ? 2 * NMF : NMF;
   constexpr int RSPREAD = NRD > NMF * 3 / 4 ? NMF : NMF * 3 / 4;
 
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
@@ -132,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  const int l16 = lane & 15, kb = lane >> 4;
+  const int l32 = lane & 31, kb = lane >> 5;
   const int prog = pgs::program_of(blockIdx.x, P.s.G, P.s.X, P.s.xcd_major);
   // the loader tile's problem and the matrix cores' tile's problem
   int Ml = P.M, Nl = P.N, Kl = P.K;
@@ -153,40 +214,41 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   }
 
   // Global -> LDS.  Operands: instruction q covers rows 8q .. 8q + 7, lane p
-  // row 8q + p / 8, LDS chunk p % 8, global chunk (p % 8) ^ ((row >> 1) & 7).
-  // Instruction i of wave w is q = w * NA + i (NA even), so the chunk depends
-  // on the lane and on i's parity only.
+  // slot p / 8 of LDS chunk q; instruction d of wave w is q = w * N + d.
   const int r8 = lane >> 3;
-  const unsigned chunk0 = (unsigned)((lane & 7) ^ ((r8 >> 1) & 7));  // q even; odd q: ^ 4
-  unsigned aoff = 0, boff = 0;  // instruction 0, chunk excluded
-  unsigned astep = 0;           // 8 rows
+  unsigned aoff = 0, boff = 0;  // row of instruction 0
+  unsigned rowb = 0;
   auto lane_offsets = [&](int Kx) {
-    const unsigned rowb = (unsigned)Kx >> 1;
-    aoff = (unsigned)(wave * NA * 8 + r8) * rowb;
-    boff = (unsigned)(wave * NB * 8 + r8) * rowb;
-    astep = 8u * rowb;
+    rowb = (unsigned)Kx >> 1;
+    aoff = (unsigned)(wave * NA * 8 + slot_row<SM>(r8)) * rowb;
+    boff = (unsigned)(wave * NB * 8 + slot_row<SN>(r8)) * rowb;
   };
   lane_offsets(Kl);
-  // Scales: LDS dword d of the A region (group, half of the tile, l16, block)
-  // holds the word of row half * TM + block * 16 + l16; likewise B.
-  auto scale_row = [&](int d, int B, int T, int SB, int& grp, int& row) {
-    grp = d / B;
-    const int rem = d % B, half = rem / T, e = rem % T;
-    row = half * T + (e % SB) * 16 + e / SB;
-  };
+  // 16-byte piece of the lane in instruction 0, in bytes; d flips bits of it
+  const unsigned apiece = (unsigned)((lane & 7) ^ (SM == 2 ? r8 >> 1 & 1 : 0)) * 16u;
+  const unsigned bpiece = (unsigned)((lane & 7) ^ (SN == 2 ? r8 >> 1 & 1 : 0)) * 16u;
+  // Scale words, four rows of one group per lane: waves 0 and 1 A's, 2 and 3
+  // B's.  256 rows: a group each; 128 rows: both groups, twice the same.
+  const bool of_a = wave < 2;
+  const int srows = of_a ? BM : BN;
+  const int sgrp = srows == 256 ? (wave & 1) : (lane >> 5);
+  const int srow = (srows == 256 ? lane : (lane & 31)) * 4;
+  const unsigned slds = (unsigned)(S::A_BYTES + S::B_BYTES + (of_a ? 0 : S::SA_BYTES) +
+                                   (srows == 256 ? (wave & 1) * 1024 : 0));
   const unsigned lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
 
-  // LDS reads: step s, block i: row (block origin) + l16, chunk 4 s + kb.
-  unsigned rd_a[2], rd_b[2];
+  // LDS reads: step s, half u: piece 4 s + 2 u + kb of row l32 of a block.
+  unsigned rd_a[2][2], rd_b[2][2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const unsigned c = (unsigned)((4 * s + kb) ^ ((l16 >> 1) & 7));
-    rd_a[s] = (unsigned)((wm * S::TM + l16) * 128) + c * 16u;
-    rd_b[s] = (unsigned)(S::A_BYTES + (wn * S::TN + l16) * 128) + c * 16u;
+  for (int q = 0; q < 4; ++q) {
+    const unsigned c = (unsigned)((2 * q + kb) ^ (l32 >> 1 & 7)) * 16u;
+    rd_a[q >> 1][q & 1] = (unsigned)(wm * S::TM * 128 + row_slot<SM>(l32)) + c;
+    rd_b[q >> 1][q & 1] = (unsigned)(S::A_BYTES + wn * S::TN * 128 + row_slot<SN>(l32)) + c;
   }
-  const unsigned rd_sa = (unsigned)(S::A_BYTES + S::B_BYTES + (wm * S::TM + l16 * SM) * 4);
-  const unsigned rd_sb = (unsigned)(S::A_BYTES + S::B_BYTES + S::SA_BYTES + (wn * S::TN + l16 * SN) * 4);
-  // v_perm selectors: byte kb of two words into the low or the high half
+  const unsigned rd_sa = (unsigned)(S::A_BYTES + S::B_BYTES + (wm * S::TM + l32 * SM) * 4);
+  const unsigned rd_sb = (unsigned)(S::A_BYTES + S::B_BYTES + S::SA_BYTES + (wn * S::TN + l32 * SN) * 4);
+  // v_perm selectors: byte kb (half 1: kb + 2) of two words into the low or
+  // the high half
   const unsigned sel_lo = 0x0c0c0400u + 0x0101u * (unsigned)kb;
   const unsigned sel_hi = 0x04000c0cu + 0x01010000u * (unsigned)kb;
 
@@ -218,11 +280,11 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   for (int i = 0; i < NST - 1; ++i) pend[i] = -1;
   int claims = 0;
   int lm0 = 0, ln0 = 0;
-  rsrc_words_t rA, rB, rSA, rSB;
+  rsrc_words_t rA, rB, rS;
   unsigned long long a_ptr = 0, b_ptr = 0;
   unsigned a_rec = 0, b_rec = 0;
-  unsigned half0 = 0, half1 = 0;  // kOob in lanes whose chunk is past K (even, odd instructions)
-  unsigned soa[S::NSA], sob[S::NSB];
+  unsigned half0 = 0, half1 = 0;  // kOob in lanes whose piece is past K, by bit 2 of the flip
+  unsigned soff = 0;
 
   auto begin_tile = [&](int t) {
     lt = t;
@@ -248,17 +310,8 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     b_ptr = reinterpret_cast<unsigned long long>(Bl + (size_t)ln0 * rowb);
     a_rec = (unsigned)(ra * rowb);
     b_rec = (unsigned)(rb * rowb);
-    int grp, row;
-#pragma unroll
-    for (int i = 0; i < S::NSA; ++i) {
-      scale_row((wave * S::NSA + i) * 64 + lane, BM, S::TM, SM, grp, row);
-      soa[i] = lm0 + row < Ml ? (unsigned)(grp * Ml + row) * 4u : kOob;
-    }
-#pragma unroll
-    for (int i = 0; i < S::NSB; ++i) {
-      scale_row((wave * S::NSB + i) * 64 + lane, BN, S::TN, SN, grp, row);
-      sob[i] = ln0 + row < Nl ? (unsigned)(grp * Nl + row) * 4u : kOob;
-    }
+    const int sm = of_a ? Ml : Nl, s0 = of_a ? lm0 : ln0;
+    soff = s0 + srow < sm ? (unsigned)(sgrp * sm + srow) * 4u : kOob;
   };
 
   // The next slab's resources; without one they are empty and the loads read
@@ -290,72 +343,77 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     }
     rA = rsrc_words_u64(a_ptr + (unsigned long long)(k0 >> 1), load ? a_rec - (unsigned)(k0 >> 1) : 0u);
     rB = rsrc_words_u64(b_ptr + (unsigned long long)(k0 >> 1), load ? b_rec - (unsigned)(k0 >> 1) : 0u);
-    // the second half of an odd last slab is past K: its chunks are past
+    // the second half of an odd last slab is past K: its pieces are past
     // every range, its scale words (the other group's rows) likewise
     const bool odd = k0 + 128 >= Kl;
-    const unsigned hi0 = (chunk0 & 4u) ? kOob : 0u;
+    const unsigned hi0 = (lane & 4) ? kOob : 0u;
     half0 = odd ? hi0 : 0u;
     half1 = odd ? hi0 ^ kOob : 0u;
     const int grp = k0 >> 7, ng = odd ? 1 : 2;
-    rSA = rsrc_words_u64(reinterpret_cast<unsigned long long>(SAl + ((size_t)grp * Ml + lm0) * 4),
-                         load ? (unsigned)(ng * Ml - lm0) * 4u : 0u);
-    rSB = rsrc_words_u64(reinterpret_cast<unsigned long long>(SBl + ((size_t)grp * Nl + ln0) * 4),
-                         load ? (unsigned)(ng * Nl - ln0) * 4u : 0u);
+    const int sm = of_a ? Ml : Nl, s0 = of_a ? lm0 : ln0;
+    rS = rsrc_words_u64(reinterpret_cast<unsigned long long>((of_a ? SAl : SBl) + ((size_t)grp * sm + s0) * 4),
+                        load ? (unsigned)(ng * sm - s0) * 4u : 0u);
   };
 
   auto dma = [&](int st, int d) PGK_INLINE {
     const unsigned sb = lds0 + (unsigned)(st * S::STAGE);
     if (d < NA) {
-      const unsigned ch = (d & 1) ? (chunk0 ^ 4u) : chunk0;
+      const unsigned flip = piece_flip<SM>(d) * 16u;
       load_lds16(rA, sb + (unsigned)((wave * NA + d) * 1024),
-                 (aoff + (unsigned)d * astep + ch * 16u) | ((d & 1) ? half1 : half0));
+                 (aoff + (unsigned)d * 8u * rowb + (apiece ^ flip)) | ((flip & 64u) ? half1 : half0));
     } else if (d < NO) {
       const int e = d - NA;
-      const unsigned ch = (e & 1) ? (chunk0 ^ 4u) : chunk0;
+      const unsigned flip = piece_flip<SN>(e) * 16u;
       load_lds16(rB, sb + (unsigned)(S::A_BYTES + (wave * NB + e) * 1024),
-                 (boff + (unsigned)e * astep + ch * 16u) | ((e & 1) ? half1 : half0));
-    } else if (d < NO + S::NSA) {
-      load_lds4(rSA, sb + (unsigned)(S::A_BYTES + S::B_BYTES + (wave * S::NSA + d - NO) * 256), soa[d - NO]);
+                 (boff + (unsigned)e * 8u * rowb + (bpiece ^ flip)) | ((flip & 64u) ? half1 : half0));
     } else {
-      const int e = d - NO - S::NSA;
-      load_lds4(rSB, sb + (unsigned)(S::A_BYTES + S::B_BYTES + S::SA_BYTES + (wave * S::NSB + e) * 256), sob[e]);
+      load_lds16(rS, sb + slds, soff);
     }
   };
 
-  f32x4 acc[SN][SM];
-  i32x4 aq[2][SM], bq[2][SN];               // fragments, by step
-  u32x4 wa[2][SM / 4], wb[2][SN / 4];       // scale words, by step
-  int sa[SM / 4], sb[SN / 4];               // gathered scale bytes of the step on the matrix cores
+  f32x16 acc[SN][SM];
+  i32x4 aq[2][2][SM], bq[2][2][SN];  // fragments, by step and half
+  typedef typename Words<SM>::type wa_t;
+  typedef typename Words<SN>::type wb_t;
+  wa_t wa[2];  // scale words, by step
+  wb_t wb[2];
+  int sa[2], sb[2];  // gathered scale bytes of the step on the matrix cores, by half
 
-  // LDS read r of step s: scale words, then B block 0, the A blocks, the other
-  // B blocks (the order the MFMAs consume them).
+  // LDS read r of step s: scale words, then for each half B block 0, the A
+  // blocks, the other B blocks (the order the MFMAs consume them).
   auto read = [&](int st, int s, int r) PGK_INLINE {
     const unsigned char* p = smem + st * S::STAGE;
-    constexpr int NW = SM / 4 + SN / 4;
-    if (r < SM / 4) {
-      wa[s][r] = *reinterpret_cast<const u32x4*>(p + rd_sa + s * BM * 4 + r * 16);
-    } else if (r < NW) {
-      wb[s][r - SM / 4] = *reinterpret_cast<const u32x4*>(p + rd_sb + s * BN * 4 + (r - SM / 4) * 16);
-    } else if (r == NW) {
-      bq[s][0] = *reinterpret_cast<const i32x4*>(p + rd_b[s]);
-    } else if (r <= NW + SM) {
-      aq[s][r - NW - 1] = *reinterpret_cast<const i32x4*>(p + rd_a[s] + (r - NW - 1) * 2048);
+    if (r == 0) {
+      wa[s] = *reinterpret_cast<const wa_t*>(p + rd_sa + s * BM * 4);
+    } else if (r == 1) {
+      wb[s] = *reinterpret_cast<const wb_t*>(p + rd_sb + s * BN * 4);
     } else {
-      bq[s][r - NW - SM] = *reinterpret_cast<const i32x4*>(p + rd_b[s] + (r - NW - SM) * 2048);
+      const int u = (r - 2) / (SM + SN), e = (r - 2) % (SM + SN);
+      if (e == 0)
+        bq[s][u][0] = *reinterpret_cast<const i32x4*>(p + rd_b[s][u]);
+      else if (e <= SM)
+        aq[s][u][e - 1] = *reinterpret_cast<const i32x4*>(p + rd_a[s][u] + (e - 1) * (1024 / SM));
+      else
+        bq[s][u][e - SM] = *reinterpret_cast<const i32x4*>(p + rd_b[s][u] + (e - SM) * (1024 / SN));
     }
   };
-  auto gather = [&](u32x4 w) {
-    return (int)(__builtin_amdgcn_perm(w[1], w[0], sel_lo) | __builtin_amdgcn_perm(w[3], w[2], sel_hi));
+  // byte kb + 2 u of each word (one per block)
+  auto gather = [&](auto w, int u) {
+    const unsigned d = 0x0202u * (unsigned)u;
+    unsigned o = __builtin_amdgcn_perm(w[1], w[0], sel_lo + d);
+    if constexpr (sizeof(w) == 16) o |= __builtin_amdgcn_perm(w[3], w[2], sel_hi + (d << 16));
+    return (int)o;
   };
   auto scales = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < SM / 4; ++i) sa[i] = gather(wa[s][i]);
-#pragma unroll
-    for (int i = 0; i < SN / 4; ++i) sb[i] = gather(wb[s][i]);
+    for (int u = 0; u < 2; ++u) {
+      sa[u] = gather(wa[s], u);
+      sb[u] = gather(wb[s], u);
+    }
   };
   auto mfma = [&](auto sc, auto jc) PGK_INLINE {
-    constexpr int s = sc, sn = jc / SM, sm = jc % SM;
-    acc[sn][sm] = mfma_scaled<sn % 4, sm % 4>(bq[s][sn], aq[s][sm], acc[sn][sm], sb[sn / 4], sa[sm / 4]);
+    constexpr int s = sc, u = jc / (SM * SN), sn = jc / SM % SN, sm = jc % SM;
+    acc[sn][sm] = mfma_scaled32<sm, sn>(aq[s][u][sm], bq[s][u][sn], acc[sn][sm], sa[u], sb[u]);
   };
   // Step s on the matrix cores; the other step's reads (of stage st_rd) and
   // the loads that fall on this half of the period.
@@ -373,31 +431,36 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     });
   };
 
-  auto epilogue = [&](int m0, int n0) {
-    const int64_t N = Nc;
-    const int mb = m0 + wm * S::TM + l16, nb = n0 + wn * S::TN;
+  // Lane l holds SN consecutive columns, l % 32 * SN of the wave's, one per
+  // block; registers 4 g + e hold rows (8 g + 4 (l / 32) + e) * SM + block: a
+  // store of the wave covers two rows' 32 * SN consecutive columns.
+  auto put_tile = [&](int m0, int n0, auto out, auto edge) {
+    typedef decltype(out) T;
+    const int64_t n = n0 + wn * S::TN + l32 * SN;
+    const int m = m0 + wm * S::TM + 4 * kb * SM;
+    T* base = static_cast<T*>(Cc) + (int64_t)m * Nc + n;
 #pragma unroll
-    for (int i = 0; i < SM; ++i) {
-      const int m = mb + i * 16;
-      if (m >= Mc) continue;
-      if (P.out_f32) {
-        float* row = static_cast<float*>(Cc) + (int64_t)m * N;
+    for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int j = 0; j < SN; ++j) store_f32x4(row, nb + j * 16 + 4 * kb, N, acc[j][i]);
-      } else {
-        unsigned short* row = static_cast<unsigned short*>(Cc) + (int64_t)m * N;
-        // Two neighbouring blocks at a time: v_permlane16_swap trades the odd
-        // 16-lane rows of one for the even rows of the other, which leaves each
-        // lane eight consecutive columns.
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < SN; j += 2) {
-          const f32x4 a = acc[j][i], b = acc[j + 1][i];
-          const auto s0 = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[0], a[1]), pack_bf16x2(b[0], b[1]), false, false);
-          const auto s1 = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[2], a[3]), pack_bf16x2(b[2], b[3]), false, false);
-          store_bf16x8(row, nb + (j + (kb & 1)) * 16 + 4 * (kb & 2), N, u32x4{s0[0], s1[0], s0[1], s1[1]});
+        for (int i = 0; i < SM; ++i) {
+          const int r = (8 * g + e) * SM + i;
+          if (edge && m + r >= Mc) continue;
+          float v[SN];
+#pragma unroll
+          for (int j = 0; j < SN; ++j) v[j] = acc_read(acc[j][i][4 * g + e]);
+          store_row<SN>(base + (int64_t)r * Nc, v, edge ? (int64_t)Nc - n : (int64_t)SN);
         }
-      }
-    }
+  };
+  auto epilogue = [&](int m0, int n0) {
+    const bool edge = m0 + BM > Mc || n0 + BN > Nc;
+    const std::integral_constant<bool, true> yes;
+    const std::integral_constant<bool, false> no;
+    if (P.out_f32)
+      edge ? put_tile(m0, n0, 0.0f, yes) : put_tile(m0, n0, 0.0f, no);
+    else
+      edge ? put_tile(m0, n0, (unsigned short)0, yes) : put_tile(m0, n0, (unsigned short)0, no);
   };
 
   if (tid == 0) s_first[0] = walker.first();
@@ -449,7 +512,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
 #pragma unroll
     for (int j = 0; j < SN; ++j)
 #pragma unroll
-      for (int i = 0; i < SM; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < SM; ++i) acc[j][i] = f32x16{};
     // A period per slab: the barrier, step 1 of the slab before (fragments in
     // registers) while step 0 of this one is read, then step 0 while step 1 is
     // read.  The tile's first slab has no step before it.
@@ -483,12 +546,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
       ++g;
     }
     static_for<NMF>([&](auto jc) PGK_INLINE { mfma(step1, jc); });
-    // all of them before the epilogue's branches, whose blocks they would
-    // otherwise move into, each wait then for one block's results
-#pragma unroll
-    for (int j = 0; j < SN; ++j)
-#pragma unroll
-      for (int i = 0; i < SM; ++i) asm volatile("" : "+a"(acc[j][i]));
+    mfma_results_ready();
     epilogue(m0, n0);
     ++it;
     ct = pend[0];
