@@ -86,14 +86,27 @@ def gemm_bytes(M: int, N: int, K: int, dtype) -> dict:
     return out
 
 
+# torch is imported by the first call that needs it; a short call would spend
+# as long on import statements as on its checks.
+_TENSOR = None
+_RAW_STREAM = None
+
+
+def _tensor_type():
+    global _TENSOR, _RAW_STREAM
+    import torch
+    _RAW_STREAM = torch._C._cuda_getCurrentRawStream
+    _TENSOR = torch.Tensor
+    return _TENSOR
+
+
 def _check_tensor(x, what, dtypes=None, nbytes=None):
     """Layout, element type and extent of a tensor argument (host-side checks,
     before any device is involved).  Raw int pointers pass unchecked: the
     library itself checks that every range lies inside one device allocation."""
     if isinstance(x, int):
         return
-    import torch
-    if not isinstance(x, torch.Tensor):
+    if not isinstance(x, _TENSOR or _tensor_type()):
         raise TypeError(f"{what}: expected a torch tensor or an int device pointer")
     if not x.is_contiguous():
         raise ValueError(f"{what}: tensor must be contiguous (row-major)")
@@ -101,8 +114,8 @@ def _check_tensor(x, what, dtypes=None, nbytes=None):
         allowed = _torch_dtypes(dtypes)
         if x.dtype not in allowed:
             raise ValueError(f"{what}: dtype {x.dtype} not in {allowed}")
-    if nbytes is not None and x.numel() * x.element_size() < nbytes:
-        raise ValueError(f"{what}: tensor holds {x.numel() * x.element_size()} bytes, "
+    if nbytes is not None and x.nbytes < nbytes:
+        raise ValueError(f"{what}: tensor holds {x.nbytes} bytes, "
                          f"the call reads or writes {nbytes}")
 
 
@@ -126,9 +139,11 @@ def _stream(stream, device=None):
     """Raw HIP stream handle: `stream` itself (an int or a torch stream), else
     torch's current stream on `device` (the config's device)."""
     if stream is None:
-        import torch
         if device is not None:
-            return torch._C._cuda_getCurrentRawStream(device)
+            if _RAW_STREAM is None:
+                _tensor_type()
+            return _RAW_STREAM(device)
+        import torch
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -152,17 +167,25 @@ def make_args(tile=None, group_size=0, grid=0, claim_chunk=0, a_scale=None, b_sc
               debug_flags=0, straggler_program=-1, straggler_ns=0, pipeline="default",
               program_order="default"):
     a = _abi.pgemm_args()
+    # a new structure holds zeros; a field costs as much to set as a check
     if tile is not None:
         a.tile_m, a.tile_n, a.tile_k = (tuple(tile) + (0,))[:3]
-    a.group_size = group_size
-    a.grid = grid
-    a.claim_chunk = claim_chunk
-    a.a_scale = _ptr(a_scale, "a_scale", _SCALE) if a_scale is not None else None
-    a.b_scale = _ptr(b_scale, "b_scale", _SCALE) if b_scale is not None else None
+    if group_size:
+        a.group_size = group_size
+    if grid:
+        a.grid = grid
+    if claim_chunk:
+        a.claim_chunk = claim_chunk
+    if a_scale is not None:
+        a.a_scale = _ptr(a_scale, "a_scale", _SCALE)
+    if b_scale is not None:
+        a.b_scale = _ptr(b_scale, "b_scale", _SCALE)
     a._scales = (a_scale, b_scale)  # checked against M, N, K when the call is made
-    a.debug_flags = debug_flags
+    if debug_flags:
+        a.debug_flags = debug_flags
     a.straggler_program = straggler_program
-    a.straggler_ns = straggler_ns
+    if straggler_ns:
+        a.straggler_ns = straggler_ns
     a.pipeline = PIPELINES[pipeline] if isinstance(pipeline, str) else int(pipeline)
     a.program_order = ORDERS[program_order] if isinstance(program_order, str) else int(program_order)
     return a
@@ -379,11 +402,12 @@ def _matrix(x, what, rows, cols, ld=None):
     pointer with its row stride `ld`."""
     if isinstance(x, int):
         return x, int(cols if ld is None else ld)
-    import torch
-    if not isinstance(x, torch.Tensor):
+    if not isinstance(x, _TENSOR or _tensor_type()):
         raise TypeError(f"{what}: expected a torch tensor or an int device pointer")
-    if ld is None and x.dim() == 2 and tuple(x.shape) == (rows, cols) and (x.stride(1) == 1 or cols == 1):
-        return _dev(x, what), int(x.stride(0)) if rows > 1 else cols
+    if ld is None and x.shape == (rows, cols):
+        step = x.stride()
+        if step[1] == 1 or cols == 1:
+            return _dev(x, what), step[0] if rows > 1 else cols
     ld = cols if ld is None else int(ld)
     need = ((rows - 1) * ld + cols if rows else 0) * x.element_size()
     _check_tensor(x, what, None, need)

@@ -192,7 +192,7 @@ int padd_tiles_per_step(int tr, int tc);
 bool gemm_fp4_tile_supported(int bm, int bn, int bk);
 bool gemm_fp4_eligible(int bm, int bn, long long M, long long N, long long K);
 void gemm_fp4_default_tile(long long M, long long N, long long K, int cus, int& bm, int& bn, int& bk);
-hipError_t launch_gemm_fp4(const GemmParams& p, int bm, int bn, hipStream_t stream);
+hipError_t launch_gemm_fp4(const GemmParams& p, int bm, int bn, bool few, hipStream_t stream);
 
 // Launch shape of a kernel instance: threads and dynamic LDS per workgroup,
 // and how many such workgroups one CU holds at once (registers, LDS, waves).
@@ -216,7 +216,8 @@ KernelInfo info_gemm_bf16_lds(int bm, int bn, bool out_bf16);
 KernelInfo info_gemm_bf16_pp(bool out_bf16);
 hipError_t launch_gemm_bf16_pp(const GemmParams& p, bool out_bf16, bool witness, hipStream_t stream);
 KernelInfo info_gemm_fp8(int bm, int bn);
-KernelInfo info_gemm_fp4(int bm, int bn, bool grouped);
+// few: at most one tile per CU (another ring depth at some tiles)
+KernelInfo info_gemm_fp4(int bm, int bn, bool few, bool grouped);
 KernelInfo info_padd(int tr, int tc, bool vec);
 
 // Resident workgroups per CU of `kern` (at least 1), after raising its

@@ -15,6 +15,7 @@
 //  * gemm_fp4_skinny_kernel for up to 64 rows: bound by the bytes of B, which
 //    each wave streams straight into registers; the waves of a workgroup split
 //    K and add their sums in LDS.
+#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -32,7 +33,6 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256;
 constexpr int kFmtE2M1 = 4;  // f8f6f4 operand format code of e2m1
 constexpr int kMaxWaves = 8;  // of a workgroup of the kernel for few rows
 constexpr int BK = 256;      // k per slab: 128 bytes of a row, two scale groups
@@ -128,19 +128,19 @@ __device__ __forceinline__ void store_row(unsigned short* p, const float (&v)[W]
 // four blocks' words with one ds_read_b128 and gathers its own byte of each
 // into one register (v_perm), from which the MFMA selects by opsel.  Byte
 // reads per block would be four times the LDS instructions.
-template <int BM, int BN, int NST_>
+template <int BM, int BN, int NST_, int WN_>
 struct Shape {
   static constexpr int NST = NST_;
-  static constexpr int TM = BM / 2, TN = BN / 2;
+  static constexpr int WN = WN_, WAVES = 2 * WN;  // 2 x WN waves
+  static constexpr int TM = BM / 2, TN = BN / WN;
   static constexpr int SM = TM / 32, SN = TN / 32;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int SA_BYTES = BM * 8, SB_BYTES = BN * 8;  // two groups of words
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-  static constexpr int LDS_BYTES = NST * STAGE + 16;  // + first tile, next tile [2]
-  static constexpr int NA = BM / 32, NB = BN / 32;    // 1 KB operand loads per wave per slab
+  static constexpr int LDS_BYTES = NST * STAGE + 16 + (WAVES > 4 ? 1024 : 0);  // + first tile, next tile [2]
+  static constexpr int NA = BM / 8 / WAVES, NB = BN / 8 / WAVES;  // 1 KB operand loads per wave per slab
   static constexpr int NL = NA + NB + 1;              // + one 1 KB load of scale words
-  static constexpr int NMF = 2 * SM * SN;             // MFMAs per 128-deep step
-  static constexpr int NRD = 2 * SM + 2 * SN + 2;     // LDS reads per 128-deep step
+  static constexpr int NMF = SM * SN;                 // MFMAs per 64-deep step
   static_assert((SM == 2 || SM == 4) && (SN == 2 || SN == 4), "a row's scale words in one LDS read");
   static_assert(BM % 128 == 0 && BN % 128 == 0 && NA % 2 == 0 && NB % 2 == 0, "whole loads per wave");
 };
@@ -175,15 +175,14 @@ struct Words<2> {
   typedef u32x2 type;
 };
 
-template <int BM, int BN, int NST, bool GRP>
-__global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
-  using S = Shape<BM, BN, NST>;
-  constexpr int NA = S::NA, NB = S::NB, NO = NA + NB, NL = S::NL, NMF = S::NMF, NRD = S::NRD;
+template <int BM, int BN, int NST, int WN, bool GRP>
+__global__ void __launch_bounds__(128 * WN) gemm_fp4_kernel(GemmParams P) {
+  using S = Shape<BM, BN, NST, WN>;
+  constexpr int NA = S::NA, NB = S::NB, NO = NA + NB, NL = S::NL, NMF = S::NMF;
   constexpr int SM = S::SM, SN = S::SN;
-  // Of a period's 2 * NMF MFMA positions, the loads take the first SPREAD, and
-  // the next step's LDS reads the first RSPREAD of each step's.
-  constexpr int SPREAD = NST > 2 ? 2 * NMF : NMF;
-  constexpr int RSPREAD = NRD > NMF * 3 / 4 ? NMF : NMF * 3 / 4;
+  // Of a period's 4 * NMF MFMA positions, the loads take the first SPREAD: half
+  // of them where the ring's second stage has to have landed by the next period.
+  constexpr int SPREAD = NST > 2 ? 4 * NMF : 2 * NMF;
 
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   int* s_first = reinterpret_cast<int*>(smem + NST * S::STAGE);
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   const int l32 = lane & 31, kb = lane >> 5;
   const int prog = pgs::program_of(blockIdx.x, P.s.G, P.s.X, P.s.xcd_major);
   // the loader tile's problem and the matrix cores' tile's problem
@@ -225,29 +224,31 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   };
   lane_offsets(Kl);
   // 16-byte piece of the lane in instruction 0, in bytes; d flips bits of it
-  const unsigned apiece = (unsigned)((lane & 7) ^ (SM == 2 ? r8 >> 1 & 1 : 0)) * 16u;
-  const unsigned bpiece = (unsigned)((lane & 7) ^ (SN == 2 ? r8 >> 1 & 1 : 0)) * 16u;
+  const unsigned apiece = ((unsigned)((lane & 7) ^ (SM == 2 ? r8 >> 1 & 1 : 0)) ^ piece_flip<SM>(wave * NA)) * 16u;
+  const unsigned bpiece = ((unsigned)((lane & 7) ^ (SN == 2 ? r8 >> 1 & 1 : 0)) ^ piece_flip<SN>(wave * NB)) * 16u;
   // Scale words, four rows of one group per lane: waves 0 and 1 A's, 2 and 3
-  // B's.  256 rows: a group each; 128 rows: both groups, twice the same.
+  // B's; waves past them, which issue the same instruction, nothing, into a
+  // kilobyte of their own.  256 rows: a group each; 128 rows: both groups, twice the same.
   const bool of_a = wave < 2;
   const int srows = of_a ? BM : BN;
   const int sgrp = srows == 256 ? (wave & 1) : (lane >> 5);
   const int srow = (srows == 256 ? lane : (lane & 31)) * 4;
-  const unsigned slds = (unsigned)(S::A_BYTES + S::B_BYTES + (of_a ? 0 : S::SA_BYTES) +
-                                   (srows == 256 ? (wave & 1) * 1024 : 0));
+  const unsigned slds = wave >= 4 ? (unsigned)(NST * S::STAGE + 16)
+                                  : (unsigned)(S::A_BYTES + S::B_BYTES + (of_a ? 0 : S::SA_BYTES) +
+                                               (srows == 256 ? (wave & 1) * 1024 : 0));
   const unsigned lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
 
-  // LDS reads: step s, half u: piece 4 s + 2 u + kb of row l32 of a block.
-  unsigned rd_a[2][2], rd_b[2][2];
+  // LDS reads: step h: piece 2 h + kb of row l32 of a block.
+  unsigned rd_a[4], rd_b[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const unsigned c = (unsigned)((2 * q + kb) ^ (l32 >> 1 & 7)) * 16u;
-    rd_a[q >> 1][q & 1] = (unsigned)(wm * S::TM * 128 + row_slot<SM>(l32)) + c;
-    rd_b[q >> 1][q & 1] = (unsigned)(S::A_BYTES + wn * S::TN * 128 + row_slot<SN>(l32)) + c;
+    rd_a[q] = (unsigned)(wm * S::TM * 128 + row_slot<SM>(l32)) + c;
+    rd_b[q] = (unsigned)(S::A_BYTES + wn * S::TN * 128 + row_slot<SN>(l32)) + c;
   }
   const unsigned rd_sa = (unsigned)(S::A_BYTES + S::B_BYTES + (wm * S::TM + l32 * SM) * 4);
   const unsigned rd_sb = (unsigned)(S::A_BYTES + S::B_BYTES + S::SA_BYTES + (wn * S::TN + l32 * SN) * 4);
-  // v_perm selectors: byte kb (half 1: kb + 2) of two words into the low or
+  // v_perm selectors: byte kb (odd steps: kb + 2) of two words into the low or
   // the high half
   const unsigned sel_lo = 0x0c0c0400u + 0x0101u * (unsigned)kb;
   const unsigned sel_hi = 0x04000c0cu + 0x01010000u * (unsigned)kb;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   rsrc_words_t rA, rB, rS;
   unsigned long long a_ptr = 0, b_ptr = 0;
   unsigned a_rec = 0, b_rec = 0;
-  unsigned half0 = 0, half1 = 0;  // kOob in lanes whose piece is past K, by bit 2 of the flip
+  unsigned ahalf = 0, bhalf = 0, hflip = 0;  // kOob in lanes whose piece is past K (instruction 0; flipped)
   unsigned soff = 0;
 
   auto begin_tile = [&](int t) {
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     a_rec = (unsigned)(ra * rowb);
     b_rec = (unsigned)(rb * rowb);
     const int sm = of_a ? Ml : Nl, s0 = of_a ? lm0 : ln0;
-    soff = s0 + srow < sm ? (unsigned)(sgrp * sm + srow) * 4u : kOob;
+    soff = wave < 4 && s0 + srow < sm ? (unsigned)(sgrp * sm + srow) * 4u : kOob;
   };
 
   // The next slab's resources; without one they are empty and the loads read
@@ -346,9 +347,9 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     // the second half of an odd last slab is past K: its pieces are past
     // every range, its scale words (the other group's rows) likewise
     const bool odd = k0 + 128 >= Kl;
-    const unsigned hi0 = (lane & 4) ? kOob : 0u;
-    half0 = odd ? hi0 : 0u;
-    half1 = odd ? hi0 ^ kOob : 0u;
+    hflip = odd ? kOob : 0u;
+    ahalf = (apiece & 64u) ? hflip : 0u;
+    bhalf = (bpiece & 64u) ? hflip : 0u;
     const int grp = k0 >> 7, ng = odd ? 1 : 2;
     const int sm = of_a ? Ml : Nl, s0 = of_a ? lm0 : ln0;
     rS = rsrc_words_u64(reinterpret_cast<unsigned long long>((of_a ? SAl : SBl) + ((size_t)grp * sm + s0) * 4),
@@ -360,42 +361,40 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     if (d < NA) {
       const unsigned flip = piece_flip<SM>(d) * 16u;
       load_lds16(rA, sb + (unsigned)((wave * NA + d) * 1024),
-                 (aoff + (unsigned)d * 8u * rowb + (apiece ^ flip)) | ((flip & 64u) ? half1 : half0));
+                 (aoff + (unsigned)d * 8u * rowb + (apiece ^ flip)) | ((flip & 64u) ? ahalf ^ hflip : ahalf));
     } else if (d < NO) {
       const int e = d - NA;
       const unsigned flip = piece_flip<SN>(e) * 16u;
       load_lds16(rB, sb + (unsigned)(S::A_BYTES + (wave * NB + e) * 1024),
-                 (boff + (unsigned)e * 8u * rowb + (bpiece ^ flip)) | ((flip & 64u) ? half1 : half0));
+                 (boff + (unsigned)e * 8u * rowb + (bpiece ^ flip)) | ((flip & 64u) ? bhalf ^ hflip : bhalf));
     } else {
-      load_lds16(rS, sb + slds, soff);
+      load_lds16(rS, (wave < 4 ? sb : lds0) + slds, soff);
     }
   };
 
   f32x16 acc[SN][SM];
-  i32x4 aq[2][2][SM], bq[2][2][SN];  // fragments, by step and half
+  i32x4 aq[2][SM], bq[2][SN];  // fragments, by the step's parity
   typedef typename Words<SM>::type wa_t;
   typedef typename Words<SN>::type wb_t;
-  wa_t wa[2];  // scale words, by step
-  wb_t wb[2];
-  int sa[2], sb[2];  // gathered scale bytes of the step on the matrix cores, by half
+  wa_t wa;  // scale words of a group: two steps
+  wb_t wb;
+  int sa = 0, sb = 0;  // gathered scale bytes of the step on the matrix cores
 
-  // LDS read r of step s: scale words, then for each half B block 0, the A
-  // blocks, the other B blocks (the order the MFMAs consume them).
-  auto read = [&](int st, int s, int r) PGK_INLINE {
+  // LDS read r of step h: B block 0, the A blocks, the other B blocks (the
+  // order the MFMAs consume them); even steps the scale words too.
+  auto reads = [](int h) { return SM + SN + (h % 2 == 0 ? 2 : 0); };
+  auto read = [&](int st, int h, int r) PGK_INLINE {
     const unsigned char* p = smem + st * S::STAGE;
-    if (r == 0) {
-      wa[s] = *reinterpret_cast<const wa_t*>(p + rd_sa + s * BM * 4);
-    } else if (r == 1) {
-      wb[s] = *reinterpret_cast<const wb_t*>(p + rd_sb + s * BN * 4);
-    } else {
-      const int u = (r - 2) / (SM + SN), e = (r - 2) % (SM + SN);
-      if (e == 0)
-        bq[s][u][0] = *reinterpret_cast<const i32x4*>(p + rd_b[s][u]);
-      else if (e <= SM)
-        aq[s][u][e - 1] = *reinterpret_cast<const i32x4*>(p + rd_a[s][u] + (e - 1) * (1024 / SM));
-      else
-        bq[s][u][e - SM] = *reinterpret_cast<const i32x4*>(p + rd_b[s][u] + (e - SM) * (1024 / SN));
-    }
+    if (r == 0)
+      bq[h & 1][0] = *reinterpret_cast<const i32x4*>(p + rd_b[h]);
+    else if (r <= SM)
+      aq[h & 1][r - 1] = *reinterpret_cast<const i32x4*>(p + rd_a[h] + (r - 1) * (1024 / SM));
+    else if (r < SM + SN)
+      bq[h & 1][r - SM] = *reinterpret_cast<const i32x4*>(p + rd_b[h] + (r - SM) * (1024 / SN));
+    else if (r == SM + SN)
+      wa = *reinterpret_cast<const wa_t*>(p + rd_sa + (h >> 1) * BM * 4);
+    else
+      wb = *reinterpret_cast<const wb_t*>(p + rd_sb + (h >> 1) * BN * 4);
   };
   // byte kb + 2 u of each word (one per block)
   auto gather = [&](auto w, int u) {
@@ -404,28 +403,28 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     if constexpr (sizeof(w) == 16) o |= __builtin_amdgcn_perm(w[3], w[2], sel_hi + (d << 16));
     return (int)o;
   };
-  auto scales = [&](int s) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      sa[u] = gather(wa[s], u);
-      sb[u] = gather(wb[s], u);
-    }
+  auto scales = [&](int h) {
+    sa = gather(wa, h & 1);
+    sb = gather(wb, h & 1);
   };
-  auto mfma = [&](auto sc, auto jc) PGK_INLINE {
-    constexpr int s = sc, u = jc / (SM * SN), sn = jc / SM % SN, sm = jc % SM;
-    acc[sn][sm] = mfma_scaled32<sm, sn>(aq[s][u][sm], bq[s][u][sn], acc[sn][sm], sa[u], sb[u]);
+  auto mfma = [&](auto hc, auto jc) PGK_INLINE {
+    constexpr int b = hc & 1, sn = jc / SM, sm = jc % SM;
+    acc[sn][sm] = mfma_scaled32<sm, sn>(aq[b][sm], bq[b][sn], acc[sn][sm], sa, sb);
   };
-  // Step s on the matrix cores; the other step's reads (of stage st_rd) and
-  // the loads that fall on this half of the period.
-  auto step = [&](auto sc, int st_rd, int st_dma) PGK_INLINE {
+  // Step h on the matrix cores (of a period that runs steps 3, 0, 1, 2); the
+  // next step's reads (of stage st_rd) and the loads that fall on this quarter
+  // of the period.
+  auto step = [&](auto hc, int st_rd, int st_dma) PGK_INLINE {
+    scales(hc);
+    __builtin_amdgcn_sched_barrier(0);
     static_for<NMF>([&](auto jc) PGK_INLINE {
-      constexpr int s = sc, j = jc;
-      mfma(sc, jc);
-      static_for<NRD>([&](auto rc) PGK_INLINE {
-        if constexpr (rc * RSPREAD / NRD == j) read(st_rd, s ^ 1, rc);
+      constexpr int h = hc, j = jc, nx = (h + 1) % 4, nr = SM + SN + (nx % 2 == 0 ? 2 : 0);
+      mfma(hc, jc);
+      static_for<nr>([&](auto rc) PGK_INLINE {
+        if constexpr (rc * NMF / nr == j) read(st_rd, nx, rc);
       });
       static_for<NL>([&](auto dc) PGK_INLINE {
-        if constexpr (dc * SPREAD / NL == (s == 1 ? j : NMF + j)) dma(st_dma, dc);
+        if constexpr (dc * SPREAD / NL == nx * NMF + j) dma(st_dma, dc);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -500,6 +499,8 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
   };
   const std::integral_constant<int, 0> step0;
   const std::integral_constant<int, 1> step1;
+  const std::integral_constant<int, 2> step2;
+  const std::integral_constant<int, 3> step3;
   while (ct >= 0) {
     if (tid == 0) {
       if (witness) {
@@ -513,23 +514,22 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
     for (int j = 0; j < SN; ++j)
 #pragma unroll
       for (int i = 0; i < SM; ++i) acc[j][i] = f32x16{};
-    // A period per slab: the barrier, step 1 of the slab before (fragments in
-    // registers) while step 0 of this one is read, then step 0 while step 1 is
-    // read.  The tile's first slab has no step before it.
+    // A period per slab: the barrier, step 3 of the slab before (fragments in
+    // registers) while step 0 of this one is read, then steps 0 to 2, each
+    // while the next is read.  The tile's first slab has no step before it.
     {
       slab_start();
       const int st = g % NST, st_dma = st == 0 ? NST - 1 : st - 1;
 #pragma unroll
-      for (int r = 0; r < NRD; ++r) read(st, 0, r);
+      for (int r = 0; r < reads(0); ++r) read(st, 0, r);
       __builtin_amdgcn_sched_barrier(0);
       prep();
 #pragma unroll
       for (int d = 0; d < NL; ++d)
         if (d * SPREAD / NL < NMF) dma(st_dma, d);
-      scales(0);
-      __builtin_amdgcn_sched_barrier(0);
       step(step0, st, st_dma);
-      scales(1);
+      step(step1, st, st_dma);
+      step(step2, st, st_dma);
       ++g;
     }
     for (int ck = 1; ck < cnk; ++ck) {
@@ -537,15 +537,14 @@ __global__ void __launch_bounds__(kThreads) gemm_fp4_kernel(GemmParams P) {
       const int st = g % NST, st_dma = st == 0 ? NST - 1 : st - 1;
       prep();
       __builtin_amdgcn_sched_barrier(0);
-      step(step1, st, st_dma);
-      scales(0);
-      __builtin_amdgcn_sched_barrier(0);
+      step(step3, st, st_dma);
       step(step0, st, st_dma);
-      scales(1);
-      __builtin_amdgcn_sched_barrier(0);
+      step(step1, st, st_dma);
+      step(step2, st, st_dma);
       ++g;
     }
-    static_for<NMF>([&](auto jc) PGK_INLINE { mfma(step1, jc); });
+    scales(3);
+    static_for<NMF>([&](auto jc) PGK_INLINE { mfma(step3, jc); });
     mfma_results_ready();
     epilogue(m0, n0);
     ++it;
@@ -718,17 +717,22 @@ __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmPar
 
 // --------------------------------------------------------------- instances
 
+constexpr int kDevices = 64;
+
 // A built tile: its kernels (one problem, several), threads and LDS.
 struct Instance {
   int bm, bn;
   int threads, lds;
   void (*kern[2])(GemmParams);
+  // resident workgroups per CU, by kernel and device; 0: not asked for yet (the
+  // question and the LDS limit it sets cost microseconds of a short call)
+  mutable std::atomic<int> resident[2][kDevices] = {};
 };
 
-template <int BM, int BN, int NST>
+template <int BM, int BN, int NST, int WN>
 Instance tiled() {
-  return {BM, BN, kThreads, Shape<BM, BN, NST>::LDS_BYTES,
-          {gemm_fp4_kernel<BM, BN, NST, false>, gemm_fp4_kernel<BM, BN, NST, true>}};
+  return {BM, BN, 128 * WN, Shape<BM, BN, NST, WN>::LDS_BYTES,
+          {gemm_fp4_kernel<BM, BN, NST, WN, false>, gemm_fp4_kernel<BM, BN, NST, WN, true>}};
 }
 template <int SM, int SN, int DEPTH>
 Instance skinny(int waves) {
@@ -736,11 +740,17 @@ Instance skinny(int waves) {
           {gemm_fp4_skinny_kernel<SM, SN, DEPTH, false>, gemm_fp4_skinny_kernel<SM, SN, DEPTH, true>}};
 }
 
-const Instance* instance(int bm, int bn) {
+const Instance* instance(int bm, int bn, bool few) {
   static const Instance all[] = {
-      tiled<256, 256, 2>(), tiled<256, 128, 3>(), tiled<128, 128, 2>(),
-      skinny<1, 1, 4>(8),   skinny<1, 2, 4>(4),   skinny<2, 2, 2>(4),   skinny<4, 2, 2>(4),
+      tiled<256, 256, 2, 4>(), tiled<256, 128, 3, 2>(), tiled<128, 128, 2, 2>(),
+      skinny<1, 1, 4>(8),      skinny<1, 2, 4>(4),      skinny<2, 2, 2>(4),       skinny<4, 2, 2>(4),
   };
+  // At most one tile per CU: no second workgroup there covers the waits for
+  // memory of a two-stage ring (512 x 8192 x 8192 33.1 -> 26.6 us, 128 x 28672 x
+  // 8192 47.1 -> 36.8; with several tiles per CU two workgroups are faster, 8192^3
+  // 340 against 360 us).
+  static const Instance deep = tiled<128, 128, 3, 2>();
+  if (few && bm == deep.bm && bn == deep.bn) return &deep;
   for (const Instance& i : all)
     if (i.bm == bm && i.bn == bn) return &i;
   return nullptr;
@@ -748,7 +758,7 @@ const Instance* instance(int bm, int bn) {
 
 }  // namespace
 
-bool gemm_fp4_tile_supported(int bm, int bn, int bk) { return bk == BK && instance(bm, bn) != nullptr; }
+bool gemm_fp4_tile_supported(int bm, int bn, int bk) { return bk == BK && instance(bm, bn, false) != nullptr; }
 
 // Offsets of one tile's operand panels, and of two groups' scales, within 31
 // bits (C is addressed with 64).
@@ -757,33 +767,50 @@ bool gemm_fp4_eligible(int bm, int bn, long long M, long long N, long long K) {
   return rows * (K / 2) < (1LL << 31) && M < (1LL << 28) && N < (1LL << 28);
 }
 
+// The tile of the least estimated time, in units of what a CU needs for one
+// 256-deep slab (measured with all CUs busy: 256 x 256 2.0 us, 256 x 128 1.15,
+// two workgroups of 128 x 128 1.3, one of them 0.75), times the rounds of tiles.
+// Up to 64 rows the streaming kernel, unless more than half of the CUs get a
+// 128 x 128 tile: past 16 rows its re-reading of A costs more than the tile's
+// idle rows (64 x 28672 x 8192 65.8 against 35.4 us, 64 x 8192 x 8192 18.3
+// against 23.9).
 void gemm_fp4_default_tile(long long M, long long N, long long K, int cus, int& bm, int& bn, int& bk) {
   bk = BK;
-  if (M <= 64) {
+  auto tiles = [&](int m, int n) { return (M + m - 1) / m * ((N + n - 1) / n); };
+  if (M <= 16 || (M <= 64 && 2 * tiles(128, 128) <= cus)) {
     bm = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     bn = bm == 16 && N <= 16LL * 4 * cus ? 16 : 32;
     return;
   }
-  bm = M <= 128 ? 128 : 256;
-  bn = bm == 128 ? 128 : (M + 255) / 256 * ((N + 255) / 256) >= cus ? 256 : 128;
-  if (bm == 256 && bn == 128 && (M + 255) / 256 * ((N + 127) / 128) < cus) bm = 128;
+  auto rounds = [](long long t, long long slots) { return (double)((t + slots - 1) / slots); };
+  const long long t = tiles(128, 128);
+  const double big = rounds(tiles(256, 256), cus) * 2.0, mid = rounds(tiles(256, 128), cus) * 1.15;
+  const double small = t <= cus ? 0.75 : rounds(t, 2LL * cus) * 1.3;
+  bm = small < big && small < mid ? 128 : 256;
+  bn = bm == 256 && big <= mid ? 256 : 128;
 }
 
-KernelInfo info_gemm_fp4(int bm, int bn, bool grouped) {
-  const Instance* i = instance(bm, bn);
+KernelInfo info_gemm_fp4(int bm, int bn, bool few, bool grouped) {
+  const Instance* i = instance(bm, bn, few);
   if (!i) return KernelInfo{0, 0, 0};
-  return KernelInfo{i->threads, i->lds,
-                    occupancy_of(reinterpret_cast<const void*>(i->kern[grouped ? 1 : 0]), i->threads, i->lds)};
+  const int g = grouped ? 1 : 0;
+  const void* kern = reinterpret_cast<const void*>(i->kern[g]);
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices)
+    return KernelInfo{i->threads, i->lds, occupancy_of(kern, i->threads, i->lds)};
+  int n = i->resident[g][dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    n = occupancy_of(kern, i->threads, i->lds);
+    i->resident[g][dev].store(n, std::memory_order_release);
+  }
+  return KernelInfo{i->threads, i->lds, n};
 }
 
-hipError_t launch_gemm_fp4(const GemmParams& p, int bm, int bn, hipStream_t stream) {
-  const Instance* i = instance(bm, bn);
+// After info_gemm_fp4 on the same device, which raises the kernel's LDS limit.
+hipError_t launch_gemm_fp4(const GemmParams& p, int bm, int bn, bool few, hipStream_t stream) {
+  const Instance* i = instance(bm, bn, few);
   if (!i) return hipErrorInvalidValue;
-  auto kern = i->kern[p.ngemm > 0 ? 1 : 0];
-  const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, i->lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(p.s.G), dim3(i->threads), i->lds, stream, p);
+  hipLaunchKernelGGL(i->kern[p.ngemm > 0 ? 1 : 0], dim3(p.s.G), dim3(i->threads), i->lds, stream, p);
   return hipGetLastError();
 }
 

@@ -112,6 +112,35 @@ bool device_range(const void* p, size_t bytes, int dev) {
   return q >= b && q - b <= size && bytes <= size - (q - b);
 }
 
+// device_range for the buffers of one call: a buffer inside an allocation that
+// an earlier one of them lies in is not looked up again (short calls are bound
+// by the host, and each look-up is two calls of the runtime).
+struct CallRanges {
+  int dev;
+  int n = 0;
+  uintptr_t lo[8], hi[8];
+  explicit CallRanges(int d) : dev(d) {}
+  bool holds(const void* p, size_t bytes) {
+    const uintptr_t q = (uintptr_t)p;
+    for (int i = 0; i < n; ++i)
+      if (q >= lo[i] && q < hi[i]) return bytes <= hi[i] - q;
+    if (!is_device_ptr(p, dev)) return false;
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    if (hipMemGetAddressRange(&base, &size, const_cast<void*>(p)) != hipSuccess) {
+      (void)hipGetLastError();
+      return false;
+    }
+    const uintptr_t b = (uintptr_t)base;
+    if (q < b || q - b > size) return false;
+    if (n < 8) {
+      lo[n] = b;
+      hi[n++] = b + size;
+    }
+    return bytes <= size - (q - b);
+  }
+};
+
 // M * N * element size, or SIZE_MAX if it does not fit (then no allocation holds it).
 size_t span_bytes(int64_t rows, int64_t cols, size_t esz) {
   if (rows <= 0 || cols <= 0) return 0;
@@ -296,6 +325,7 @@ struct GemmChoice {
   pgemm_kernel kernel;
   bool out_bf16;
   bool vec;  // register-staged kernel: 16-byte vector path
+  bool few;  // MXFP4: at most one tile per CU
 };
 
 bool is_fp4(pgemm_dtype dtype) { return dtype == PGEMM_MXFP4_OUT_BF16 || dtype == PGEMM_MXFP4_OUT_F32; }
@@ -337,6 +367,7 @@ pgemm_status choose_gemm(const pgemm_config* cfg, int64_t M, int64_t N, int64_t 
     if (ch.bm < 1 || ch.bn < 1 || ch.bk < 1) return PGEMM_ERR_INVALID;
     ch.out_bf16 = dtype == PGEMM_MXFP4_OUT_BF16;
     ch.vec = false;
+    ch.few = (M + ch.bm - 1) / ch.bm * ((N + ch.bn - 1) / ch.bn) <= cfg->num_cus;
     ch.kernel = PGEMM_KERNEL_FP4;
     if (!pgk::gemm_fp4_tile_supported(ch.bm, ch.bn, ch.bk) || !pgk::gemm_fp4_eligible(ch.bm, ch.bn, M, N, K) ||
         !fp4_aligned(A, B, C, args ? args->a_scale : nullptr, args ? args->b_scale : nullptr, dtype))
@@ -386,7 +417,7 @@ pgemm_status choose_gemm(const pgemm_config* cfg, int64_t M, int64_t N, int64_t 
 pgk::KernelInfo gemm_info(const GemmChoice& ch) {
   switch (ch.kernel) {
     case PGEMM_KERNEL_FP8: return pgk::info_gemm_fp8(ch.bm, ch.bn);
-    case PGEMM_KERNEL_FP4: return pgk::info_gemm_fp4(ch.bm, ch.bn, false);
+    case PGEMM_KERNEL_FP4: return pgk::info_gemm_fp4(ch.bm, ch.bn, ch.few, false);
     case PGEMM_KERNEL_BF16_LDS: return pgk::info_gemm_bf16_lds(ch.bm, ch.bn, ch.out_bf16);
     case PGEMM_KERNEL_BF16_PINGPONG: return pgk::info_gemm_bf16_pp(ch.out_bf16);
     default: return pgk::info_gemm_bf16(ch.bm, ch.bn, ch.bk, ch.out_bf16, ch.vec);
@@ -824,7 +855,7 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
   DeviceGuard gd(dev);
   if (!gd.ok) return PGEMM_ERR_DEVICE;
   const pgk::KernelInfo ki =
-      fp4 ? pgk::info_gemm_fp4(bm, bn, true)
+      fp4 ? pgk::info_gemm_fp4(bm, bn, total <= cfg->num_cus, true)
           : fp8 ? pgk::info_gemm_fp8_grouped(bm, bn) : pgk::info_gemm_bf16_lds_grouped(bm, bn, csz == 2);
   if (ki.threads == 0) return PGEMM_ERR_UNSUPPORTED;
   pgemm_status st = make_sched(cfg, sched, args, (int)total, 1, cfg->num_cus * ki.occupancy, true, p.s);
@@ -837,7 +868,7 @@ pgemm_status pgemm_run_grouped(pgemm_config* cfg, const pgemm_problem* problems,
   if (st != PGEMM_OK) return st;
   st = reset_counters(args, p.s, cfg->capacity, &cfg->counters_dirty, witness, stream);
   if (st != PGEMM_OK) return st;
-  hipError_t e = fp4 ? pgk::launch_gemm_fp4(p, bm, bn, stream)
+  hipError_t e = fp4 ? pgk::launch_gemm_fp4(p, bm, bn, total <= cfg->num_cus, stream)
                  : fp8 ? pgk::launch_gemm_fp8_grouped(p, bm, bn, witness, stream)
                      : pgk::launch_gemm_bf16_lds_grouped(p, bm, bn, csz == 2, witness, stream);
   if (e == hipErrorInvalidValue) return PGEMM_ERR_UNSUPPORTED;
@@ -942,9 +973,10 @@ pgemm_status gemm_call(pgemm_config* cfg, const void* A, const void* B, void* C,
   const int dev = cfg->device;
   const size_t csz = out_size(dtype);
   const size_t ab = operand_bytes(dtype, M, K), bb = operand_bytes(dtype, N, K), cb = span_bytes(M, N, csz);
-  if (!device_range(A, ab, dev) || !device_range(B, bb, dev) || !device_range(C, cb, dev)) return PGEMM_ERR_INVALID;
-  if (scaled && (!device_range(args->a_scale, scale_bytes(dtype, M, K), dev) ||
-                 !device_range(args->b_scale, scale_bytes(dtype, N, K), dev)))
+  CallRanges in(dev);
+  if (!in.holds(A, ab) || !in.holds(B, bb) || !in.holds(C, cb)) return PGEMM_ERR_INVALID;
+  if (scaled && (!in.holds(args->a_scale, scale_bytes(dtype, M, K)) ||
+                 !in.holds(args->b_scale, scale_bytes(dtype, N, K))))
     return PGEMM_ERR_INVALID;
   // C must not overlap A or B (MXFP4: nor the scales)
   if (overlaps(C, cb, A, ab) || overlaps(C, cb, B, bb)) return PGEMM_ERR_INVALID;
@@ -1001,7 +1033,7 @@ pgemm_status gemm_call(pgemm_config* cfg, const void* A, const void* B, void* C,
 
   hipError_t e;
   if (fp4)
-    e = pgk::launch_gemm_fp4(p, ch.bm, ch.bn, stream);
+    e = pgk::launch_gemm_fp4(p, ch.bm, ch.bn, ch.few, stream);
   else if (fp8)
     e = sk ? pgk::launch_gemm_fp8_sk(p, ch.bm, ch.bn, stream)
            : pgk::launch_gemm_fp8(p, ch.bm, ch.bn, ch.bk, true, witness, stream);
@@ -1148,8 +1180,8 @@ size_t matrix_bytes(int64_t rows, int64_t cols, int64_t ld, size_t esz) {
 
 // A buffer of `bytes` that starts on its elements' alignment and lies in one
 // allocation; an empty one is not looked at.
-bool buffer_ok(const void* p, size_t bytes, size_t align, int dev) {
-  return bytes == 0 || (p != nullptr && aligned(p, align) && device_range(p, bytes, dev));
+bool buffer_ok(const void* p, size_t bytes, size_t align, CallRanges& in) {
+  return bytes == 0 || (p != nullptr && aligned(p, align) && in.holds(p, bytes));
 }
 
 int64_t padded(int64_t n) { return (n + 127) / 128 * 128; }
@@ -1168,7 +1200,8 @@ pgemm_status pmx_quant_run(pgemm_config* cfg, const void* X, int x_type, int64_t
   const size_t xb = matrix_bytes(rows, cols, ldx, type_size(x_type));
   const size_t qb = span_bytes(lines, padded(len) / 2, 1), sb = span_bytes(padded(len) / 128, lines, 4);
   const int dev = cfg->device;
-  if (!buffer_ok(X, xb, type_size(x_type), dev) || !buffer_ok(Q, qb, 1, dev) || !buffer_ok(scale, sb, 1, dev))
+  CallRanges in(dev);
+  if (!buffer_ok(X, xb, type_size(x_type), in) || !buffer_ok(Q, qb, 1, in) || !buffer_ok(scale, sb, 1, in))
     return PGEMM_ERR_INVALID;
   if (overlaps(Q, qb, X, xb) || overlaps(scale, sb, X, xb) || overlaps(Q, qb, scale, sb)) return PGEMM_ERR_INVALID;
   if (!aligned(Q, 4) || !aligned(scale, 4)) return PGEMM_ERR_UNSUPPORTED;
@@ -1186,7 +1219,8 @@ pgemm_status pmx_dequant_run(pgemm_config* cfg, const uint8_t* Q, const uint8_t*
   const size_t yb = matrix_bytes(rows, cols, ldy, type_size(y_type));
   const size_t qb = span_bytes(rows, padded(cols) / 2, 1), sb = span_bytes(padded(cols) / 128, rows, 4);
   const int dev = cfg->device;
-  if (!buffer_ok(Y, yb, type_size(y_type), dev) || !buffer_ok(Q, qb, 1, dev) || !buffer_ok(scale, sb, 1, dev))
+  CallRanges in(dev);
+  if (!buffer_ok(Y, yb, type_size(y_type), in) || !buffer_ok(Q, qb, 1, in) || !buffer_ok(scale, sb, 1, in))
     return PGEMM_ERR_INVALID;
   if (overlaps(Y, yb, Q, qb) || overlaps(Y, yb, scale, sb)) return PGEMM_ERR_INVALID;
   if (!aligned(Q, 4) || !aligned(scale, 4)) return PGEMM_ERR_UNSUPPORTED;
@@ -1212,6 +1246,7 @@ pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx,
   if ((r_type != x_type && r_type != PMX_F32) || (w_type != x_type && w_type != PMX_F32)) return PGEMM_ERR_UNSUPPORTED;
   if (rows == 0) return PGEMM_OK;
   const int dev = cfg->device;
+  CallRanges in(dev);
   const size_t xs = type_size(x_type), rs = type_size(r_type), ws = type_size(w_type);
   const int64_t kp = padded(cols);
   const size_t xb = matrix_bytes(rows, cols, ldx, xs), wb = (size_t)cols * ws;
@@ -1220,9 +1255,9 @@ pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx,
                           : matrix_bytes(rows, cols, ldy, xs);
   const size_t sb = quant ? span_bytes(kp / 128, rows, out == PRMS_OUT_FP8_B128 ? 1 : 4) : 0;
   const size_t tb = rstd ? span_bytes(rows, 4, 1) : 0;
-  if (!buffer_ok(X, xb, xs, dev) || !buffer_ok(R, rb, rs, dev) || !buffer_ok(W, wb, ws, dev) ||
-      !buffer_ok(H, hb, rs, dev) || !buffer_ok(Y, yb, quant ? 1 : xs, dev) || !buffer_ok(y_scale, sb, 1, dev) ||
-      !buffer_ok(rstd, tb, 4, dev))
+  if (!buffer_ok(X, xb, xs, in) || !buffer_ok(R, rb, rs, in) || !buffer_ok(W, wb, ws, in) ||
+      !buffer_ok(H, hb, rs, in) || !buffer_ok(Y, yb, quant ? 1 : xs, in) || !buffer_ok(y_scale, sb, 1, in) ||
+      !buffer_ok(rstd, tb, 4, in))
     return PGEMM_ERR_INVALID;
   // every output against every input and every other output; in place: H on R
   // or X, Y on X
@@ -1256,13 +1291,14 @@ pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_
     return PGEMM_ERR_INVALID;
   if ((h_type != y_type && h_type != PMX_F32) || (w_type != y_type && w_type != PMX_F32)) return PGEMM_ERR_UNSUPPORTED;
   const int dev = cfg->device;
+  CallRanges in(dev);
   const size_t ys = type_size(y_type), hs = type_size(h_type), ws = type_size(w_type);
   const size_t yb = matrix_bytes(rows, cols, ldy, ys), hb = matrix_bytes(rows, cols, ldh, hs);
   const size_t db = dH ? matrix_bytes(rows, cols, ldd, hs) : 0, xb = matrix_bytes(rows, cols, ldx, hs);
   const size_t wb = (size_t)cols * ws, tb = span_bytes(rows, 4, 1), gb = dW ? (size_t)cols * 4 : 0;
-  if (!buffer_ok(dY, yb, ys, dev) || !buffer_ok(H, hb, hs, dev) || !buffer_ok(dH, db, hs, dev) ||
-      !buffer_ok(W, wb, ws, dev) || !buffer_ok(rstd, tb, 4, dev) || !buffer_ok(dX, xb, hs, dev) ||
-      !buffer_ok(dW, gb, 4, dev))
+  if (!buffer_ok(dY, yb, ys, in) || !buffer_ok(H, hb, hs, in) || !buffer_ok(dH, db, hs, in) ||
+      !buffer_ok(W, wb, ws, in) || !buffer_ok(rstd, tb, 4, in) || !buffer_ok(dX, xb, hs, in) ||
+      !buffer_ok(dW, gb, 4, in))
     return PGEMM_ERR_INVALID;
   const bool on_dy = dX == dY && ldx == ldy && y_type == h_type, on_dh = dX == dH && ldx == ldd;
   if ((!on_dy && overlaps(dX, xb, dY, yb)) || (!on_dh && overlaps(dX, xb, dH, db)) || overlaps(dX, xb, H, hb) ||
