@@ -233,7 +233,8 @@ typedef struct {
  * XCD count, allocates and zeroes an int32 work-stealing counter array of
  * max_xcds entries (0 => 16), and allocates the stream-K workspace for the
  * default grid of every stream-K tile (two fp32 tiles per program:
- * CUs x 512 KiB at 256x256 tiles, 128 MiB on 256 CUs).  Fails with PGEMM_ERR_INVALID if the device has more XCDs than max_xcds
+ * CUs x 512 KiB at 256x256 tiles, 128 MiB on 256 CUs) and 64 MiB for
+ * prms_grad_run.  Fails with PGEMM_ERR_INVALID if the device has more XCDs than max_xcds
  * (the counter index p mod X would run past the array), with
  * PGEMM_ERR_UNSUPPORTED if the device is not gfx950.  *out receives the new
  * config, owned by the caller until pgemm_config_destroy. */
@@ -500,17 +501,18 @@ PGEMM_API pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, in
                       void* hip_stream);
 
 /* Gradients of prms_run, the rounding of its output taken as the identity:
- *   g = w * dy, dx = dh + rstd * g - h * rstd^3 * sum(g * h) / cols
- *   dw = sum over the rows of dy * h * rstd
+ *   g = w * dy, n = h * rstd, dx = dh + rstd * (g - n * mean(g * n))
+ *   dw = sum over the rows of dy * n
  * dY [rows][cols] y_type, H (the h of the forward), dH (the gradient that
  * reaches h past the norm; may be NULL: none) and dX h_type (y_type or
  * PMX_F32), W w_type (y_type or PMX_F32), rstd fp32 [rows] as prms_run wrote
  * it, dW fp32 [cols] (may be NULL: not computed).  dX is the gradient of both
  * x and r.  Sums in fp32 in an order that depends on the sizes only, so results
  * repeat bit for bit.  dX may be dH exactly, or dY exactly if the types are
- * the same (same stride).  The partial sums of dW live in the config's
- * workspace (see pgemm_config_create): PGEMM_ERR_UNSUPPORTED if one row of
- * cols floats does not fit there.  rows == 0 writes zeros to dW. */
+ * the same (same stride).  The partial sums of dW live in a buffer of 64 MiB
+ * that the config allocates when it is created and keeps in place (calls with
+ * dW on one config must not overlap in time): PGEMM_ERR_UNSUPPORTED if one
+ * row of cols floats does not fit there.  rows == 0 writes zeros to dW. */
 PGEMM_API pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_t ldy, const void* H,
                            int h_type, int64_t ldh, const void* dH, int64_t ldd, const void* W, int w_type,
                            const float* rstd, int64_t rows, int64_t cols, void* dX, int64_t ldx,

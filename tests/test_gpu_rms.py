@@ -222,6 +222,22 @@ def test_gradient_in_place_strided_and_repeatable(cols, ld, off):
     assert torch.equal(again, dX) and torch.equal(dWa, dW)
 
 
+@pytest.mark.parametrize("exponent", [-90, -60, 50, 62])
+def test_gradient_of_very_small_and_large_rows(exponent):
+    """rstd of 2^90 or 2^-62: its third power and sums of h leave the range of
+    fp32, the gradient (of order rstd) does not."""
+    for rows, cols in [(3, 200), (2, 20000)]:
+        rng = np.random.default_rng(exponent + 100)
+        H = tensor(rng.standard_normal((rows, cols)) * 2.0 ** exponent, "f32")
+        W, dY = tensor(1 + 0.3 * rng.standard_normal(cols), "f32"), tensor(rng.standard_normal((rows, cols)), "f32")
+        T = tensor(mx.rms(host(H), host(W), 0.0)[1], "f32")
+        dX, dW = torch.empty_like(H), torch.empty(cols, device="cuda:0")
+        note(f"prms_grad_run {rows}x{cols} 2^{exponent}")
+        pg.prms_grad_run(config(), dY, H, W, T, dX, dW, rows, cols)
+        sync()
+        check_grad(host(dX), host(dW), host(dY), host(H), host(W), host(T), None, "f32", "f32", (rows, cols))
+
+
 def test_gradient_against_differences():
     """dX and dW of an fp32 call against central differences of the forward
     (computed in 64 bits from perturbed inputs): step 1e-4 on values of order

@@ -131,6 +131,10 @@ def _dev(x, what):
 def _ptr(x, what, dtypes=None, nbytes=None):
     """Device pointer of a torch tensor (contiguous, on a GPU, of an allowed
     dtype, at least nbytes long) or a raw int pointer."""
+    if (type(x) is _TENSOR and x.is_cuda and x.is_contiguous() and (nbytes is None or x.nbytes >= nbytes)
+            and (dtypes is None or x.dtype in _torch_dtypes(dtypes))):
+        return x.data_ptr()
+    # what the short form does not take: named errors, raw pointers, empty buffers
     _check_tensor(x, what, dtypes, nbytes)
     return _dev(x, what)
 
@@ -383,6 +387,9 @@ _ELEM = {}
 
 def _elem(x, what, given=None):
     """PMX_* element type of a tensor argument (raw pointers: `given`)."""
+    t = _ELEM.get(getattr(x, "dtype", None))
+    if t is not None:
+        return t
     if isinstance(x, int):
         if given is None:
             raise ValueError(f"{what}: a raw pointer needs its element type")
@@ -400,14 +407,16 @@ def _matrix(x, what, rows, cols, ld=None):
     """(device pointer, row stride) of a [rows][cols] matrix: a 2-D tensor with
     dense rows, a contiguous tensor of at least rows * cols elements, or a raw
     pointer with its row stride `ld`."""
+    if ld is None and type(x) is _TENSOR and x.is_cuda and x.shape == (rows, cols):
+        step = x.stride()
+        if step[1] == 1 or cols == 1:
+            return x.data_ptr(), step[0] if rows > 1 else cols
     if isinstance(x, int):
         return x, int(cols if ld is None else ld)
     if not isinstance(x, _TENSOR or _tensor_type()):
         raise TypeError(f"{what}: expected a torch tensor or an int device pointer")
-    if ld is None and x.shape == (rows, cols):
-        step = x.stride()
-        if step[1] == 1 or cols == 1:
-            return _dev(x, what), step[0] if rows > 1 else cols
+    if ld is None and x.shape == (rows, cols) and (x.stride(1) == 1 or cols == 1):
+        return _dev(x, what), int(x.stride(0)) if rows > 1 else cols
     ld = cols if ld is None else int(ld)
     need = ((rows - 1) * ld + cols if rows else 0) * x.element_size()
     _check_tensor(x, what, None, need)

@@ -1,6 +1,8 @@
 // Gradient of the RMS norm:
-//   g = w * dy, c = sum(g * h), dx = dh + rstd * g - h * rstd^3 * c / cols
-//   dw = sum over the rows of dy * h * rstd
+//   g = w * dy, n = h * rstd, dx = dh + rstd * (g - n * mean(g * n))
+//   dw = sum over the rows of dy * n
+// n is of order one whatever h's size is, so no power of rstd or sum of h
+// leaves the range of fp32 before the result does.
 //
 // One pass over dy, h and dh gives both.  A workgroup walks a strided set of
 // rows; its threads own columns, so their shares of dw stay in registers
@@ -45,15 +47,15 @@ __device__ __forceinline__ void weights(const RmsGradParams& p, int64_t c, float
     vec8_f32<YT>(vec8_load<YT>(p.W, c, p.cols), w);
 }
 
-// dx of eight columns; k = rstd^3 * c / cols.
+// dx of eight columns; mean = mean(g * n) of the row.
 template <int YT, int HT>
 __device__ __forceinline__ void put_dx(const RmsGradParams& p, int64_t row, int64_t c, const float (&dy)[8],
-                                       const float (&h)[8], const Vec8<HT>& dh, const float (&w)[8], float rstd,
-                                       float k) {
+                                       const float (&n)[8], const Vec8<HT>& dh, const float (&w)[8], float rstd,
+                                       float mean) {
   float d[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    d[e] = rstd * (dy[e] * w[e]) - h[e] * k;
+    d[e] = rstd * (dy[e] * w[e] - n[e] * mean);
     if (p.dH) d[e] += vec8_get(dh, e);
   }
   vec8_store<HT>(static_cast<char*>(p.dX) + row * p.ldx * (HT == kTypeF32 ? 4 : 2), c, p.cols, vec8_pack<HT>(d));
@@ -93,22 +95,23 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_kernel(RmsGradParams p,
     if (VPT != 1) load_w();  // two vectors leave no registers to keep it in
     const float r = now.rstd;
     float c = 0.0f;
-    float dy[VPT][8], h[VPT][8];
+    float dy[VPT][8], nh[VPT][8];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       vec8_f32<YT>(now.dy[v], dy[v]);
-      vec8_f32<HT>(now.h[v], h[v]);
+      vec8_f32<HT>(now.h[v], nh[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        c += dy[v][e] * w[v][e] * h[v][e];
-        if (on) acc[v][e] += dy[v][e] * (h[v][e] * r);
+        nh[v][e] *= r;
+        c += dy[v][e] * w[v][e] * nh[v][e];
+        if (on) acc[v][e] += dy[v][e] * nh[v][e];
       }
     }
-    const float k = r * r * r * (row_sum(c, L, s_sum, turn) * inv);
+    const float mean = row_sum(c, L, s_sum, turn) * inv;
     if (on) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
-        put_dx<YT, HT>(p, row, ((int64_t)v * L + t0) * 8, dy[v], h[v], now.dh[v], w[v], r, k);
+        put_dx<YT, HT>(p, row, ((int64_t)v * L + t0) * 8, dy[v], nh[v], now.dh[v], w[v], r, mean);
     }
     if (AHEAD) now = next;
   }
@@ -166,9 +169,9 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_long_dx_kernel(RmsGradP
       vec8_f32<HT>(vec8_load<HT>(hr, c, p.cols), h);
       weights<YT>(p, c, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += dy[e] * w[e] * h[e];
+      for (int e = 0; e < 8; ++e) s += dy[e] * w[e] * (h[e] * r);
     }
-    const float k = r * r * r * (row_sum(s, kRmsMaxLanes, s_sum, turn) / (float)p.cols);
+    const float mean = row_sum(s, kRmsMaxLanes, s_sum, turn) / (float)p.cols;
     for (int64_t c = threadIdx.x * 8; c < p.cols; c += kRmsMaxLanes * 8) {
       float dy[8], h[8], w[8];
       Vec8<HT> dh;
@@ -176,7 +179,9 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_long_dx_kernel(RmsGradP
       vec8_f32<HT>(vec8_load<HT>(hr, c, p.cols), h);
       if (p.dH) dh = vec8_load<HT>(static_cast<const char*>(p.dH) + row * p.ldd * hsz, c, p.cols);
       weights<YT>(p, c, w);
-      put_dx<YT, HT>(p, row, c, dy, h, dh, w, r, k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] *= r;
+      put_dx<YT, HT>(p, row, c, dy, h, dh, w, r, mean);
     }
   }
 }

@@ -45,6 +45,7 @@ struct pgemm_config {
   bool counters_dirty;  // the counters may hold a launch's values (see reset_counters)
   float* ws;          // stream-K partial-sum workspace (device), grown on demand
   size_t ws_bytes;
+  float* grad_ws;  // partial sums of the norm's dw (device), kGradWsBytes
   unsigned char* scratch;  // this device's address of the static `scratch` array
   OrderChoice order_choice[kOrderCache];  // recent numbering decisions (choose_order)
   int order_next = 0;                     // slot the next new decision replaces
@@ -75,6 +76,10 @@ constexpr int kDefaultGroup = 8;     // GEMM: rows of tiles per group of the gro
 // 128x128 tiles, 4.2 -> 4.8 at 32x16).
 constexpr int kDefaultAddGroup = 1;
 constexpr int kMaxGemmChunk = 64;  // tiles per work-stealing claim, GEMM
+// Partial sums of the norm's dw: a row of up to 16384 columns for each of 256
+// CUs is 16 MiB; longer rows take fewer partial sums.  An allocation of its
+// own, which never moves: a captured call keeps its address.
+constexpr size_t kGradWsBytes = (size_t)64 << 20;
 // PGEMM_PIPELINE_DEFAULT takes the ping-pong kernel where it applies.
 constexpr bool kPingPongDefault = false;
 
@@ -647,10 +652,12 @@ pgemm_status pgemm_config_create(int device, int max_xcds, pgemm_config** out) {
   if (e == hipSuccess) e = hipMemset(c->counters, 0, cbytes);
   if (e == hipSuccess) e = hipMalloc((void**)&c->ws, wsb);
   if (e == hipSuccess) c->ws_bytes = wsb;
+  if (e == hipSuccess) e = hipMalloc((void**)&c->grad_ws, kGradWsBytes);
   if (e == hipSuccess) e = hipDeviceSynchronize();
   if (e != hipSuccess) {
     if (c->counters) (void)hipFree(c->counters);
     if (c->ws) (void)hipFree(c->ws);
+    if (c->grad_ws) (void)hipFree(c->grad_ws);
     delete c;
     return from_hip(e);
   }
@@ -677,6 +684,7 @@ pgemm_status pgemm_config_destroy(pgemm_config* cfg) {
   free_witness(cfg);
   if (cfg->counters) (void)hipFree(cfg->counters);
   if (cfg->ws) (void)hipFree(cfg->ws);
+  if (cfg->grad_ws) (void)hipFree(cfg->grad_ws);
   delete cfg;
   return PGEMM_OK;
 }
@@ -1308,14 +1316,14 @@ pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_
   int partials = 0;
   if (dW) {
     partials = pgk::rms_grad_partials(rows, cols, cfg->num_cus);
-    const int64_t fit = (int64_t)(cfg->ws_bytes / ((size_t)cols * sizeof(float)));
+    const int64_t fit = (int64_t)(kGradWsBytes / ((size_t)cols * sizeof(float)));
     if (fit < 1) return PGEMM_ERR_UNSUPPORTED;
     if (partials > fit) partials = (int)fit;
   }
   DeviceGuard g(dev);
   if (!g.ok) return PGEMM_ERR_DEVICE;
   const pgk::RmsGradParams p = {dY,  H,   dH,  W,    rstd, y_type, h_type, w_type,  ldy,
-                                ldh, ldd, ldx, rows, cols, dX,     dW,     cfg->ws, partials, cfg->num_cus};
+                                ldh, ldd, ldx, rows, cols, dX,     dW,     cfg->grad_ws, partials, cfg->num_cus};
   return pgk::launch_rms_grad(p, (hipStream_t)hip_stream) == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
 }
 
