@@ -121,7 +121,9 @@ struct Quad<2> {
 };
 
 // Elements i .. i + 7 of a row that ends at `n` (elements past it zero).
-template <int T>
+// WHOLE: n is a multiple of 8, as i is, and the code for a vector's part falls
+// away.
+template <int T, bool WHOLE = false>
 __device__ __forceinline__ Vec8<T> vec8_load(const void* row, int64_t i, int64_t n) {
   constexpr int esz = T == kTypeF32 ? 4 : 2;
   Vec8<T> v;
@@ -131,7 +133,7 @@ __device__ __forceinline__ Vec8<T> vec8_load(const void* row, int64_t i, int64_t
     const auto* p = reinterpret_cast<const typename Quad<esz>::type*>(static_cast<const char*>(row) + i * esz);
 #pragma unroll
     for (int q = 0; q < esz / 2; ++q) v.q[q] = p[q];
-  } else if (i < n) {
+  } else if (!WHOLE && i < n) {
 #pragma unroll
     for (int e = 0; e < 7; ++e) {
       if (i + e >= n) continue;
@@ -144,14 +146,14 @@ __device__ __forceinline__ Vec8<T> vec8_load(const void* row, int64_t i, int64_t
   return v;
 }
 
-template <int T>
+template <int T, bool WHOLE = false>
 __device__ __forceinline__ void vec8_store(void* row, int64_t i, int64_t n, const Vec8<T>& v) {
   constexpr int esz = T == kTypeF32 ? 4 : 2;
   if (i + 8 <= n) {
     auto* p = reinterpret_cast<typename Quad<esz>::type*>(static_cast<char*>(row) + i * esz);
 #pragma unroll
     for (int q = 0; q < esz / 2; ++q) p[q] = v.q[q];
-  } else if (i < n) {
+  } else if (!WHOLE && i < n) {
 #pragma unroll
     for (int e = 0; e < 7; ++e) {
       if (i + e >= n) continue;

@@ -22,15 +22,25 @@ __device__ __forceinline__ float narrow_odd(double y) {
   return (float)__builtin_bit_cast(double, (unsigned long long)(hi | (lo != 0u ? 1u : 0u)) << 32);
 }
 
-// The row group of workgroup i: ranges of `chunk` consecutive ones go to the
-// workgroups of one XCD (which take every X-th index), because the scale bytes
+// How the rows are divided: L threads to a row, `per` rows side by side in a
+// workgroup, n groups of them.
+struct RowPlan {
+  int L, per;
+  unsigned n;
+  unsigned full;  // groups in whole rounds of xcds << shift
+  unsigned xcds;
+  int shift;
+};
+
+// The row group of workgroup i: ranges of 2^shift consecutive ones go to the
+// workgroups of one XCD (which take every xcds-th index), because the scale bytes
 // of consecutive rows share lines of memory, which that XCD's L2 then writes
-// whole.
-__device__ __forceinline__ int64_t group_of(int64_t i, int64_t n, int X, int chunk) {
-  const int64_t per = (int64_t)X * chunk;
-  if (i >= n / per * per) return i;
-  const int64_t j = i / X, x = i - j * X;
-  return j / chunk * per + x * chunk + j % chunk;
+// whole.  (32 bits and one division: every workgroup computes it before its
+// first load.)
+__device__ __forceinline__ unsigned group_of(unsigned i, const RowPlan& g) {
+  if (i >= g.full) return i;
+  const unsigned j = i / g.xcds, x = i - j * g.xcds;
+  return ((((j >> g.shift) * g.xcds) + x) << g.shift) + (j & ((1u << g.shift) - 1u));
 }
 
 // 1 / sqrt(x) to the last bit or two: the approximate instruction and two
@@ -45,14 +55,14 @@ __device__ __forceinline__ double inv_sqrt(double x) {
   return x > 0.0 && x < __builtin_inf() ? r : r0;
 }
 
-template <int WT>
+template <int WT, bool WHOLE>
 __device__ __forceinline__ void weights(const RmsParams& p, int64_t c, float (&w)[8]) {
-  vec8_f32<WT>(vec8_load<WT>(p.W, c, p.cols), w);
+  vec8_f32<WT>(vec8_load<WT, WHOLE>(p.W, c, p.cols), w);
 }
 
 // h = x + r as it is stored (RT: its type), written to H where there is a
 // residual.
-template <int XT, int RT, bool RES>
+template <int XT, int RT, bool RES, bool WHOLE>
 __device__ __forceinline__ void h_of(const RmsParams& p, int64_t row, int64_t c, const Vec8<XT>& x, const Vec8<RT>& r,
                                      float (&h)[8]) {
   vec8_f32<XT>(x, h);
@@ -62,13 +72,13 @@ __device__ __forceinline__ void h_of(const RmsParams& p, int64_t row, int64_t c,
 #pragma unroll
     for (int e = 0; e < 8; ++e) a[e] += h[e];
     const Vec8<RT> s = vec8_pack<RT>(a);
-    vec8_store<RT>(static_cast<char*>(p.H) + row * p.ldh * (RT == kTypeF32 ? 4 : 2), c, p.cols, s);
+    vec8_store<RT, WHOLE>(static_cast<char*>(p.H) + row * p.ldh * (RT == kTypeF32 ? 4 : 2), c, p.cols, s);
     vec8_f32<RT>(s, h);
   }
 }
 
 // Eight columns of the output.  Called by whole rows of 16 lanes.
-template <int XT, int OUT>
+template <int XT, int OUT, bool WHOLE>
 __device__ __forceinline__ void put(const RmsParams& p, int64_t row, int64_t c, int64_t kp, const float (&h)[8],
                                     const float (&w)[8], double rstd) {
   float y[8];
@@ -78,13 +88,17 @@ __device__ __forceinline__ void put(const RmsParams& p, int64_t row, int64_t c, 
     y[e] = OUT == kRmsSame && XT == kTypeF32 ? (float)v : narrow_odd(v);
   }
   if (OUT == kRmsSame) {
-    vec8_store<XT>(static_cast<char*>(p.Y) + row * p.ldy * (XT == kTypeF32 ? 4 : 2), c, p.cols, vec8_pack<XT>(y));
+    vec8_store<XT, WHOLE>(static_cast<char*>(p.Y) + row * p.ldy * (XT == kTypeF32 ? 4 : 2), c, p.cols, vec8_pack<XT>(y));
     return;
   }
-  if (c + 8 > p.cols) {  // the padding is zero whatever rstd is
+  if (!WHOLE && c + 8 > p.cols) {  // the padding is zero whatever rstd is
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (c + e >= p.cols) y[e] = 0.0f;
+  }
+  if (WHOLE && c >= p.cols) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
   }
   const Vec8<kTypeF32> v = vec8_pack<kTypeF32>(y);
   const int lane16 = threadIdx.x & 15;
@@ -115,15 +129,15 @@ __device__ __forceinline__ void put(const RmsParams& p, int64_t row, int64_t c, 
 }
 
 // Rows held in registers: VPT vectors per thread.
-template <int XT, int RT, bool RES, int OUT, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? kRmsMaxLanes : kRmsMaxLanes / 2) rms_kernel(RmsParams p, int L, int chunk) {
+template <int XT, int RT, bool RES, int OUT, int VPT, bool WHOLE>
+__global__ void __launch_bounds__(VPT == 1 ? kRmsMaxLanes : kRmsMaxLanes / 2) rms_kernel(RmsParams p, RowPlan g) {
   __shared__ double s_sum[2][16];
-  const int per = (int)blockDim.x / L, sub = (int)threadIdx.x / L, t0 = (int)threadIdx.x - sub * L;
-  const int64_t kp = (p.cols + 127) / 128 * 128, n = (p.rows + per - 1) / per;
+  const int L = g.L, sub = (int)threadIdx.x / L, t0 = (int)threadIdx.x - sub * L;
+  const int64_t kp = (p.cols + 127) / 128 * 128;
   constexpr int xsz = XT == kTypeF32 ? 4 : 2, rsz = RT == kTypeF32 ? 4 : 2;
   int turn = 0;
-  for (int64_t i = blockIdx.x; i < n; i += gridDim.x, turn ^= 1) {
-    const int64_t row = group_of(i, n, p.xcds, chunk) * per + sub;
+  for (unsigned i = blockIdx.x; i < g.n; i += gridDim.x, turn ^= 1) {
+    const int64_t row = (int64_t)group_of(i, g) * g.per + sub;
     const bool on = row < p.rows;
     const int64_t at = on ? row : p.rows - 1;
     Vec8<XT> x[VPT];
@@ -131,15 +145,15 @@ __global__ void __launch_bounds__(VPT == 1 ? kRmsMaxLanes : kRmsMaxLanes / 2) rm
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int64_t c = ((int64_t)v * L + t0) * 8;
-      x[v] = vec8_load<XT>(static_cast<const char*>(p.X) + at * p.ldx * xsz, c, p.cols);
-      if (RES) r[v] = vec8_load<RT>(static_cast<const char*>(p.R) + at * p.ldr * rsz, c, p.cols);
+      x[v] = vec8_load<XT, WHOLE>(static_cast<const char*>(p.X) + at * p.ldx * xsz, c, p.cols);
+      if (RES) r[v] = vec8_load<RT, WHOLE>(static_cast<const char*>(p.R) + at * p.ldr * rsz, c, p.cols);
     }
     float h[VPT][8];
     double s = 0.0;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int64_t c = ((int64_t)v * L + t0) * 8;
-      h_of<XT, RT, RES>(p, at, on ? c : p.cols, x[v], r[v], h[v]);
+      h_of<XT, RT, RES, WHOLE>(p, at, on ? c : p.cols, x[v], r[v], h[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += (double)h[v][e] * (double)h[v][e];
     }
@@ -153,10 +167,10 @@ __global__ void __launch_bounds__(VPT == 1 ? kRmsMaxLanes : kRmsMaxLanes / 2) rm
       if (c >= kp) continue;
       float w[8];
       if (p.w_type == kTypeF32)
-        weights<kTypeF32>(p, c, w);
+        weights<kTypeF32, WHOLE>(p, c, w);
       else
-        weights<XT>(p, c, w);
-      put<XT, OUT>(p, row, c, kp, h[v], w, rstd);
+        weights<XT, WHOLE>(p, c, w);
+      put<XT, OUT, WHOLE>(p, row, c, kp, h[v], w, rstd);
     }
   }
 }
@@ -176,7 +190,7 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_long_kernel(RmsParams p) {
       Vec8<RT> r;
       if (RES) r = vec8_load<RT>(static_cast<const char*>(p.R) + row * p.ldr * rsz, c, p.cols);
       float h[8];
-      h_of<XT, RT, RES>(p, row, c, vec8_load<XT>(xr, c, p.cols), r, h);
+      h_of<XT, RT, RES, false>(p, row, c, vec8_load<XT>(xr, c, p.cols), r, h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += (double)h[e] * (double)h[e];
     }
@@ -190,10 +204,10 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_long_kernel(RmsParams p) {
       else
         vec8_f32<XT>(vec8_load<XT>(xr, c, p.cols), h);
       if (p.w_type == kTypeF32)
-        weights<kTypeF32>(p, c, w);
+        weights<kTypeF32, false>(p, c, w);
       else
-        weights<XT>(p, c, w);
-      put<XT, OUT>(p, row, c, kp, h, w, rstd);
+        weights<XT, false>(p, c, w);
+      put<XT, OUT, false>(p, row, c, kp, h, w, rstd);
     }
   }
 }
@@ -217,11 +231,18 @@ void launch_typed(const RmsParams& p, hipStream_t stream) {
   const dim3 threads(L * per);
   const int64_t n = (p.rows + per - 1) / per;
   const dim3 grid((unsigned)(n < kMaxGrid ? n : kMaxGrid));
-  const int chunk = line > per ? line / per : 1;
-  if (vpt == 1)
-    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 1>), grid, threads, 0, stream, p, L, chunk);
+  RowPlan g = {L, per, (unsigned)n, 0, (unsigned)p.xcds, 0};
+  while ((per << g.shift) < line) ++g.shift;
+  g.full = (unsigned)(n / ((int64_t)p.xcds << g.shift) * ((int64_t)p.xcds << g.shift));
+  const bool whole = p.cols % 8 == 0;
+  if (vpt == 1 && whole)
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 1, true>), grid, threads, 0, stream, p, g);
+  else if (vpt == 1)
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 1, false>), grid, threads, 0, stream, p, g);
+  else if (whole)
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 4, true>), grid, threads, 0, stream, p, g);
   else
-    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 4>), grid, threads, 0, stream, p, L, chunk);
+    hipLaunchKernelGGL((rms_kernel<XT, RT, RES, OUT, 4, false>), grid, threads, 0, stream, p, g);
 }
 
 template <int XT, int RT, bool RES>
