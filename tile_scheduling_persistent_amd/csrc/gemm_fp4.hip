@@ -78,30 +78,37 @@ __device__ __forceinline__ void store_f32x4(float* row, int64_t c, int64_t n, f3
       if (c + e < n) row[c + e] = v[e];
   }
 }
-// W (2 or 4) columns at p, those before `left`.
-template <int W>
+// W (2 or 4) columns at p, those before `left`; non-temporal where NT.
+template <bool NT, class V>
+__device__ __forceinline__ void store_vec(V* p, V v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+template <int W, bool NT>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[W], int64_t left) {
   if (left >= W) {
     if constexpr (W == 4)
-      *reinterpret_cast<u32x4_a4*>(p) = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+      store_vec<NT>(reinterpret_cast<u32x4_a4*>(p), __builtin_bit_cast(u32x4_a4, f32x4{v[0], v[1], v[2], v[3]}));
     else
-      *reinterpret_cast<u32x2_a4*>(p) = __builtin_bit_cast(u32x2, f32x2{v[0], v[1]});
+      store_vec<NT>(reinterpret_cast<u32x2_a4*>(p), __builtin_bit_cast(u32x2_a4, f32x2{v[0], v[1]}));
   } else {
 #pragma unroll
     for (int e = 0; e < W - 1; ++e)
       if (e < left) p[e] = v[e];
   }
 }
-template <int W>
+template <int W, bool NT>
 __device__ __forceinline__ void store_row(unsigned short* p, const float (&v)[W], int64_t left) {
   unsigned o[W / 2];
 #pragma unroll
   for (int e = 0; e < W / 2; ++e) o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
   if (left >= W) {
     if constexpr (W == 4)
-      *reinterpret_cast<u32x2_a2*>(p) = u32x2{o[0], o[1]};
+      store_vec<NT>(reinterpret_cast<u32x2_a2*>(p), u32x2_a2{o[0], o[1]});
     else
-      *reinterpret_cast<u32_a2*>(p) = o[0];
+      store_vec<NT>(reinterpret_cast<u32_a2*>(p), (u32_a2)o[0]);
   } else {
 #pragma unroll
     for (int e = 0; e < W - 1; ++e)
@@ -433,7 +440,7 @@ __global__ void __launch_bounds__(128 * WN) gemm_fp4_kernel(GemmParams P) {
   // Lane l holds SN consecutive columns, l % 32 * SN of the wave's, one per
   // block; registers 4 g + e hold rows (8 g + 4 (l / 32) + e) * SM + block: a
   // store of the wave covers two rows' 32 * SN consecutive columns.
-  auto put_tile = [&](int m0, int n0, auto out, auto edge) {
+  auto put_tile = [&](int m0, int n0, auto out, auto edge, auto nt) {
     typedef decltype(out) T;
     const int64_t n = n0 + wn * S::TN + l32 * SN;
     const int m = m0 + wm * S::TM + 4 * kb * SM;
@@ -449,17 +456,30 @@ __global__ void __launch_bounds__(128 * WN) gemm_fp4_kernel(GemmParams P) {
           float v[SN];
 #pragma unroll
           for (int j = 0; j < SN; ++j) v[j] = acc_read(acc[j][i][4 * g + e]);
-          store_row<SN>(base + (int64_t)r * Nc, v, edge ? (int64_t)Nc - n : (int64_t)SN);
+          store_row<SN, nt>(base + (int64_t)r * Nc, v, edge ? (int64_t)Nc - n : (int64_t)SN);
         }
   };
+  // Non-temporal where rows of C start on 128-byte lines, so that C does not
+  // push operand panels out of L2 (8192^3 260 -> 250 us, 2000 x 28672 x 512 to
+  // fp32 58 -> 51; partial lines cost more than that: 3000 x 7000 x 2048 to fp32
+  // 44 against 48).
   auto epilogue = [&](int m0, int n0) {
     const bool edge = m0 + BM > Mc || n0 + BN > Nc;
+    const bool lines = (Nc & (P.out_f32 ? 31 : 63)) == 0 && (reinterpret_cast<uintptr_t>(Cc) & 127) == 0;
     const std::integral_constant<bool, true> yes;
     const std::integral_constant<bool, false> no;
+    auto put = [&](auto out) {
+      if (edge)
+        put_tile(m0, n0, out, yes, no);
+      else if (lines)
+        put_tile(m0, n0, out, no, yes);
+      else
+        put_tile(m0, n0, out, no, no);
+    };
     if (P.out_f32)
-      edge ? put_tile(m0, n0, 0.0f, yes) : put_tile(m0, n0, 0.0f, no);
+      put(0.0f);
     else
-      edge ? put_tile(m0, n0, (unsigned short)0, yes) : put_tile(m0, n0, (unsigned short)0, no);
+      put((unsigned short)0);
   };
 
   if (tid == 0) s_first[0] = walker.first();
