@@ -3,18 +3,16 @@
 // consecutive k (SA[K/128][M][4], SB[K/128][N][4]), fp32 accumulate, C bf16
 // or fp32.
 //
-// The scales enter v_mfma_scale_f32_16x16x128_f8f6f4: lane l supplies the 32
-// k-values of row l % 16, block l / 16 of a 128-deep step as 16 bytes and the
-// scale byte of exactly that block.  C comes out transposed in the lanes (the
-// B rows are the first operand): lane l holds row l % 16 of a 16x16 block of
-// C, columns 4 * (l / 16) .. +3.
-//
 // Two kernels:
-//  * gemm_fp4_kernel, tiles staged through LDS: bound by the matrix cores and,
-//    on data that is not all zeros, by the power they draw.
-//  * gemm_fp4_skinny_kernel for up to 64 rows: bound by the bytes of B, which
-//    each wave streams straight into registers; the waves of a workgroup split
-//    K and add their sums in LDS.
+//  * gemm_fp4_kernel, tiles staged through LDS, on v_mfma_scale_f32_32x32x64:
+//    bound by how fast a CU's loads arrive (8192^3 250 us, 4.4 PFLOP/s; 172 to
+//    184 us with the loads taken out, 249 with the LDS reads taken out).
+//  * gemm_fp4_skinny_kernel for few rows, on v_mfma_scale_f32_16x16x128: bound by
+//    the bytes of B (1 x 28672 x 8192 27 us, 4.6 TB/s), which each wave streams
+//    straight into registers; the waves of a workgroup split K and add their
+//    sums in LDS.
+// In both, a lane supplies the 32 k-values of one row and block as 16 bytes
+// and the scale byte of exactly that block.
 #include <atomic>
 #include <type_traits>
 #include <utility>
@@ -118,23 +116,27 @@ __device__ __forceinline__ void store_row(unsigned short* p, const float (&v)[W]
 
 // ------------------------------------------------------------ tiles in LDS
 //
-// Four waves, 2 x 2, each TM x TN of the tile.  A slab is 256 deep: 128 bytes
-// of each row of A and of B, so every global access is whole 128-byte lines,
-// and the scale words of its two 128-deep groups.  A ring of NST slabs in LDS
-// is filled by hand-issued buffer_load ... lds (gemm_device.hpp); the loads of
-// slab g + NST - 1 are spread over the first MFMAs of a slab period, across
-// tiles too.
+// 2 x WN waves, each TM x TN of the tile.  A slab is 256 deep: 128 bytes of
+// each row of A and of B, so every global access is whole 128-byte lines (64-byte
+// pieces of twice the rows: 8192^3 290 -> 326 us), and the scale words of its
+// two 128-deep groups.  A ring of NST slabs in LDS is filled by hand-issued
+// buffer_load ... lds (gemm_device.hpp); the loads of slab g + NST - 1 are
+// spread over the MFMAs of a slab period, across tiles too.  What a load costs
+// is its instruction more than its bytes (8192^3 at four waves: 184 us with
+// none, 204 with the scales' alone, 270 with the operands', 290 with both), so
+// all are 16 bytes a lane.  At 256 x 256, eight waves are level with four on
+// long K and gain 6% where K is short (3000 x 7000 x 2048 46 -> 43 us): two waves
+// on a SIMD cover each other's barriers and stores.
 //
-// Both operands have 128-byte rows in LDS, chunk-swizzled like A of the fp8
-// kernel: a ds_read_b128 is served 16 lanes at a time, here 16 consecutive
-// rows at one 16-byte chunk, which the XOR with (row >> 1) spreads over the 16
-// slots of a 256-byte window.
-//
-// Scales: the load of the scale words permutes rows so that the words of row
-// l of all the wave's 16-row blocks stand side by side in LDS: a lane reads
-// four blocks' words with one ds_read_b128 and gathers its own byte of each
-// into one register (v_perm), from which the MFMA selects by opsel.  Byte
-// reads per block would be four times the LDS instructions.
+// Which rows make up an MFMA block is free, and chosen so that a lane's scale
+// words and its results are consecutive: block b of a wave holds every SM-th
+// (SN-th) row, from row b on.  A lane then reads the words of all its blocks
+// with one ds_read_b128 (b64 for two blocks) from words that came in memory
+// order, gathers its own byte of each into one register (v_perm), from which
+// the MFMA selects by opsel, and stores SN consecutive columns, 32 lanes a
+// stretch of 32 * SN of a row of C.  (Blocks of consecutive rows, words loaded
+// four bytes a lane to reorder them: 8192^3 274 us, 256 x 28672 x 8192 55 against
+// 260 and 47.)
 template <int BM, int BN, int NST_, int WN_>
 struct Shape {
   static constexpr int NST = NST_;
@@ -787,9 +789,13 @@ bool gemm_fp4_eligible(int bm, int bn, long long M, long long N, long long K) {
   return rows * (K / 2) < (1LL << 31) && M < (1LL << 28) && N < (1LL << 28);
 }
 
-// The tile of the least estimated time, in units of what a CU needs for one
-// 256-deep slab (measured with all CUs busy: 256 x 256 2.0 us, 256 x 128 1.15,
-// two workgroups of 128 x 128 1.3, one of them 0.75), times the rounds of tiles.
+// The tile of the least estimated time: the rounds of tiles times what a CU
+// needs for one, us for a 256-deep slab and for the stores (measured with all
+// CUs busy: 256 x 256 2.0 and 5, 256 x 128 1.15 and 5, two workgroups of 128 x
+// 128 1.3 and 4, one of them 0.75 and 4).  256 x 256 / 256 x 128 / 128 x 128
+// measured: 8192^3 250 / 288 / 296 us, 4096^3 41 / 45 / 46, 2048 x 4096 x 4096
+// 32 / 27 / 26, 1024 x 8192 x 8192 53 / 42 / 44, 512 x 8192 x 8192 47 / 34 / 27,
+// 3000 x 7000 x 2048 to fp32 44 / 46 / 47, 700 x 5000 x 1408 19 / 18 / 12.
 // Up to 64 rows the streaming kernel, unless more than half of the CUs get a
 // 128 x 128 tile: past 16 rows its re-reading of A costs more than the tile's
 // idle rows (64 x 28672 x 8192 65.8 against 35.4 us, 64 x 8192 x 8192 18.3
@@ -804,8 +810,9 @@ void gemm_fp4_default_tile(long long M, long long N, long long K, int cus, int& 
   }
   auto rounds = [](long long t, long long slots) { return (double)((t + slots - 1) / slots); };
   const long long t = tiles(128, 128);
-  const double big = rounds(tiles(256, 256), cus) * 2.0, mid = rounds(tiles(256, 128), cus) * 1.15;
-  const double small = t <= cus ? 0.75 : rounds(t, 2LL * cus) * 1.3;
+  const double slabs = (double)((K + BK - 1) / BK);
+  const double big = rounds(tiles(256, 256), cus) * (2.0 * slabs + 5), mid = rounds(tiles(256, 128), cus) * (1.15 * slabs + 5);
+  const double small = t <= cus ? 0.75 * slabs + 4 : rounds(t, 2LL * cus) * (1.3 * slabs + 4);
   bm = small < big && small < mid ? 128 : 256;
   bn = bm == 256 && big <= mid ? 256 : 128;
 }

