@@ -77,20 +77,21 @@ __device__ __forceinline__ void store_f32x4(float* row, int64_t c, int64_t n, f3
   }
 }
 // W (2 or 4) columns at p, those before `left`; non-temporal where NT.
-template <bool NT, class V>
-__device__ __forceinline__ void store_vec(V* p, V v) {
-  if constexpr (NT)
-    __builtin_nontemporal_store(v, p);
-  else
-    *p = v;
-}
+// (Macro: a template would drop the alignment of the typedefs above.)
+#define PGK_STORE(NT, type, p, ...)                                               \
+  do {                                                                            \
+    if constexpr (NT)                                                             \
+      __builtin_nontemporal_store(__VA_ARGS__, reinterpret_cast<type*>(p));       \
+    else                                                                          \
+      *reinterpret_cast<type*>(p) = __VA_ARGS__;                                  \
+  } while (0)
 template <int W, bool NT>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[W], int64_t left) {
   if (left >= W) {
     if constexpr (W == 4)
-      store_vec<NT>(reinterpret_cast<u32x4_a4*>(p), __builtin_bit_cast(u32x4_a4, f32x4{v[0], v[1], v[2], v[3]}));
+      PGK_STORE(NT, u32x4_a4, p, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
     else
-      store_vec<NT>(reinterpret_cast<u32x2_a4*>(p), __builtin_bit_cast(u32x2_a4, f32x2{v[0], v[1]}));
+      PGK_STORE(NT, u32x2_a4, p, __builtin_bit_cast(u32x2, f32x2{v[0], v[1]}));
   } else {
 #pragma unroll
     for (int e = 0; e < W - 1; ++e)
@@ -104,9 +105,9 @@ __device__ __forceinline__ void store_row(unsigned short* p, const float (&v)[W]
   for (int e = 0; e < W / 2; ++e) o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
   if (left >= W) {
     if constexpr (W == 4)
-      store_vec<NT>(reinterpret_cast<u32x2_a2*>(p), u32x2_a2{o[0], o[1]});
+      PGK_STORE(NT, u32x2_a2, p, u32x2{o[0], o[1]});
     else
-      store_vec<NT>(reinterpret_cast<u32_a2*>(p), (u32_a2)o[0]);
+      PGK_STORE(NT, u32_a2, p, o[0]);
   } else {
 #pragma unroll
     for (int e = 0; e < W - 1; ++e)
@@ -595,8 +596,8 @@ __global__ void __launch_bounds__(128 * WN) gemm_fp4_kernel(GemmParams P) {
 template <int SM, int SN, int DEPTH, bool GRP>
 __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmParams P) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  f32x4* s_part = reinterpret_cast<f32x4*>(smem);  // [waves][SN][SM][64]
-  __shared__ int s_tile;
+  f32x4* s_part = reinterpret_cast<f32x4*>(smem);  // [2][waves][SN][SM][64], by the tile's parity
+  __shared__ int s_tile[2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, kb = lane >> 4;
@@ -609,24 +610,13 @@ __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmPar
     t_start = wall_ticks();
     c_start = shader_cycles();
   }
-  struct Unit {
-    u32x4 b[2][SN], a[2][SM];
-    unsigned sb[2][SN], sa[2][SM];
+  struct Tile {
+    void* C;
+    int M, N, m0, n0;
+    const uint8_t *A, *B, *sa, *sb;
+    int rowb, steps, ra, rb, u0, u1;
   };
-  int it = 0, v = 0;
-  for (;; ++it) {
-    if (tid == 0) s_tile = it == 0 ? walker.first() : walker.next(v);
-    __syncthreads();
-    v = __builtin_amdgcn_readfirstlane(s_tile);
-    if (v < 0) break;
-    if (tid == 0) {
-      if (witness) {
-        atomicAdd(P.w.visits + v, 1);
-        P.w.owner[v] = prog;
-        P.w.order[v] = it;
-      }
-      if (is_straggler(P.s, prog)) spin_ns(P.s.straggler_ns, P.s.wall_khz);
-    }
+  auto open = [&](int v, Tile& t) {
     GemmProblem pr;
     int pm, pn;
     if (GRP) {
@@ -646,51 +636,88 @@ __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmPar
       pr.K = P.K;
       walker.tile_coords(v, pm, pn);
     }
-    const int m0 = pm * 16 * SM, n0 = pn * 16 * SN;
-    const int rowb = pr.K >> 1, steps = pr.K >> 7;
-    const int ra = pr.M - m0 < 16 * SM ? pr.M - m0 : 16 * SM, rb = pr.N - n0 < 16 * SN ? pr.N - n0 : 16 * SN;
-    // rows past the operands read as zeros (range checks)
-    const auto rA = rsrc(static_cast<const uint8_t*>(pr.A) + (size_t)m0 * rowb, (unsigned)(ra * rowb));
-    const auto rB = rsrc(static_cast<const uint8_t*>(pr.B) + (size_t)n0 * rowb, (unsigned)(rb * rowb));
-    const unsigned off = (unsigned)l16 * (unsigned)rowb + (unsigned)kb * 16u;
-    const unsigned soff = (unsigned)(l16 * 4 + kb);
-    auto load = [&](int u, Unit& x) PGK_INLINE {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int st = u * 2 + s;
-        const bool in = st < steps;  // uniform
-        const unsigned at = in ? off + (unsigned)st * 64u : kOob;
-        const auto rSA = rsrc(pr.sa + ((size_t)(in ? st : 0) * pr.M + m0) * 4, (unsigned)(ra * 4));
-        const auto rSB = rsrc(pr.sb + ((size_t)(in ? st : 0) * pr.N + n0) * 4, (unsigned)(rb * 4));
-#pragma unroll
-        for (int j = 0; j < SN; ++j) {
-          x.b[s][j] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB, at + (unsigned)(j * 16) * (unsigned)rowb, 0, 0));
-          x.sb[s][j] = __builtin_amdgcn_raw_buffer_load_b8(rSB, soff + j * 64, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < SM; ++i) {
-          x.a[s][i] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, at + (unsigned)(i * 16) * (unsigned)rowb, 0, 0));
-          x.sa[s][i] = __builtin_amdgcn_raw_buffer_load_b8(rSA, soff + i * 64, 0, 0);
-        }
-      }
-    };
-    f32x4 acc[SN][SM] = {};
+    t.C = pr.C;
+    t.M = pr.M;
+    t.N = pr.N;
+    t.m0 = pm * 16 * SM;
+    t.n0 = pn * 16 * SN;
+    t.rowb = pr.K >> 1;
+    t.steps = pr.K >> 7;
+    t.ra = pr.M - t.m0 < 16 * SM ? pr.M - t.m0 : 16 * SM;
+    t.rb = pr.N - t.n0 < 16 * SN ? pr.N - t.n0 : 16 * SN;
+    t.A = static_cast<const uint8_t*>(pr.A) + (size_t)t.m0 * t.rowb;
+    t.B = static_cast<const uint8_t*>(pr.B) + (size_t)t.n0 * t.rowb;
+    t.sa = pr.sa + (size_t)t.m0 * 4;
+    t.sb = pr.sb + (size_t)t.n0 * 4;
     // the wave's units: a consecutive stretch, so that a row's lines are read
     // one after the other
-    const int units = (steps + 1) >> 1, u0 = units * wave / waves, u1 = units * (wave + 1) / waves;
-    Unit x[DEPTH];
+    const int units = (t.steps + 1) >> 1;
+    t.u0 = units * wave / waves;
+    t.u1 = units * (wave + 1) / waves;
+  };
+  struct Unit {
+    u32x4 b[2][SN], a[2][SM];
+    unsigned sb[2][SN], sa[2][SM];
+  };
+  // Unit u of a tile; rows past the operands read as zeros (range checks).
+  auto load = [&](const Tile& t, int u, Unit& x) PGK_INLINE {
+    const auto rA = rsrc(t.A, (unsigned)(t.ra * t.rowb));
+    const auto rB = rsrc(t.B, (unsigned)(t.rb * t.rowb));
+    const unsigned off = (unsigned)l16 * (unsigned)t.rowb + (unsigned)kb * 16u;
+    const unsigned soff = (unsigned)(l16 * 4 + kb);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int st = u * 2 + s;
+      const bool in = st < t.steps;  // uniform
+      const unsigned at = in ? off + (unsigned)st * 64u : kOob;
+      const auto rSA = rsrc(t.sa + (size_t)(in ? st : 0) * t.M * 4, (unsigned)(t.ra * 4));
+      const auto rSB = rsrc(t.sb + (size_t)(in ? st : 0) * t.N * 4, (unsigned)(t.rb * 4));
+#pragma unroll
+      for (int j = 0; j < SN; ++j) {
+        x.b[s][j] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB, at + (unsigned)(j * 16) * (unsigned)t.rowb, 0, 0));
+        x.sb[s][j] = __builtin_amdgcn_raw_buffer_load_b8(rSB, soff + j * 64, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < SM; ++i) {
+        x.a[s][i] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, at + (unsigned)(i * 16) * (unsigned)t.rowb, 0, 0));
+        x.sa[s][i] = __builtin_amdgcn_raw_buffer_load_b8(rSA, soff + i * 64, 0, 0);
+      }
+    }
+  };
+  Tile t;
+  Unit x[DEPTH];
+  auto begin = [&](int v) PGK_INLINE {
+    open(v, t);
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
-      if (u0 + d < u1) load(u0 + d, x[d]);
-    for (int u = u0; u < u1; u += DEPTH) {
+      if (t.u0 + d < t.u1) load(t, t.u0 + d, x[d]);
+  };
+  if (tid == 0) s_tile[0] = walker.first();
+  __syncthreads();
+  int v = __builtin_amdgcn_readfirstlane(s_tile[0]);
+  if (v >= 0) begin(v);
+  int it = 0;
+  while (v >= 0) {
+    const int par = it & 1;
+    if (tid == 0) {
+      s_tile[par ^ 1] = walker.next(v);
+      if (witness) {
+        atomicAdd(P.w.visits + v, 1);
+        P.w.owner[v] = prog;
+        P.w.order[v] = it;
+      }
+      if (is_straggler(P.s, prog)) spin_ns(P.s.straggler_ns, P.s.wall_khz);
+    }
+    f32x4 acc[SN][SM] = {};
+    for (int u = t.u0; u < t.u1; u += DEPTH) {
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
-        if (u + d >= u1) break;
+        if (u + d >= t.u1) break;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if ((u + d) * 2 + s >= steps) break;
+          if ((u + d) * 2 + s >= t.steps) break;
 #pragma unroll
           for (int j = 0; j < SN; ++j)
 #pragma unroll
@@ -699,34 +726,45 @@ __global__ void __launch_bounds__(kMaxWaves * 64) gemm_fp4_skinny_kernel(GemmPar
                                             __builtin_bit_cast(i32x4, x[d].a[s][i]), acc[j][i], (int)x[d].sb[s][j],
                                             (int)x[d].sa[s][i]);
         }
-        if (u + DEPTH + d < u1) load(u + DEPTH + d, x[d]);
+        if (u + DEPTH + d < t.u1) load(t, u + DEPTH + d, x[d]);
       }
     }
+    f32x4* part = s_part + par * waves * SN * SM * 64;
 #pragma unroll
     for (int j = 0; j < SN; ++j)
 #pragma unroll
-      for (int i = 0; i < SM; ++i) s_part[((wave * SN + j) * SM + i) * 64 + lane] = acc[j][i];
+      for (int i = 0; i < SM; ++i) part[((wave * SN + j) * SM + i) * 64 + lane] = acc[j][i];
+    // every wave's sums and the next tile; the sums of the tile before were
+    // read before the barrier, so that two sets are enough
     __syncthreads();
+    void* const C = t.C;
+    const int M = t.M, N = t.N, m0 = t.m0, n0 = t.n0;
+    v = __builtin_amdgcn_readfirstlane(s_tile[par ^ 1]);
+    ++it;
+    // Tiles of 16 columns have the next one's first units on their way
+    // meanwhile (1 x 2048 x 8192 8.7 -> 7.7 us); at 32 columns the registers that
+    // holds cost more than it hides (1 x 28672 x 8192 31.6 -> 33.1).
+    if (SN == 1 && v >= 0) begin(v);
     for (int q = wave; q < SN * SM; q += waves) {
-      f32x4 s = s_part[q * 64 + lane];
-      for (int w = 1; w < waves; ++w) s += s_part[(w * SN * SM + q) * 64 + lane];
+      f32x4 s = part[q * 64 + lane];
+      for (int w = 1; w < waves; ++w) s += part[(w * SN * SM + q) * 64 + lane];
       const int64_t m = m0 + (q % SM) * 16 + l16, n = n0 + (q / SM) * 16 + 4 * kb;
-      if (m >= pr.M) continue;
+      if (m >= M) continue;
       if (P.out_f32) {
-        store_f32x4(static_cast<float*>(pr.C) + m * pr.N, n, pr.N, s);
+        store_f32x4(static_cast<float*>(C) + m * N, n, N, s);
       } else {
-        unsigned short* row = static_cast<unsigned short*>(pr.C) + m * pr.N;
+        unsigned short* row = static_cast<unsigned short*>(C) + m * N;
         const unsigned lo = pack_bf16x2(s[0], s[1]), hi = pack_bf16x2(s[2], s[3]);
-        typedef unsigned u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
-        if (n + 4 <= pr.N) {
-          *reinterpret_cast<u32x2_a2*>(row + n) = u32x2_a2{lo, hi};
+        if (n + 4 <= N) {
+          *reinterpret_cast<u32x2_a2*>(row + n) = u32x2{lo, hi};
         } else {
-          if (n < pr.N) row[n] = (unsigned short)lo;
-          if (n + 1 < pr.N) row[n + 1] = (unsigned short)(lo >> 16);
-          if (n + 2 < pr.N) row[n + 2] = (unsigned short)hi;
+          if (n < N) row[n] = (unsigned short)lo;
+          if (n + 1 < N) row[n + 1] = (unsigned short)(lo >> 16);
+          if (n + 2 < N) row[n + 2] = (unsigned short)hi;
         }
       }
     }
+    if (SN != 1 && v >= 0) begin(v);
   }
   if (witness && tid == 0) {
     P.w.t_start[prog] = t_start;
@@ -758,7 +796,7 @@ Instance tiled() {
 }
 template <int SM, int SN, int DEPTH>
 Instance skinny(int waves) {
-  return {SM * 16, SN * 16, waves * 64, waves * SM * SN * 1024,
+  return {SM * 16, SN * 16, waves * 64, 2 * waves * SM * SN * 1024,
           {gemm_fp4_skinny_kernel<SM, SN, DEPTH, false>, gemm_fp4_skinny_kernel<SM, SN, DEPTH, true>}};
 }
 
@@ -799,13 +837,15 @@ bool gemm_fp4_eligible(int bm, int bn, long long M, long long N, long long K) {
 // Up to 64 rows the streaming kernel, unless more than half of the CUs get a
 // 128 x 128 tile: past 16 rows its re-reading of A costs more than the tile's
 // idle rows (64 x 28672 x 8192 65.8 against 35.4 us, 64 x 8192 x 8192 18.3
-// against 23.9).
+// against 23.9).  Tiles of 16 columns and eight waves while every tile has a CU
+// (1 x 4096 x 14336 11.3 us against 14.2 with 32 columns and four; 1 x 8192 x 8192
+// 14.1 against 10.8).
 void gemm_fp4_default_tile(long long M, long long N, long long K, int cus, int& bm, int& bn, int& bk) {
   bk = BK;
   auto tiles = [&](int m, int n) { return (M + m - 1) / m * ((N + n - 1) / n); };
   if (M <= 16 || (M <= 64 && 2 * tiles(128, 128) <= cus)) {
     bm = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    bn = bm == 16 && N <= 16LL * 4 * cus ? 16 : 32;
+    bn = bm == 16 && N <= 16LL * cus ? 16 : 32;
     return;
   }
   auto rounds = [](long long t, long long slots) { return (double)((t + slots - 1) / slots); };
