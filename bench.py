@@ -55,22 +55,22 @@ BF16_SOURCES = ["gemm_bf16_lds.hip", "gemm_device.hpp", "common.hpp", "sched.hpp
 FP8_SOURCES = ["gemm_fp8.hip", "gemm_device.hpp", "common.hpp", "sched.hpp", "runtime.hip"]
 ADD_SOURCES = ["padd.hip", "common.hpp", "sched.hpp", "runtime.hip"]
 TRAFFIC = {
-    "bf16_8192cube_work_stealing": {"sources": BF16_SOURCES, "sha256_16": "6ad34d738c399914",
-        "read_bytes": 1610946752, "write_bytes": 186131840},
-    "fp8_8192cube_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "c29722996871b668",
-        "read_bytes": 811933376, "write_bytes": 144911136},
-    "fp8_256x28672x8192_128x256_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "c29722996871b668",
-        "read_bytes": 253829248, "write_bytes": 14680320},
-    "fp8_256x28672x8192_128x256_grouped": {"sources": FP8_SOURCES, "sha256_16": "c29722996871b668",
-        "read_bytes": 253793792, "write_bytes": 14680064},
-    "add_8192sq_128x128_blocked": {"sources": ADD_SOURCES, "sha256_16": "e9c3685c3537e947",
-        "read_bytes": 536905728, "write_bytes": 268644352},
-    "add_8192sq_128x128_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "e9c3685c3537e947",
-        "read_bytes": 536960000, "write_bytes": 268485120},
-    "add_8192sq_32x16_blocked": {"sources": ADD_SOURCES, "sha256_16": "e9c3685c3537e947",
-        "read_bytes": 1073797120, "write_bytes": 268435456},
-    "add_8192sq_32x16_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "e9c3685c3537e947",
-        "read_bytes": 536980160, "write_bytes": 320627072},
+    "bf16_8192cube_work_stealing": {"sources": BF16_SOURCES, "sha256_16": "dde99983cd65c934",
+        "read_bytes": 1611021248, "write_bytes": 189075776},
+    "fp8_8192cube_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "df49f027541c068b",
+        "read_bytes": 811950208, "write_bytes": 146007776},
+    "fp8_256x28672x8192_128x256_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "df49f027541c068b",
+        "read_bytes": 253829120, "write_bytes": 14680320},
+    "fp8_256x28672x8192_128x256_grouped": {"sources": FP8_SOURCES, "sha256_16": "df49f027541c068b",
+        "read_bytes": 253792768, "write_bytes": 14680064},
+    "add_8192sq_128x128_blocked": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
+        "read_bytes": 536904192, "write_bytes": 268653056},
+    "add_8192sq_128x128_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
+        "read_bytes": 536958976, "write_bytes": 268505344},
+    "add_8192sq_32x16_blocked": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
+        "read_bytes": 1073796096, "write_bytes": 268435456},
+    "add_8192sq_32x16_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
+        "read_bytes": 536979968, "write_bytes": 321761792},
 }
 
 
