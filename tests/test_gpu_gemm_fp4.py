@@ -65,6 +65,59 @@ def test_default_tile_any_shape(dtype):
         check(run(qa, sa, qb, sb, M, N, K, dtype, "grouped"), Cref, Abs, K, dtype, (M, N, K))
 
 
+TILES = [(256, 256), (256, 128), (128, 128), (64, 32), (32, 32), (16, 32), (16, 16)]
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("dtype", list(OUTS))
+def test_every_tile_on_ragged_shapes(tile, dtype):
+    """Every built tile: edges in M and N, one to six K groups (odd ones end
+    inside a slab), C rows that start on a line (N = 512) or not, and eight
+    programs, so that each walks several tiles and the loads run on across
+    them."""
+    for i, (M, N, K) in enumerate([(5, 7, 128), (259, 263, 384), (513, 512, 256), (270, 512, 640), (600, 777, 768)]):
+        if tile[0] <= 64 and M > 300:
+            M = M // 8
+        qa, sa = operand(M, K, 500 + i)
+        qb, sb = operand(N, K, 600 + i)
+        Cref, Abs = mx.gemm_mxfp4(qa, sa, qb, sb)
+        for sched, grid in (("grouped", 0), ("interleaved", 8), ("work_stealing", 8)):
+            C = run(qa, sa, qb, sb, M, N, K, dtype, sched, tile=tile + (256,), grid=grid)
+            check(C, Cref, Abs, K, dtype, (tile, M, N, K, sched))
+
+
+def test_more_tiles_than_cus_and_fewer_give_the_same_bits():
+    """128 x 128 tiles take another ring depth where no CU gets two of them: the
+    columns that both launches share have the same sums in the same order."""
+    M, K, wide, few = 260, 640, 16500, 900
+    qa, sa = operand(M, K, 1)
+    qb, sb = operand(wide, K, 2)
+    A = run(qa, sa, qb, sb, M, wide, K, "mxfp4_out_f32", "grouped", tile=(128, 128, 256))
+    B = run(qa, sa, qb[:few].copy(), sb[:, :few].copy(), M, few, K, "mxfp4_out_f32", "grouped", tile=(128, 128, 256))
+    a, b = A.as_f64().reshape(M, wide), B.as_f64().reshape(M, few)
+    assert np.array_equal(a[:, :few], b)
+    Cref, Abs = mx.gemm_mxfp4(qa, sa, qb[-few:].copy(), sb[:, -few:].copy())
+    assert np.all(np.abs(a[:, -few:] - Cref) <= K / 128 * 2.0 ** -22 * Abs)
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_grouped_problems_on_every_tile(tile):
+    shapes = [(70, 130, 256), (1, 257, 640), (290, 512, 384)]
+    ops, outs = [], []
+    for i, (M, N, K) in enumerate(shapes):
+        qa, sa = operand(M, K, 70 + i)
+        qb, sb = operand(N, K, 80 + i)
+        C = Guarded(M * N, "bf16")
+        outs.append((C, qa, sa, qb, sb, M, N, K))
+        ops.append((dev_u8(qa), dev_u8(qb), C.view, M, N, K, dev_u8(sa), dev_u8(sb)))
+    note(f"grouped mxfp4 {tile}")
+    pg.pgemm_run_grouped(config(), ops, "mxfp4_out_bf16", "work_stealing", pg.make_args(tile=tile + (256,)))
+    sync()
+    for C, qa, sa, qb, sb, M, N, K in outs:
+        assert C.guards_intact()
+        check(C, *mx.gemm_mxfp4(qa, sa, qb, sb), K, "mxfp4_out_bf16", (tile, M, N, K))
+
+
 @pytest.mark.parametrize("sched", SCHEDS)
 def test_schedulers_agree(sched):
     for M, N, K in [(1, 700, 512), (40, 2100, 384), (700, 1100, 640)]:
