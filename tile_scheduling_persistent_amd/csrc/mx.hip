@@ -2,9 +2,11 @@
 // columns, and the way back.  Each is one pass over the data: a block's
 // largest magnitude, its scale byte (integer arithmetic on the magnitude's
 // bits) and the conversion, which on gfx950 is one instruction for two values.
-// All three are bound by memory: 8192 x 8192 bf16 there and back, 340 MB, in 67
-// us (5.1 TB/s, a copy's rate); 5000 x 7000 fp32 transposed and back, 247 MB, in
-// 57 us.
+// All three are bound by memory: 8192 x 8192 bf16 there and back, 340 MB, in 56
+// us (6.1 TB/s); 5000 x 7000 fp32 transposed and back, 247 MB, in 55.5 us.  Where
+// the tiles fill the device, the wide side (values read, values written back)
+// goes past the caches, non-temporal: 68 us there and back without, 57 with
+// either; codes and scales stay for the product.
 #include "common.hpp"
 #include "mx_device.hpp"
 
@@ -38,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p) {
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
       const int64_t row = row0 + r < p.rows ? row0 + r : p.rows - 1;
-      v[r] = vec8_load<T>(static_cast<const char*>(p.X) + row * p.ldx * esz, c, p.cols);
+      v[r] = vec8_load<T, false, RW == 8>(static_cast<const char*>(p.X) + row * p.ldx * esz, c, p.cols);
     }
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(DequantParams p) {
       if (row0 + r >= p.rows) break;
       float x[8];
       e2m1_values(code[r], byte[r], x);
-      vec8_store<T>(static_cast<char*>(p.Y) + (row0 + r) * p.ldy * esz, c, p.cols, vec8_pack<T>(x));
+      vec8_store<T, false, RW == 8>(static_cast<char*>(p.Y) + (row0 + r) * p.ldy * esz, c, p.cols, vec8_pack<T>(x));
     }
   }
 }

@@ -123,7 +123,7 @@ struct Quad<2> {
 // Elements i .. i + 7 of a row that ends at `n` (elements past it zero).
 // WHOLE: n is a multiple of 8, as i is, and the code for a vector's part falls
 // away.
-template <int T, bool WHOLE = false>
+template <int T, bool WHOLE = false, bool NT = false>
 __device__ __forceinline__ Vec8<T> vec8_load(const void* row, int64_t i, int64_t n) {
   constexpr int esz = T == kTypeF32 ? 4 : 2;
   Vec8<T> v;
@@ -132,7 +132,12 @@ __device__ __forceinline__ Vec8<T> vec8_load(const void* row, int64_t i, int64_t
   if (i + 8 <= n) {
     const auto* p = reinterpret_cast<const typename Quad<esz>::type*>(static_cast<const char*>(row) + i * esz);
 #pragma unroll
-    for (int q = 0; q < esz / 2; ++q) v.q[q] = p[q];
+    for (int q = 0; q < esz / 2; ++q) {
+      if constexpr (NT)
+        v.q[q] = __builtin_nontemporal_load(p + q);
+      else
+        v.q[q] = p[q];
+    }
   } else if (!WHOLE && i < n) {
 #pragma unroll
     for (int e = 0; e < 7; ++e) {
@@ -146,13 +151,18 @@ __device__ __forceinline__ Vec8<T> vec8_load(const void* row, int64_t i, int64_t
   return v;
 }
 
-template <int T, bool WHOLE = false>
+template <int T, bool WHOLE = false, bool NT = false>
 __device__ __forceinline__ void vec8_store(void* row, int64_t i, int64_t n, const Vec8<T>& v) {
   constexpr int esz = T == kTypeF32 ? 4 : 2;
   if (i + 8 <= n) {
     auto* p = reinterpret_cast<typename Quad<esz>::type*>(static_cast<char*>(row) + i * esz);
 #pragma unroll
-    for (int q = 0; q < esz / 2; ++q) p[q] = v.q[q];
+    for (int q = 0; q < esz / 2; ++q) {
+      if constexpr (NT)
+        __builtin_nontemporal_store(v.q[q], p + q);
+      else
+        p[q] = v.q[q];
+    }
   } else if (!WHOLE && i < n) {
 #pragma unroll
     for (int e = 0; e < 7; ++e) {

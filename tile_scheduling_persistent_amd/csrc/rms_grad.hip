@@ -27,6 +27,8 @@ struct GradRow {
   float rstd;
 };
 
+// The inputs' last use: non-temporal (8192 x 8192 bf16 108.7 -> 103.9 us; dx
+// stored that way too 106).
 template <int YT, int HT, int VPT>
 __device__ __forceinline__ void load_row(const RmsGradParams& p, int64_t row, int L, int t0,
                                          GradRow<YT, HT, VPT>& g) {
@@ -35,9 +37,9 @@ __device__ __forceinline__ void load_row(const RmsGradParams& p, int64_t row, in
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int64_t c = ((int64_t)v * L + t0) * 8;
-    g.dy[v] = vec8_load<YT>(static_cast<const char*>(p.dY) + row * p.ldy * ysz, c, p.cols);
-    g.h[v] = vec8_load<HT>(static_cast<const char*>(p.H) + row * p.ldh * hsz, c, p.cols);
-    if (p.dH) g.dh[v] = vec8_load<HT>(static_cast<const char*>(p.dH) + row * p.ldd * hsz, c, p.cols);
+    g.dy[v] = vec8_load<YT, false, true>(static_cast<const char*>(p.dY) + row * p.ldy * ysz, c, p.cols);
+    g.h[v] = vec8_load<HT, false, true>(static_cast<const char*>(p.H) + row * p.ldh * hsz, c, p.cols);
+    if (p.dH) g.dh[v] = vec8_load<HT, false, true>(static_cast<const char*>(p.dH) + row * p.ldd * hsz, c, p.cols);
   }
 }
 
