@@ -5,10 +5,10 @@
 //
 // Two kernels:
 //  * gemm_fp4_kernel, tiles staged through LDS, on v_mfma_scale_f32_32x32x64:
-//    bound by how fast a CU's loads arrive (8192^3 250 us, 4.4 PFLOP/s; 172 to
-//    184 us with the loads taken out, 249 with the LDS reads taken out).
+//    bound by how fast a CU's loads arrive (8192^3 239 to 250 us, 4.4 to 4.6
+//    PFLOP/s; 172 to 184 us with the loads taken out).
 //  * gemm_fp4_skinny_kernel for few rows, on v_mfma_scale_f32_16x16x128: bound by
-//    the bytes of B (1 x 28672 x 8192 27 us, 4.6 TB/s), which each wave streams
+//    the bytes of B (1 x 28672 x 8192 26 to 32 us, 3.9 to 4.75 TB/s), which each wave streams
 //    straight into registers; the waves of a workgroup split K and add their
 //    sums in LDS.
 // In both, a lane supplies the 32 k-values of one row and block as 16 bytes

@@ -3,8 +3,8 @@
 //
 // One pass over the data: a row's h = x + r stays in registers between the sum
 // of squares and the output, and its blocks' scale exponents are found there
-// too.  Bound by memory (8192 x 8192 bf16 with residual to e4m3: 470 MB in 101 us,
-// 4.7 TB/s, where a copy of that size reaches 5.2); the arithmetic is in 64 bits (which gfx950 runs at
+// too.  Bound by memory (8192 x 8192 bf16 with residual to e4m3: 470 MB in 84 to
+// 94 us, 5.0 to 5.6 TB/s, where a copy of that size reaches 5.2); the arithmetic is in 64 bits (which gfx950 runs at
 // the rate of unpacked 32-bit operations), because the quantised outputs round
 // at borders: y in fp32 would now and then be on the other side of one, and a
 // scale byte off by one is a factor of two.

@@ -9,7 +9,7 @@
 // (fp32) over the whole walk and leave once, as one row of partial sums.  The
 // next row's loads go out before this row's sum is waited for.  A second
 // kernel adds the partial sums in a fixed order: results repeat bit for bit.
-// Bound by memory: 8192 x 8192 bf16 with dh, 537 MB, in 104 to 108 us, 5.0 to 5.2
+// Bound by memory: 8192 x 8192 bf16 with dh, 537 MB, in 100 to 105 us, 5.1 to 5.4
 // TB/s, a copy's rate.  One workgroup per CU: more of them leave more partial
 // sums than they hide.
 #include "common.hpp"
