@@ -55,13 +55,13 @@ BF16_SOURCES = ["gemm_bf16_lds.hip", "gemm_device.hpp", "common.hpp", "sched.hpp
 FP8_SOURCES = ["gemm_fp8.hip", "gemm_device.hpp", "common.hpp", "sched.hpp", "runtime.hip"]
 ADD_SOURCES = ["padd.hip", "common.hpp", "sched.hpp", "runtime.hip"]
 TRAFFIC = {
-    "bf16_8192cube_work_stealing": {"sources": BF16_SOURCES, "sha256_16": "dde99983cd65c934",
+    "bf16_8192cube_work_stealing": {"sources": BF16_SOURCES, "sha256_16": "709390e41d996896",
         "read_bytes": 1611021248, "write_bytes": 189075776},
-    "fp8_8192cube_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "df49f027541c068b",
+    "fp8_8192cube_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "4d1033e50b242ee0",
         "read_bytes": 811950208, "write_bytes": 146007776},
-    "fp8_256x28672x8192_128x256_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "df49f027541c068b",
+    "fp8_256x28672x8192_128x256_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "4d1033e50b242ee0",
         "read_bytes": 253829120, "write_bytes": 14680320},
-    "fp8_256x28672x8192_128x256_grouped": {"sources": FP8_SOURCES, "sha256_16": "df49f027541c068b",
+    "fp8_256x28672x8192_128x256_grouped": {"sources": FP8_SOURCES, "sha256_16": "4d1033e50b242ee0",
         "read_bytes": 253792768, "write_bytes": 14680064},
     "add_8192sq_128x128_blocked": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
         "read_bytes": 536904192, "write_bytes": 268653056},

@@ -70,13 +70,6 @@ __device__ __forceinline__ void load_lds_u8(rsrc_words_t r, unsigned lds_address
   asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_ubyte %1, %2, 0 offen lds"
                :: "s"(lds_address), "v"(voff), "s"(r) : "memory", "m0");
 }
-
-// buffer_load_dword ... lds: one dword per lane from byte offset voff to the
-// LDS dword at M0 + 4 * lane.
-__device__ __forceinline__ void load_lds4(rsrc_words_t r, unsigned lds_address, unsigned voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :: "s"(lds_address), "v"(voff), "s"(r) : "memory", "m0");
-}
 #pragma clang diagnostic pop
 
 __device__ __forceinline__ void load_lds16(rsrc_words_t r, unsigned char* lds_dst, unsigned voff) {

@@ -46,29 +46,9 @@ __device__ __forceinline__ float scale_value(unsigned byte) {
 typedef __bf16 bf16x2_d __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2_d __attribute__((ext_vector_type(2)));
 typedef float f32x2_d __attribute__((ext_vector_type(2)));
-typedef float f32x4_d __attribute__((ext_vector_type(4)));
 typedef short s16x2_d __attribute__((ext_vector_type(2)));
 typedef unsigned u32x2_d __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4_d __attribute__((ext_vector_type(4)));
-
-// Element i of a matrix of element type T as fp32.
-template <int T>
-__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
-  if (T == kTypeF32) return static_cast<const float*>(p)[i];
-  if (T == kTypeBF16)
-    return __builtin_bit_cast(float, (unsigned)static_cast<const unsigned short*>(p)[i] << 16);
-  return (float)static_cast<const _Float16*>(p)[i];
-}
-
-template <int T>
-__device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
-  if (T == kTypeF32)
-    static_cast<float*>(p)[i] = v;
-  else if (T == kTypeBF16)
-    static_cast<__bf16*>(p)[i] = (__bf16)v;
-  else
-    static_cast<_Float16*>(p)[i] = (_Float16)v;
-}
 
 // Eight consecutive elements as stored: 16 bytes (16-bit types) or 32 (fp32).
 template <int T>
