@@ -510,9 +510,16 @@ PGEMM_API pgemm_status prms_run(pgemm_config* cfg, const void* X, int x_type, in
  * x and r.  Sums in fp32 in an order that depends on the sizes only, so results
  * repeat bit for bit.  dX may be dH exactly, or dY exactly if the types are
  * the same (same stride).  The partial sums of dW live in a buffer of 64 MiB
- * that the config allocates when it is created and keeps in place (calls with
- * dW on one config must not overlap in time): PGEMM_ERR_UNSUPPORTED if one
- * row of cols floats does not fit there.  rows == 0 writes zeros to dW. */
+ * that the config allocates when it is created and keeps in place:
+ * PGEMM_ERR_UNSUPPORTED if one row of cols floats does not fit there.  Calls
+ * with dW on several streams use it one after the other: the config's first one
+ * on a second stream synchronises the device (PGEMM_ERR_DEVICE, nothing
+ * enqueued, if that fails, as it does while another stream is being captured),
+ * and from then on each waits on its stream for the one before.  A captured
+ * call cannot wait so and takes another part of the buffer (up to 131072
+ * columns): replays may run beside eager calls, but two captured calls with dW of
+ * one config, in one graph or two, must be ordered by the caller.  rows == 0
+ * writes zeros to dW. */
 PGEMM_API pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_t ldy, const void* H,
                            int h_type, int64_t ldh, const void* dH, int64_t ldd, const void* W, int w_type,
                            const float* rstd, int64_t rows, int64_t cols, void* dX, int64_t ldx,

@@ -499,7 +499,10 @@ def prms_run(cfg: Config, X, W, Y, rows: int, cols: int, eps: float = 1e-6, R=No
 def prms_grad_run(cfg: Config, dY, H, W, rstd, dX, dW, rows: int, cols: int, dH=None, stream=None):
     """Gradients of prms_run (asynchronous on `stream`): dX [rows][cols] of H's
     type (the gradient of X and of R), dW float32 [cols] (None: not wanted).  H:
-    the forward's h; dH: the gradient that reaches h past the norm (None: none)."""
+    the forward's h; dH: the gradient that reaches h past the norm (None: none).
+    Calls with dW share the config's buffer of partial sums: on several streams
+    each waits for the one before (the first on a second stream synchronises the
+    device); captured ones of one config must not be replayed at the same time."""
     rows, cols = int(rows), int(cols)
     yt, ht, wt = _elem(dY, "dY"), _elem(H, "H"), _elem(W, "W")
     if _elem(dX, "dX") != ht or (dH is not None and _elem(dH, "dH") != ht):
