@@ -28,7 +28,7 @@ constexpr int64_t kMaxGrid = 1 << 20;
 template <int T, int RW>
 __global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p) {
   constexpr int ROWS = 4 * RW;
-  __shared__ unsigned char s_scale[4][ROWS][4];
+  __shared__ __attribute__((aligned(4))) unsigned char s_scale[4][ROWS][4];  // read as words
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t groups = (p.cols + 127) / 128, ctiles = (groups + 3) / 4;
   const int64_t tiles = (p.rows + ROWS - 1) / ROWS * ctiles;
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) quant_transposed_kernel(QuantParams 
   constexpr int CPL = T == kTypeF32 ? 1 : 2, COLS = 64 * CPL;
   constexpr int PITCH = 128 + 16;  // bytes of a column's codes in LDS: 16-byte accesses of 16 lanes meet all banks
   __shared__ __attribute__((aligned(16))) unsigned char s_codes[COLS * PITCH];
-  __shared__ unsigned char s_scale[2][COLS][4];
+  __shared__ __attribute__((aligned(4))) unsigned char s_scale[2][COLS][4];  // read as words
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t groups = (p.rows + 127) / 128, rtiles = (groups + 1) / 2, ctiles = (p.cols + COLS - 1) / COLS;
   for (int64_t tile = blockIdx.x; tile < rtiles * ctiles; tile += gridDim.x) {
