@@ -39,6 +39,20 @@ def test_quant_of_many_rows(kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+def test_quant_of_many_rows_that_start_on_lines(kind):
+    cols, ld = COLS - 3, 3008
+    x, _ = data(kind)
+    big = torch.full((ROWS, ld), float("nan"), dtype=TYPES[kind], device="cuda:0")
+    big[:, :cols] = x[:, :cols]
+    assert big.data_ptr() % 128 == 0
+    v = x[:, :cols].double().cpu().numpy()
+    for rule in ("ceil", "floor"):
+        q, s = quant(big[:, :cols], ROWS, cols, False, rule)
+        qr, sr = mx.quant_mxfp4(v, rule)
+        assert np.array_equal(s, sr) and np.array_equal(q, qr), rule
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
 def test_dequant_of_many_rows(kind):
     _, want = data(kind)
     q, s = want["ceil"]

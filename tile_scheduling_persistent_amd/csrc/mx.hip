@@ -2,11 +2,21 @@
 // columns, and the way back.  Each is one pass over the data: a block's
 // largest magnitude, its scale byte (integer arithmetic on the magnitude's
 // bits) and the conversion, which on gfx950 is one instruction for two values.
-// All three are bound by memory: 8192 x 8192 bf16 there and back, 340 MB, in 56
-// us (6.1 TB/s); 5000 x 7000 fp32 transposed and back, 247 MB, in 55.5 us.  Where
-// the tiles fill the device, the wide side (values read, values written back)
-// goes past the caches, non-temporal: 68 us there and back without, 57 with
-// either; codes and scales stay for the product.
+// All three are bound by memory: 8192 x 8192 bf16 there and back, 340 MB, in 55
+// us (6.2 TB/s); 5000 x 7000 fp32 transposed and back, 247 MB, in 55 us.
+//
+// Where the tiles fill the device, the wide side goes past the caches,
+// non-temporal, if a wave's instructions cover whole lines of it; codes and scales
+// stay for the product.  us, plain -> non-temporal, one call on cold data:
+//  * values read, 16-bit rows that start on 16 bytes: 8192 x 8192 33.7 -> 29.6,
+//    5000 x 7000 22.8 -> 21.6 (4096 x 2056, whose last tile is 8 columns, 9.2 ->
+//    10.2); fp32 rows that start on 128-byte lines: 8192 x 8192 60.4 -> 58.0.
+//    Other rows have lines that two waves share, which come from memory twice:
+//    8192 x 8191 bf16 79.4 -> 83.6, 4096 x 2051 bf16 11.0 -> 12.5, fp32 12.8 -> 14.9.
+//  * values written back, 16 bits: 8192 x 8192 36.0 -> 26.2, 8192 x 8191 50.6 ->
+//    38.8.  A store of fp32 covers half of each line: 8192 x 8192 80.0 -> 124.5.
+// A reader that follows at once finds them in memory instead: both directions of
+// 8192 x 8192 bf16 54.4 -> 62.0, values back and a norm of them 80.0 -> 86.3.
 #include "common.hpp"
 #include "mx_device.hpp"
 
@@ -25,7 +35,7 @@ constexpr int64_t kMaxGrid = 1 << 20;
 // bytes.  The scale bytes of the tile are collected in LDS, because in memory
 // the four bytes of a row's 128 columns stand next to those of the next row:
 // 32 rows are one 128-byte line.
-template <int T, int RW>
+template <int T, int RW, bool NT>
 __global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p) {
   constexpr int ROWS = 4 * RW;
   __shared__ __attribute__((aligned(4))) unsigned char s_scale[4][ROWS][4];  // read as words
@@ -40,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p) {
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
       const int64_t row = row0 + r < p.rows ? row0 + r : p.rows - 1;
-      v[r] = vec8_load<T, false, RW == 8>(static_cast<const char*>(p.X) + row * p.ldx * esz, c, p.cols);
+      v[r] = vec8_load<T, false, NT>(static_cast<const char*>(p.X) + row * p.ldx * esz, c, p.cols);
     }
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(DequantParams p) {
       if (row0 + r >= p.rows) break;
       float x[8];
       e2m1_values(code[r], byte[r], x);
-      vec8_store<T, false, RW == 8>(static_cast<char*>(p.Y) + (row0 + r) * p.ldy * esz, c, p.cols, vec8_pack<T>(x));
+      vec8_store<T, false, RW == 8 && T != kTypeF32>(static_cast<char*>(p.Y) + (row0 + r) * p.ldy * esz, c, p.cols, vec8_pack<T>(x));
     }
   }
 }
@@ -198,10 +208,13 @@ void quant_typed(const QuantParams& p, hipStream_t stream) {
     const int64_t tiles = (p.rows + 255) / 256 * ((p.cols + COLS - 1) / COLS);
     hipLaunchKernelGGL(quant_transposed_kernel<T>, grid_of(tiles), dim3(kThreads), 0, stream, p);
   } else if (tall(p.rows, p.cols, p.cus)) {
-    hipLaunchKernelGGL((quant_kernel<T, 8>), grid_of((p.rows + 31) / 32 * ((p.cols + 511) / 512)), dim3(kThreads), 0,
-                       stream, p);
+    const dim3 grid = grid_of((p.rows + 31) / 32 * ((p.cols + 511) / 512));
+    if (T == kTypeF32 ? rows_at(p.X, p.ldx, 4, 128) : rows_at(p.X, p.ldx, 2, 16))
+      hipLaunchKernelGGL((quant_kernel<T, 8, true>), grid, dim3(kThreads), 0, stream, p);
+    else
+      hipLaunchKernelGGL((quant_kernel<T, 8, false>), grid, dim3(kThreads), 0, stream, p);
   } else {
-    hipLaunchKernelGGL((quant_kernel<T, 1>), grid_of((p.rows + 3) / 4 * ((p.cols + 511) / 512)), dim3(kThreads), 0,
+    hipLaunchKernelGGL((quant_kernel<T, 1, false>), grid_of((p.rows + 3) / 4 * ((p.cols + 511) / 512)), dim3(kThreads), 0,
                        stream, p);
   }
 }

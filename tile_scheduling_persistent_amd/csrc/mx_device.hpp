@@ -155,6 +155,11 @@ __device__ __forceinline__ void vec8_store(void* row, int64_t i, int64_t n, cons
   }
 }
 
+// Every row of a matrix starts at a multiple of `align` (a power of two) bytes.
+inline bool rows_at(const void* x, int64_t ld, int64_t esz, int64_t align) {
+  return (reinterpret_cast<uintptr_t>(x) & (uintptr_t)(align - 1)) == 0 && (ld * esz & (align - 1)) == 0;
+}
+
 // Largest over the 4 lanes of a quad, and over the 16 lanes of a row, in
 // every lane of it (data-parallel primitives: no LDS).
 __device__ __forceinline__ unsigned max_u32(unsigned a, unsigned b) { return a > b ? a : b; }
