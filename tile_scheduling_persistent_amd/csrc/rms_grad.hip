@@ -27,9 +27,12 @@ struct GradRow {
   float rstd;
 };
 
-// The inputs' last use: non-temporal (8192 x 8192 bf16 108.7 -> 103.9 us; dx
-// stored that way too 106).
-template <int YT, int HT, int VPT>
+// The inputs' last use: NT, those of 16 bits non-temporal, where their rows
+// start on 16 bytes (8192 x 8192 bf16 103.4 -> 98.4 us, with fp32 h 172.8 -> 166.3;
+// dx stored that way too costs 2 us).  Not where lines are shared by two loads,
+// which then fetch them twice: 8192 x 8191 bf16 215 -> 234; 8192 x 8192 all in fp32,
+// whose loads cover half of each line, 198 -> 209.
+template <bool NT, int YT, int HT, int VPT>
 __device__ __forceinline__ void load_row(const RmsGradParams& p, int64_t row, int L, int t0,
                                          GradRow<YT, HT, VPT>& g) {
   constexpr int ysz = YT == kTypeF32 ? 4 : 2, hsz = HT == kTypeF32 ? 4 : 2;
@@ -37,9 +40,9 @@ __device__ __forceinline__ void load_row(const RmsGradParams& p, int64_t row, in
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int64_t c = ((int64_t)v * L + t0) * 8;
-    g.dy[v] = vec8_load<YT, false, true>(static_cast<const char*>(p.dY) + row * p.ldy * ysz, c, p.cols);
-    g.h[v] = vec8_load<HT, false, true>(static_cast<const char*>(p.H) + row * p.ldh * hsz, c, p.cols);
-    if (p.dH) g.dh[v] = vec8_load<HT, false, true>(static_cast<const char*>(p.dH) + row * p.ldd * hsz, c, p.cols);
+    g.dy[v] = vec8_load<YT, false, NT && YT != kTypeF32>(static_cast<const char*>(p.dY) + row * p.ldy * ysz, c, p.cols);
+    g.h[v] = vec8_load<HT, false, NT && HT != kTypeF32>(static_cast<const char*>(p.H) + row * p.ldh * hsz, c, p.cols);
+    if (p.dH) g.dh[v] = vec8_load<HT, false, NT && HT != kTypeF32>(static_cast<const char*>(p.dH) + row * p.ldd * hsz, c, p.cols);
   }
 }
 
@@ -65,7 +68,7 @@ __device__ __forceinline__ void put_dx(const RmsGradParams& p, int64_t row, int6
   vec8_store<HT>(static_cast<char*>(p.dX) + row * p.ldx * (HT == kTypeF32 ? 4 : 2), c, p.cols, vec8_pack<HT>(d));
 }
 
-template <int YT, int HT, int VPT, bool AHEAD>
+template <int YT, int HT, int VPT, bool AHEAD, bool NT>
 __global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_kernel(RmsGradParams p, int L) {
   __shared__ float s_sum[2][16];
   __shared__ float s_dw[VPT == 1 ? kRmsMaxLanes * 8 : 1];
@@ -85,16 +88,16 @@ __global__ void __launch_bounds__(kRmsMaxLanes) rms_grad_kernel(RmsGradParams p,
     const int64_t row = j * per + sub;
     return row < p.rows ? row : p.rows - 1;
   };
-  if (AHEAD && i < n) load_row(p, row_at(i), L, t0, now);
+  if (AHEAD && i < n) load_row<NT>(p, row_at(i), L, t0, now);
   int turn = 0;
   for (; i < n; i += gridDim.x, turn ^= 1) {
     const bool on = i * per + sub < p.rows;
     const int64_t row = row_at(i);
     GradRow<YT, HT, VPT> next;
     if (AHEAD) {
-      if (i + gridDim.x < n) load_row(p, row_at(i + gridDim.x), L, t0, next);
+      if (i + gridDim.x < n) load_row<NT>(p, row_at(i + gridDim.x), L, t0, next);
     } else {
-      load_row(p, row, L, t0, now);
+      load_row<NT>(p, row, L, t0, now);
     }
     if (VPT != 1) load_w();  // two vectors leave no registers to keep it in
     const float r = now.rstd;
@@ -244,6 +247,14 @@ GradPlan grad_plan(int64_t rows, int64_t cols, int cus) {
   return g;
 }
 
+template <int YT, int HT, bool NT>
+void launch_rows(const RmsGradParams& p, const GradPlan& g, dim3 grid, dim3 threads, hipStream_t stream) {
+  if (g.vpt == 1)
+    hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 1, true, NT>), grid, threads, 0, stream, p, g.lanes);
+  else
+    hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 2, false, NT>), grid, threads, 0, stream, p, g.lanes);
+}
+
 template <int YT, int HT>
 void launch_typed(const RmsGradParams& p, hipStream_t stream) {
   const GradPlan g = grad_plan(p.rows, p.cols, p.cus);
@@ -257,10 +268,12 @@ void launch_typed(const RmsGradParams& p, hipStream_t stream) {
     hipLaunchKernelGGL((rms_grad_long_dx_kernel<YT, HT>), dim3(rows), dim3(kRmsMaxLanes), 0, stream, p);
   } else if (p.rows > 0) {
     const dim3 grid((unsigned)(p.dW ? p.partials : g.grid)), threads(g.threads);
-    if (g.vpt == 1)
-      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 1, true>), grid, threads, 0, stream, p, g.lanes);
+    const bool at16 = (YT == kTypeF32 || rows_at(p.dY, p.ldy, 2, 16)) &&
+                      (HT == kTypeF32 || (rows_at(p.H, p.ldh, 2, 16) && (!p.dH || rows_at(p.dH, p.ldd, 2, 16))));
+    if (YT != kTypeF32 && at16)
+      launch_rows<YT, HT, YT != kTypeF32>(p, g, grid, threads, stream);
     else
-      hipLaunchKernelGGL((rms_grad_kernel<YT, HT, 2, false>), grid, threads, 0, stream, p, g.lanes);
+      launch_rows<YT, HT, false>(p, g, grid, threads, stream);
   }
   if (p.dW) {
     const int64_t n = (p.cols + 31) / 32;
