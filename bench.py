@@ -55,22 +55,22 @@ BF16_SOURCES = ["gemm_bf16_lds.hip", "gemm_device.hpp", "common.hpp", "sched.hpp
 FP8_SOURCES = ["gemm_fp8.hip", "gemm_device.hpp", "common.hpp", "sched.hpp", "runtime.hip"]
 ADD_SOURCES = ["padd.hip", "common.hpp", "sched.hpp", "runtime.hip"]
 TRAFFIC = {
-    "bf16_8192cube_work_stealing": {"sources": BF16_SOURCES, "sha256_16": "709390e41d996896",
-        "read_bytes": 1611021248, "write_bytes": 189075776},
-    "fp8_8192cube_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "4d1033e50b242ee0",
-        "read_bytes": 811950208, "write_bytes": 146007776},
-    "fp8_256x28672x8192_128x256_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "4d1033e50b242ee0",
+    "bf16_8192cube_work_stealing": {"sources": BF16_SOURCES, "sha256_16": "b3b2aa4e5ca28008",
+        "read_bytes": 1610865088, "write_bytes": 190599168},
+    "fp8_8192cube_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "31f97acf80ced61d",
+        "read_bytes": 811854720, "write_bytes": 145126528},
+    "fp8_256x28672x8192_128x256_work_stealing": {"sources": FP8_SOURCES, "sha256_16": "31f97acf80ced61d",
         "read_bytes": 253829120, "write_bytes": 14680320},
-    "fp8_256x28672x8192_128x256_grouped": {"sources": FP8_SOURCES, "sha256_16": "4d1033e50b242ee0",
+    "fp8_256x28672x8192_128x256_grouped": {"sources": FP8_SOURCES, "sha256_16": "31f97acf80ced61d",
         "read_bytes": 253792768, "write_bytes": 14680064},
-    "add_8192sq_128x128_blocked": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
-        "read_bytes": 536904192, "write_bytes": 268653056},
-    "add_8192sq_128x128_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
-        "read_bytes": 536958976, "write_bytes": 268505344},
-    "add_8192sq_32x16_blocked": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
+    "add_8192sq_128x128_blocked": {"sources": ADD_SOURCES, "sha256_16": "7f963d4df0943756",
+        "read_bytes": 536904192, "write_bytes": 268601856},
+    "add_8192sq_128x128_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "7f963d4df0943756",
+        "read_bytes": 536958976, "write_bytes": 268498944},
+    "add_8192sq_32x16_blocked": {"sources": ADD_SOURCES, "sha256_16": "7f963d4df0943756",
         "read_bytes": 1073796096, "write_bytes": 268435456},
-    "add_8192sq_32x16_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "7c74a6dbf91d8314",
-        "read_bytes": 536979968, "write_bytes": 321761792},
+    "add_8192sq_32x16_work_stealing": {"sources": ADD_SOURCES, "sha256_16": "7f963d4df0943756",
+        "read_bytes": 536979136, "write_bytes": 320488256},
 }
 
 

@@ -427,15 +427,19 @@ PGEMM_API pgemm_status pgemm_plan_add(pgemm_config* cfg, const float* X, const f
                             pgemm_sched sched, const pgemm_args* args, pgemm_plan* out);
 
 /* ---- Operands of the block-scaled GEMMs ---------------------------------
- * Entry points that make, undo and feed the quantised operands above.  All
- * follow pgemm_run's rules: argument errors are reported before anything is
+ * Entry points that make and undo the quantised operands above: both operands
+ * of the MXFP4 product, and of the fp8 product A, as the norm's output (B comes
+ * from the caller).  All follow pgemm_run's rules: argument errors are reported before anything is
  * enqueued (NULL pointers, negative sizes, row strides below the row's length,
  * buffers that do not lie inside one device allocation of the config's
  * device, overlaps not named as allowed: PGEMM_ERR_INVALID; type combinations
  * not built: PGEMM_ERR_UNSUPPORTED), calls are asynchronous on hip_stream,
  * allocate nothing and may be captured into a graph.  rows == 0 is a call
- * with no rows (row buffers may then be NULL).  Buffers need the alignment
- * of their elements only; 16-byte aligned rows take the wide accesses. */
+ * with no rows (row buffers may then be NULL).  Matrices need the alignment of
+ * their elements only, codes and scales what each call states; accesses are 16
+ * bytes wide at any alignment, and fastest where rows start on 128-byte lines.
+ * prms_grad_run with dW uses memory of the config, as stated there; the other
+ * calls use none and may run on several streams at once. */
 
 /* Element types of pmx_* and prms_* matrices. */
 #define PMX_F32 0
@@ -491,7 +495,8 @@ PGEMM_API pgemm_status pmx_dequant_run(pgemm_config* cfg, const uint8_t* Q, cons
  * [cols] w_type (x_type or PMX_F32); ld*: row strides in elements (ldy: of
  * PRMS_OUT_SAME; the quantised forms are dense, Kp = cols rounded up to 128,
  * padding zero).  The norm is taken of h as stored, in 64 bits, so y is the
- * correctly rounded value of the formula.  H may be R, or X if the types and
+ * correctly rounded value of the formula (a y below 2^-126 may be rounded
+ * twice, the first time to a multiple of 2^-149).  H may be R, or X if the types and
  * strides are the same, exactly (in place); Y may be X exactly under
  * PRMS_OUT_SAME with the same stride.  Quantised Y and y_scale 4-byte (e4m3:
  * Y 8-byte) aligned (PGEMM_ERR_UNSUPPORTED otherwise). */

@@ -460,7 +460,8 @@ def prms_run(cfg: Config, X, W, Y, rows: int, cols: int, eps: float = 1e-6, R=No
     (Y e4m3 [rows][Kp], y_scale [Kp/128][rows]: the A operand of a block-scaled
     fp8 GEMM) or "mxfp4" (Y codes [rows][Kp/2], y_scale [Kp/128][rows][4]), Kp =
     cols rounded up to 128.  rstd (float32 [rows]) takes the rows' factors for
-    prms_grad_run.  H may be R (or X), Y (out="same") may be X."""
+    prms_grad_run.  H may be R (or X), Y (out="same") may be X.  The matrices and
+    W are tensors (their types are the call's types)."""
     rows, cols = int(rows), int(cols)
     o = RMS_OUTPUTS[out] if isinstance(out, str) else int(out)
     xt, wt = _elem(X, "X"), _elem(W, "W")

@@ -5,8 +5,9 @@
 //
 // Two kernels:
 //  * gemm_fp4_kernel, tiles staged through LDS, on v_mfma_scale_f32_32x32x64:
-//    bound by how fast a CU's loads arrive (8192^3 239 to 250 us, 4.4 to 4.6
-//    PFLOP/s; 172 to 184 us with the loads taken out).
+//    bound by how fast a CU's loads arrive (8192^3 237 to 257 us, 4.3 to 4.6
+//    PFLOP/s, the first fifty calls of a run the slowest; 172 to 184 us with the
+//    loads taken out).
 //  * gemm_fp4_skinny_kernel for few rows, on v_mfma_scale_f32_16x16x128: bound by
 //    the bytes of B (1 x 28672 x 8192 26 to 32 us, 3.9 to 4.75 TB/s), which each wave streams
 //    straight into registers; the waves of a workgroup split K and add their
@@ -464,8 +465,10 @@ __global__ void __launch_bounds__(128 * WN) gemm_fp4_kernel(GemmParams P) {
   };
   // Non-temporal where rows of C start on 128-byte lines, so that C does not
   // push operand panels out of L2 (8192^3 260 -> 250 us, 2000 x 28672 x 512 to
-  // fp32 58 -> 51; partial lines cost more than that: 3000 x 7000 x 2048 to fp32
-  // 44 against 48).
+  // fp32 58 -> 51; 2048 x 4096 x 2048 18.3 -> 17.2, 1024 x 2048 x 1024 9.0 -> 8.7;
+  // partial lines cost more than that: 3000 x 7000 x 2048 to fp32 44 against 48).
+  // With a norm of C that follows at once, 4096 x 4096 x 4096 63.3 -> 65.8 us together
+  // and 8192^3 338 -> 331.
   auto epilogue = [&](int m0, int n0) {
     const bool edge = m0 + BM > Mc || n0 + BN > Nc;
     const bool lines = (Nc & (P.out_f32 ? 31 : 63)) == 0 && (reinterpret_cast<uintptr_t>(Cc) & 127) == 0;

@@ -4,8 +4,9 @@
 // One pass over the data: a row's h = x + r stays in registers between the sum
 // of squares and the output, and its blocks' scale exponents are found there
 // too.  Bound by memory (8192 x 8192 bf16 with residual to e4m3: 470 MB in 84 to
-// 94 us, 5.0 to 5.6 TB/s, where a copy of that size reaches 5.2); the arithmetic is in 64 bits (which gfx950 runs at
-// the rate of unpacked 32-bit operations), because the quantised outputs round
+// 98 us, 4.8 to 5.6 TB/s, the first hundred calls of a run the slowest, where a
+// copy of that size reaches 5.2); the arithmetic is in 64 bits (which gfx950 runs
+// at the rate of unpacked 32-bit operations), because the quantised outputs round
 // at borders: y in fp32 would now and then be on the other side of one, and a
 // scale byte off by one is a factor of two.
 #include "common.hpp"
@@ -16,7 +17,8 @@ namespace {
 
 // y in 64 bits, as fp32 with the bits below the 20th of the fraction folded
 // into the last one (round to odd): whatever few bits the result is rounded to
-// next, it is rounded as from the 64-bit value.
+// next, it is rounded as from the 64-bit value.  (Below 2^-126 fp32 itself has
+// fewer bits, and the result may be rounded twice.)
 __device__ __forceinline__ float narrow_odd(double y) {
   const unsigned long long b = __builtin_bit_cast(unsigned long long, y);
   const unsigned lo = (unsigned)b, hi = (unsigned)(b >> 32);
@@ -137,9 +139,13 @@ __global__ void __launch_bounds__(VPT == 1 ? kRmsMaxLanes : kRmsMaxLanes / 2) rm
   const int64_t kp = (p.cols + 127) / 128 * 128;
   constexpr int xsz = XT == kTypeF32 ? 4 : 2, rsz = RT == kTypeF32 ? 4 : 2;
   // Rows that fill the device pass through the caches once: inputs of 16 bits and
-  // h non-temporal (8192 x 8192 bf16 to e4m3 98 -> 94 us, h alone 97; 4864 x 8000
-  // with r in fp32 107 -> 99 by h alone, 104 with r's loads too).  y stays for its
-  // product.
+  // h non-temporal (8192 x 8192 bf16 to e4m3 98 -> 94 us, h alone 97, to bf16 101 ->
+  // 88; 4864 x 8000 with r in fp32 107 -> 99 by h alone, 104 with r's loads too; 4096
+  // x 2056 20.0 -> 17.3, 2048 x 2048 level; rows at odd offsets, whose h stays in the
+  // caches, level: 8192 x 8191 152 -> 154).  A reader of h that follows at once, the
+  // next norm's residual, loses part of that on small tensors: two norms in a row
+  // 1024 x 4096 15.6 -> 16.8 us, 4096 x 4096 49 both ways, 8192 x 8192 175 -> 167.  y
+  // stays for its product.
   constexpr bool STREAM = VPT == 4;
   int turn = 0;
   for (unsigned i = blockIdx.x; i < g.n; i += gridDim.x, turn ^= 1) {
