@@ -1,6 +1,8 @@
 """Persistent tiled GEMM and persistent 2-D add with tile schedulers, and the
-operators that make the block-scaled GEMMs' operands (MXFP4 quantisation, RMS
-norm with a quantised output), for AMD Instinct MI355X (gfx950).
+operators that make the block-scaled GEMMs' operands (MXFP4 and e4m3
+quantisation, RMS norm with a quantised output), and layers of experts in e4m3
+(tokens sorted to experts and back, their products, gated activation, gradients),
+for AMD Instinct MI355X (gfx950).
 
 A thin Python binding over the C ABI of libpgemm.so (include/pgemm.h): the
 functions keep the C names, marshal torch device tensors (or raw device
@@ -38,7 +40,9 @@ RMS_OUTPUTS = {"same": _abi.PRMS_OUT_SAME, "fp8_b128": _abi.PRMS_OUT_FP8_B128, "
 
 __all__ = ["Config", "pgemm_run", "pgemm_run_noalloc", "pgemm_run_grouped", "padd_run", "padd_run_multi", "plan_gemm", "plan_add", "SCHEDULERS",
            "pmx_quant_run", "pmx_dequant_run", "prms_run", "prms_grad_run", "mxfp4_bytes", "SCALE_RULES",
-           "RMS_OUTPUTS", "DTYPES", "PgemmError", "status_str", "make_args"]
+           "pmoe_sort_run", "pmoe_gather_run", "pmoe_combine_run", "pmoe_combine_grad_run", "pfp8_quant_run",
+           "pfp8_quant_weights_run", "pgemm_run_experts", "pgemm_run_experts_wgrad", "pglu_run", "pglu_grad_run",
+           "fp8_bytes", "fp8_weight_bytes", "RMS_OUTPUTS", "DTYPES", "PgemmError", "status_str", "make_args"]
 
 
 def _check(where, code):
@@ -518,3 +522,225 @@ def prms_grad_run(cfg: Config, dY, H, W, rstd, dX, dW, rows: int, cols: int, dH=
                                     _ptr(dW, "dW", _F32, cols * 4) if dW is not None else None,
                                     _stream(stream, cfg.device))
     _check("prms_grad_run", code)
+
+
+# ------------------------------------------------------------- layers of experts
+
+_I32 = ("int32",)
+_FP8 = ("uint8", "float8_e4m3fn")
+
+
+def fp8_bytes(rows: int, cols: int) -> dict:
+    """Bytes of an e4m3 operand of a [rows][cols] matrix: Q [rows][Kp] and scale
+    [Kp/128][rows], Kp = cols rounded up to 128."""
+    kp = -(-cols // 128) * 128
+    return {"Q": rows * kp, "scale": kp // 128 * rows}
+
+
+def fp8_weight_bytes(experts: int, rows: int, cols: int) -> dict:
+    """Bytes of e4m3 weights [experts][rows][cols]: Q [experts][rows][Kp], scale
+    [experts][Rp/128][Kp/128], and the transposed Qt [experts][cols][Rp], scale_t
+    [experts][Kp/128][Rp/128]."""
+    rp, kp = -(-rows // 128) * 128, -(-cols // 128) * 128
+    s = experts * (rp // 128) * (kp // 128)
+    return {"Q": experts * rows * kp, "scale": s, "Qt": experts * cols * rp, "scale_t": s}
+
+
+def _opt(x, what, dtypes, nbytes):
+    return None if x is None else _ptr(x, what, dtypes, nbytes)
+
+
+def _out_of(out):
+    return RMS_OUTPUTS[out] if isinstance(out, str) else int(out)
+
+
+def _rows_out(out, Y, what, x_type, scale, rows, cols):
+    """(pointer, row stride, scale pointer) of an output under `out`."""
+    if out == _abi.PRMS_OUT_FP8_B128:
+        nb = fp8_bytes(rows, cols)
+        if scale is None:
+            raise ValueError(f"{what}: a quantised output needs its scales")
+        return _ptr(Y, what, _FP8, nb["Q"]), cols, _ptr(scale, what + " scale", _SCALE, nb["scale"])
+    if out == _abi.PRMS_OUT_SAME and not isinstance(Y, int) and _elem(Y, what) != x_type:
+        raise ValueError(f"{what}: must have the input's type")
+    y, ld = _matrix(Y, what, rows, cols)
+    return y, ld, None
+
+
+def pmoe_sort_run(cfg: Config, ids, place, order, offsets, tokens: int, topk: int, experts: int, ids_type=None,
+                  stream=None):
+    """Slots (token, choice) sorted by expert (asynchronous on `stream`): ids
+    [tokens][topk] int32 or int64 (outside [0, experts): no row) to place [tokens][topk]
+    (a slot's row or -1), order [tokens * topk] (a row's slot, -1 behind the last)
+    and offsets [experts + 1], all int32.  Rows of an expert keep their slots' order."""
+    tokens, topk, experts = int(tokens), int(topk), int(experts)
+    if ids_type is None:
+        ids_type = _abi.PMOE_I64 if str(getattr(ids, "dtype", "")) == "torch.int64" else _abi.PMOE_I32
+    slots = tokens * topk
+    code = _abi.lib().pmoe_sort_run(
+        cfg.handle, _ptr(ids, "ids", ("int64",) if ids_type == _abi.PMOE_I64 else _I32, slots * (8 if ids_type else 4)),
+        ids_type, tokens, topk, experts, _ptr(place, "place", _I32, slots * 4), _ptr(order, "order", _I32, slots * 4),
+        _ptr(offsets, "offsets", _I32, (experts + 1) * 4), _stream(stream, cfg.device))
+    _check("pmoe_sort_run", code)
+
+
+def pmoe_gather_run(cfg: Config, X, order, Y, tokens: int, topk: int, cols: int, out="same", y_scale=None, stream=None):
+    """Y[r] = X[order[r] / topk] for the tokens * topk rows (asynchronous on
+    `stream`): X [tokens][cols], Y of X's type or (out="fp8_b128") e4m3 with y_scale.
+    Rows without a slot are left as they were."""
+    tokens, topk, cols = int(tokens), int(topk), int(cols)
+    o, t, slots = _out_of(out), _elem(X, "X"), int(tokens) * int(topk)
+    x, ldx = _matrix(X, "X", tokens, cols)
+    y, ldy, s = _rows_out(o, Y, "Y", t, y_scale, slots, cols)
+    code = _abi.lib().pmoe_gather_run(cfg.handle, x, t, ldx, _ptr(order, "order", _I32, slots * 4), tokens, topk, cols, o,
+                                      y, ldy, s, _stream(stream, cfg.device))
+    _check("pmoe_gather_run", code)
+
+
+def pmoe_combine_run(cfg: Config, X, place, Y, tokens: int, topk: int, cols: int, weights=None, R=None, stream=None):
+    """Y[t] = R[t] + sum over j of weights[t][j] * X[place[t][j]] (asynchronous on
+    `stream`): X [tokens * topk][cols], weights float32 (None: ones), R (None: none)
+    and Y [tokens][cols] of X's type or float32.  Y may be R."""
+    tokens, topk, cols = int(tokens), int(topk), int(cols)
+    t, yt, slots = _elem(X, "X"), _elem(Y, "Y"), int(tokens) * int(topk)
+    x, ldx = _matrix(X, "X", slots, cols)
+    y, ldy = _matrix(Y, "Y", tokens, cols)
+    r, ldr = None, cols
+    if R is not None:
+        if _elem(R, "R") != yt:
+            raise ValueError("R: must have the type of Y")
+        r, ldr = _matrix(R, "R", tokens, cols)
+    code = _abi.lib().pmoe_combine_run(cfg.handle, x, t, ldx, _ptr(place, "place", _I32, slots * 4),
+                                       _opt(weights, "weights", _F32, slots * 4), r, ldr, y, yt, ldy, tokens, topk, cols,
+                                       _stream(stream, cfg.device))
+    _check("pmoe_combine_run", code)
+
+
+def pmoe_combine_grad_run(cfg: Config, dY, X, place, order, dX, tokens: int, topk: int, cols: int, weights=None, dW=None,
+                          out="same", dx_scale=None, stream=None):
+    """Gradients of pmoe_combine_run (asynchronous on `stream`): dX[r] = weights *
+    dY[token] by rows, of dY's type or (out="fp8_b128") e4m3 with dx_scale, and dW
+    float32 [tokens][topk] (None: not wanted, X may be None).  Rows without a slot are
+    left as they were."""
+    tokens, topk, cols = int(tokens), int(topk), int(cols)
+    o, t, slots = _out_of(out), _elem(dY, "dY"), int(tokens) * int(topk)
+    d, ldy = _matrix(dY, "dY", tokens, cols)
+    x, ldx = None, cols
+    if dW is not None:
+        if _elem(X, "X") != t:
+            raise ValueError("X: must have the type of dY")
+        x, ldx = _matrix(X, "X", slots, cols)
+    dx, lddx, s = _rows_out(o, dX, "dX", t, dx_scale, slots, cols)
+    code = _abi.lib().pmoe_combine_grad_run(
+        cfg.handle, d, t, ldy, x, ldx, _ptr(place, "place", _I32, slots * 4), _ptr(order, "order", _I32, slots * 4),
+        _opt(weights, "weights", _F32, slots * 4), tokens, topk, cols, o, dx, lddx, s, _opt(dW, "dW", _F32, slots * 4),
+        _stream(stream, cfg.device))
+    _check("pmoe_combine_grad_run", code)
+
+
+def pfp8_quant_run(cfg: Config, X, Q, scale, rows: int, cols: int, ldx=None, x_type=None, stream=None):
+    """e4m3 operand Q [rows][Kp] of X [rows][cols] (float32, bfloat16 or float16),
+    scale [Kp/128][rows] (asynchronous on `stream`)."""
+    rows, cols = int(rows), int(cols)
+    t, nb = _elem(X, "X", x_type), fp8_bytes(rows, cols)
+    x, ld = _matrix(X, "X", rows, cols, ldx)
+    code = _abi.lib().pfp8_quant_run(cfg.handle, x, t, rows, cols, ld, _ptr(Q, "Q", _FP8, nb["Q"]),
+                                     _ptr(scale, "scale", _SCALE, nb["scale"]), _stream(stream, cfg.device))
+    _check("pfp8_quant_run", code)
+
+
+def pfp8_quant_weights_run(cfg: Config, W, Q, scale, experts: int, rows: int, cols: int, Qt=None, scale_t=None,
+                           w_type=None, stream=None):
+    """e4m3 weights Q [experts][rows][Kp] of W [experts][rows][cols] with one scale
+    per block of 128 x 128, scale [experts][Rp/128][Kp/128], and with Qt
+    [experts][cols][Rp] and scale_t [experts][Kp/128][Rp/128] the transposed weights
+    (asynchronous on `stream`)."""
+    experts, rows, cols = int(experts), int(rows), int(cols)
+    t, nb = _elem(W, "W", w_type), fp8_weight_bytes(experts, rows, cols)
+    code = _abi.lib().pfp8_quant_weights_run(
+        cfg.handle, _ptr(W, "W", None, experts * rows * cols * (4 if t == 0 else 2)), t, experts, rows, cols,
+        _ptr(Q, "Q", _FP8, nb["Q"]), _ptr(scale, "scale", _SCALE, nb["scale"]), _opt(Qt, "Qt", _FP8, nb["Qt"]),
+        _opt(scale_t, "scale_t", _SCALE, nb["scale_t"]), _stream(stream, cfg.device))
+    _check("pfp8_quant_weights_run", code)
+
+
+def pgemm_run_experts(cfg: Config, A, B, C, rows: int, N: int, K: int, a_scale, b_scale, experts: int = 1, offsets=None,
+                      c_type=None, stream=None):
+    """C[r] = A[r] . B[e]^T, e the expert of row r by the device's offsets
+    (asynchronous on `stream`): A e4m3 [rows][K] with a_scale [K/128][rows], B e4m3
+    weights [experts][N][K] with b_scale, C [rows][N] bfloat16 or float32.  Rows of no
+    expert are left as they were."""
+    rows, N, K, experts = int(rows), int(N), int(K), int(experts)
+    t = _elem(C, "C", c_type)
+    nb = fp8_weight_bytes(experts, N, K)
+    code = _abi.lib().pgemm_run_experts(
+        cfg.handle, _ptr(A, "A", _FP8, rows * K), _ptr(a_scale, "a_scale", _SCALE, K // 128 * rows),
+        _ptr(B, "B", _FP8, nb["Q"]), _ptr(b_scale, "b_scale", _SCALE, nb["scale"]),
+        _ptr(C, "C", None, rows * N * (4 if t == 0 else 2)), t, rows, N, K, experts,
+        _opt(offsets, "offsets", _I32, (experts + 1) * 4), _stream(stream, cfg.device))
+    _check("pgemm_run_experts", code)
+
+
+def pgemm_run_experts_wgrad(cfg: Config, D, A, dB, rows: int, N: int, K: int, a_scale, d_scale=None, experts: int = 1,
+                            offsets=None, base=None, stream=None):
+    """dB[e] = base[e] + sum over the rows r of expert e of D[r]^T A[r] (asynchronous
+    on `stream`): D [rows][N] bfloat16, or e4m3 with d_scale; A e4m3 [rows][Kp] with
+    a_scale; base (None: zeros) and dB [experts][N][K] bfloat16 or float32.  base may
+    be dB."""
+    rows, N, K, experts = int(rows), int(N), int(K), int(experts)
+    if d_scale is not None:
+        nb = fp8_bytes(rows, N)
+        d, ldd, dt = _ptr(D, "D", _FP8, nb["Q"]), N, _abi.PMX_FP8_B128
+        ds = _ptr(d_scale, "d_scale", _SCALE, nb["scale"])
+    else:
+        dt, ds = _elem(D, "D"), None
+        d, ldd = _matrix(D, "D", rows, N)
+    bt, nb = _elem(dB, "dB"), fp8_bytes(rows, K)
+    size = experts * N * K * (4 if bt == 0 else 2)
+    if base is not None and _elem(base, "base") != bt:
+        raise ValueError("base: must have the type of dB")
+    code = _abi.lib().pgemm_run_experts_wgrad(
+        cfg.handle, d, dt, ldd, ds, _ptr(A, "A", _FP8, nb["Q"]), _ptr(a_scale, "a_scale", _SCALE, nb["scale"]),
+        _opt(base, "base", None, size), _ptr(dB, "dB", None, size), bt, rows, N, K, experts,
+        _opt(offsets, "offsets", _I32, (experts + 1) * 4), _stream(stream, cfg.device))
+    _check("pgemm_run_experts_wgrad", code)
+
+
+def pglu_run(cfg: Config, X, Y, rows: int, cols: int, out="same", y_scale=None, kept=None, kept_scale=None, valid=None,
+             stream=None):
+    """Y = silu(g) * u of X = [g | u] [rows][2 * cols] (asynchronous on `stream`), of
+    X's type or (out="fp8_b128") e4m3 with y_scale.  kept [rows][2][Kp] and kept_scale
+    [2][Kp/128][rows] take g and u in e4m3 for pglu_grad_run.  valid (int32 [1], on the
+    device): rows at or past it are left as they were."""
+    rows, cols = int(rows), int(cols)
+    o, t = _out_of(out), _elem(X, "X")
+    x, ldx = _matrix(X, "X", rows, 2 * cols)
+    y, ldy, s = _rows_out(o, Y, "Y", t, y_scale, rows, cols)
+    nb = fp8_bytes(rows, -(-cols // 128) * 256)
+    code = _abi.lib().pglu_run(cfg.handle, x, t, ldx, rows, cols, _opt(valid, "valid", _I32, 4), o, y, ldy, s,
+                               _opt(kept, "kept", _FP8, nb["Q"]), _opt(kept_scale, "kept_scale", _SCALE, nb["scale"]),
+                               _stream(stream, cfg.device))
+    _check("pglu_run", code)
+
+
+def pglu_grad_run(cfg: Config, dY, X, dX, rows: int, cols: int, x_scale=None, out="same", dx_scale=None, valid=None,
+                  stream=None):
+    """Gradient of pglu_run (asynchronous on `stream`): dY [rows][cols]; X the
+    forward's X of dY's type, or what it kept with x_scale = kept_scale; dX = [dg | du]
+    [rows][2 * cols] of dY's type or (out="fp8_b128", cols a multiple of 128) e4m3 with
+    dx_scale."""
+    rows, cols = int(rows), int(cols)
+    o, t = _out_of(out), _elem(dY, "dY")
+    d, ldy = _matrix(dY, "dY", rows, cols)
+    if x_scale is not None:
+        nb = fp8_bytes(rows, -(-cols // 128) * 256)
+        x, ldx, xs = _ptr(X, "X", _FP8, nb["Q"]), 2 * cols, _ptr(x_scale, "x_scale", _SCALE, nb["scale"])
+    else:
+        if _elem(X, "X") != t:
+            raise ValueError("X: must have the type of dY")
+        x, ldx = _matrix(X, "X", rows, 2 * cols)
+        xs = None
+    dx, lddx, s = _rows_out(o, dX, "dX", t, dx_scale, rows, 2 * cols)
+    code = _abi.lib().pglu_grad_run(cfg.handle, d, t, ldy, x, ldx, xs, rows, cols, _opt(valid, "valid", _I32, 4), o, dx,
+                                    lddx, s, _stream(stream, cfg.device))
+    _check("pglu_grad_run", code)

@@ -34,6 +34,10 @@ PIPELINE_DEFAULT, PIPELINE_FOUR_WAVE, PIPELINE_PINGPONG = 0, 1, 2
 PMX_F32, PMX_BF16, PMX_F16 = range(3)
 PMX_SCALE_CEIL, PMX_SCALE_FLOOR = range(2)
 PRMS_OUT_SAME, PRMS_OUT_FP8_B128, PRMS_OUT_MXFP4 = range(3)
+# layers of experts: the type of e4m3 rows, of pmoe_sort_run's ids, and the most experts
+PMX_FP8_B128 = 3
+PMOE_I32, PMOE_I64 = range(2)
+PMOE_MAX_EXPERTS = 1024
 # pgemm_args.program_order
 ORDER_DEFAULT, ORDER_DISPATCH, ORDER_XCD_MAJOR = 0, 1, 2
 
@@ -149,6 +153,27 @@ def lib() -> ctypes.CDLL:
     L.prms_grad_run.argtypes = [_cfg_p, vp, i32, i64, vp, i32, i64, vp, i64, vp, i32, vp, i64, i64, vp, i64,
                                 vp, vp]
     L.prms_grad_run.restype = st
+    L.pmoe_sort_run.argtypes = [_cfg_p, vp, i32, i64, i64, i32, vp, vp, vp, vp]
+    L.pmoe_sort_run.restype = st
+    L.pmoe_gather_run.argtypes = [_cfg_p, vp, i32, i64, vp, i64, i64, i64, i32, vp, i64, vp, vp]
+    L.pmoe_gather_run.restype = st
+    L.pmoe_combine_run.argtypes = [_cfg_p, vp, i32, i64, vp, vp, vp, i64, vp, i32, i64, i64, i64, i64, vp]
+    L.pmoe_combine_run.restype = st
+    L.pmoe_combine_grad_run.argtypes = [_cfg_p, vp, i32, i64, vp, i64, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp,
+                                        vp, vp]
+    L.pmoe_combine_grad_run.restype = st
+    L.pfp8_quant_run.argtypes = [_cfg_p, vp, i32, i64, i64, i64, vp, vp, vp]
+    L.pfp8_quant_run.restype = st
+    L.pfp8_quant_weights_run.argtypes = [_cfg_p, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]
+    L.pfp8_quant_weights_run.restype = st
+    L.pgemm_run_experts.argtypes = [_cfg_p, vp, vp, vp, vp, vp, i32, i64, i64, i64, i32, vp, vp]
+    L.pgemm_run_experts.restype = st
+    L.pgemm_run_experts_wgrad.argtypes = [_cfg_p, vp, i32, i64, vp, vp, vp, vp, vp, i32, i64, i64, i64, i32, vp, vp]
+    L.pgemm_run_experts_wgrad.restype = st
+    L.pglu_run.argtypes = [_cfg_p, vp, i32, i64, i64, i64, vp, i32, vp, i64, vp, vp, vp, vp]
+    L.pglu_run.restype = st
+    L.pglu_grad_run.argtypes = [_cfg_p, vp, i32, i64, vp, i64, vp, i64, i64, vp, i32, vp, i64, vp, vp]
+    L.pglu_grad_run.restype = st
     L.pgemm_witness_enable.argtypes = [_cfg_p, ctypes.c_int64, ctypes.c_int]
     L.pgemm_witness_enable.restype = st
     L.pgemm_witness_read.argtypes = [_cfg_p, ctypes.POINTER(pgemm_witness), ctypes.c_void_p]

@@ -161,6 +161,127 @@ struct RmsGradParams {
   int cus;
 };
 
+// e4m3 operands (pfp8_quant_run, pfp8_quant_weights_run).
+struct Fp8QuantParams {
+  const void* X;   // [rows][cols], row stride ldx
+  int type;
+  int64_t rows, cols, ldx;
+  uint8_t* Q;      // [rows][Kp]
+  uint8_t* scale;  // [Kp/128][rows]
+  int cus;
+};
+
+struct Fp8WeightsParams {
+  const void* X;     // [experts][rows][cols]
+  int type;
+  int64_t experts, rows, cols;
+  uint8_t* Q;        // [experts][rows][Kp]
+  uint8_t* scale;    // [experts][Rp/128][Kp/128]
+  uint8_t* Qt;       // [experts][cols][Rp], may be null
+  uint8_t* scale_t;  // [experts][Kp/128][Rp/128]
+};
+
+// Tokens routed to experts (pmoe_*).
+constexpr int kMaxExperts = 1024;
+constexpr int64_t kSortSmall = 16384;  // slots that one workgroup sorts
+struct SortParams {
+  const void* ids;  // [slots] int32 or int64
+  int ids64;
+  int64_t slots;
+  int experts, bits;  // bits: experts <= 2^bits
+  int* place;         // [slots]
+  int* order;         // [slots]
+  int* offsets;       // [experts + 1]
+  int64_t part;       // many slots: slots per workgroup
+  int parts;
+};
+
+struct GatherParams {
+  const void* X;     // [tokens][cols]
+  const int* order;  // [tokens * topk]
+  void* Y;           // [tokens * topk][cols], or e4m3 [..][Kp]
+  uint8_t* y_scale;  // null: Y of X's type
+  int type;
+  int64_t tokens, topk, cols, ldx, ldy;
+  int cus;
+};
+
+struct CombineParams {
+  const void* X;        // [tokens * topk][cols]
+  const int* place;     // [tokens][topk]
+  const float* weights; // [tokens][topk], may be null
+  const void* R;        // [tokens][cols], may be null
+  void* Y;              // [tokens][cols]
+  int type, y_type;
+  int64_t tokens, topk, cols, ldx, ldr, ldy;
+};
+
+struct CombineGradParams {
+  const void* dY;       // [tokens][cols]
+  const void* X;        // [tokens * topk][cols], may be null without dW
+  const int* place;
+  const int* order;
+  const float* weights; // may be null
+  void* dX;             // [tokens * topk][cols], or e4m3 [..][Kp]
+  uint8_t* dx_scale;    // null: dX of dY's type
+  float* dW;            // [tokens][topk], may be null
+  int type;
+  int64_t tokens, topk, cols, ldy, ldx, lddx;
+  int cus;
+};
+
+// The gated activation (pglu_*).
+struct GluParams {
+  const void* X;        // [rows][2 * cols]
+  int type;
+  int64_t rows, cols, ldx, ldy;
+  void* Y;              // [rows][cols], or e4m3 [rows][Kp]
+  uint8_t* y_scale;     // null: Y of X's type
+  uint8_t* kept;        // e4m3 [rows][2][Kp], may be null
+  uint8_t* kept_scale;  // [2][Kp/128][rows]
+  const int* valid;     // rows in use, may be null: all
+  int cus;
+};
+
+struct GluGradParams {
+  const void* dY;          // [rows][cols]
+  const void* X;           // [rows][2 * cols], or what glu_run kept
+  const uint8_t* x_scale;  // null: X of dY's type
+  int type;
+  int64_t rows, cols, ldy, ldx, lddx;
+  void* dX;                // [rows][2 * cols], or e4m3 [rows][2][Kp]
+  uint8_t* dx_scale;       // null: dX of dY's type
+  const int* valid;
+  int cus;
+};
+
+// The experts' products (pgemm_run_experts, pgemm_run_experts_wgrad).
+struct ExpertsParams {
+  const uint8_t* A;     // e4m3 [rows][K]
+  const uint8_t* sa;    // [K/128][rows]
+  const uint8_t* B;     // e4m3 [experts][N][K]
+  const uint8_t* sb;    // [experts][Np/128][K/128]
+  void* C;              // [rows][N]
+  const int* offsets;   // [experts + 1]; null: one expert, all rows
+  int rows, N, K, experts;
+  int out_f32;
+  int xcds;
+};
+
+struct WgradParams {
+  const void* D;        // [rows][N] bf16 (row stride ldd) or e4m3 [rows][Np]
+  const uint8_t* sd;    // null: D is bf16
+  const uint8_t* A;     // e4m3 [rows][Kp]
+  const uint8_t* sa;    // [Kp/128][rows]
+  const void* base;     // [experts][N][K] of dB's type, may be null
+  void* dB;             // [experts][N][K]
+  const int* offsets;
+  int rows, N, K, experts;
+  int64_t ldd;
+  int out_f32;
+  int xcds;
+};
+
 // Launchers: return hipErrorInvalidValue when no kernel is built for the
 // requested tile shape.
 hipError_t launch_gemm_bf16(const GemmParams& p, int bm, int bn, int bk, bool out_bf16,
@@ -176,6 +297,16 @@ hipError_t launch_dequant(const DequantParams& p, hipStream_t stream);
 hipError_t launch_rms(const RmsParams& p, hipStream_t stream);
 int rms_grad_partials(int64_t rows, int64_t cols, int cus);
 hipError_t launch_rms_grad(const RmsGradParams& p, hipStream_t stream);
+hipError_t launch_fp8_quant(const Fp8QuantParams& p, hipStream_t stream);
+hipError_t launch_fp8_quant_weights(const Fp8WeightsParams& p, hipStream_t stream);
+hipError_t launch_sort(const SortParams& p, hipStream_t stream);
+hipError_t launch_gather(const GatherParams& p, hipStream_t stream);
+hipError_t launch_combine(const CombineParams& p, hipStream_t stream);
+hipError_t launch_combine_grad(const CombineGradParams& p, hipStream_t stream);
+hipError_t launch_glu(const GluParams& p, hipStream_t stream);
+hipError_t launch_glu_grad(const GluGradParams& p, hipStream_t stream);
+hipError_t launch_gemm_experts(const ExpertsParams& p, int cus, hipStream_t stream);
+hipError_t launch_gemm_experts_wgrad(const WgradParams& p, int cus, hipStream_t stream);
 hipError_t launch_zero_i32(int* ptr, int n, hipStream_t stream);
 hipError_t launch_fill_i32(int* ptr, int n, int value, hipStream_t stream);
 bool gemm_bf16_tile_supported(int bm, int bn, int bk);

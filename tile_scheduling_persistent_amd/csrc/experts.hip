@@ -1,0 +1,454 @@
+// Tokens routed to experts: the slots (token, choice) sorted by expert, the
+// tokens' rows in that order, the experts' rows back at their tokens, and the
+// gradients of that.
+//
+// The sort is a stable counting sort, so its result does not depend on the order
+// in which waves run.  Everything else works row by row, and is bound by memory.
+// Indices that come from device memory are checked against the sizes of the call
+// before they are used: a wrong one leaves its row out.
+#include "common.hpp"
+#include "fp8_rows.hpp"
+
+namespace pgk {
+namespace {
+
+// ------------------------------------------------------------------- the sort
+//
+// A wave takes a stretch of consecutive slots.  Its lanes' counts per expert go
+// through LDS atomics (a sum, in any order); then, with the first row of each
+// wave's slots of each expert known, it walks its stretch again, 64 slots at a
+// time, and a slot's row is that first row plus the number of equal lanes below.
+
+template <typename I>
+__device__ __forceinline__ int expert_of(const SortParams& p, int64_t slot, int64_t end) {
+  if (slot >= end) return -1;
+  const int64_t e = (int64_t)static_cast<const I*>(p.ids)[slot];
+  return e >= 0 && e < p.experts ? (int)e : -1;
+}
+
+// Lanes with the same expert as this one (experts below 2^bits).
+__device__ __forceinline__ unsigned long long same_lanes(int e, int bits) {
+  unsigned long long m = __ballot(e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool on = (e >> b) & 1;
+    const unsigned long long v = __ballot(on);
+    m &= on ? v : ~v;
+  }
+  return m;
+}
+
+// Adds the slots [begin, end) to the wave's counts.
+template <typename I>
+__device__ __forceinline__ void count_slots(const SortParams& p, int64_t begin, int64_t end, int* cnt) {
+  for (int64_t s = begin + (threadIdx.x & 63); s < end; s += 64) {
+    const int e = expert_of<I>(p, s, end);
+    if (e >= 0) atomicAdd(cnt + e, 1);
+  }
+}
+
+// Rows of the slots [begin, end), from the wave's first rows `cnt`.
+template <typename I>
+__device__ __forceinline__ void place_slots(const SortParams& p, int64_t begin, int64_t end, int* cnt, bool order) {
+  const int lane = threadIdx.x & 63;
+  const unsigned long long below = (1ull << lane) - 1ull;
+  for (int64_t s0 = begin; s0 < end; s0 += 64) {
+    const int64_t s = s0 + lane;
+    const int e = expert_of<I>(p, s, end);
+    const unsigned long long m = same_lanes(e, p.bits);
+    const int first = e >= 0 ? __ffsll(m) - 1 : lane;
+    int row = 0;
+    if (e >= 0 && lane == first) row = atomicAdd(cnt + e, __popcll(m));
+    row = __shfl(row, first) + __popcll(m & below);
+    if (s < end) {
+      p.place[s] = e >= 0 ? row : -1;
+      if (order && e >= 0) p.order[row] = (int)s;
+    }
+  }
+}
+
+// Exclusive prefix sums over the workgroup's threads; *total: the sum.
+template <int THREADS>
+__device__ __forceinline__ int block_prefix(int v, int* s_wave, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 63) s_wave[wave] = x;
+  __syncthreads();
+  int base = 0, all = 0;
+  for (int w = 0; w < THREADS / 64; ++w) {
+    if (w < wave) base += s_wave[w];
+    all += s_wave[w];
+  }
+  *total = all;
+  __syncthreads();
+  return base + x - v;
+}
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+// Experts: one thread each.
+static_assert(kMaxExperts <= kSortThreads, "a thread per expert");
+
+// Few slots: one workgroup, one launch.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortParams p) {
+  extern __shared__ int s_cnt[];  // [waves][experts]
+  __shared__ int s_wave[kSortWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, E = p.experts;
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
+  __syncthreads();
+  const int64_t per = (p.slots + kSortThreads - 1) / kSortThreads * 64;
+  const int64_t begin = wave * per < p.slots ? wave * per : p.slots;
+  const int64_t end = begin + per < p.slots ? begin + per : p.slots;
+  count_slots<I>(p, begin, end, s_cnt + wave * E);
+  __syncthreads();
+  int mine = 0;
+  if (tid < E)
+    for (int w = 0; w < kSortWaves; ++w) mine += s_cnt[w * E + tid];
+  int total;
+  int at = block_prefix<kSortThreads>(mine, s_wave, &total);
+  if (tid < E) {
+    p.offsets[tid] = at;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = s_cnt[w * E + tid];
+      s_cnt[w * E + tid] = at;
+      at += n;
+    }
+  }
+  if (tid == 0) p.offsets[E] = total;
+  __syncthreads();
+  place_slots<I>(p, begin, end, s_cnt + wave * E, true);
+  for (int64_t r = total + tid; r < p.slots; r += kSortThreads) p.order[r] = -1;
+}
+
+// Many slots: a count per workgroup and expert, kept in `order` until the last
+// of three launches writes that.
+constexpr int kPartThreads = 256, kPartWaves = kPartThreads / 64;
+template <typename I>
+__global__ void __launch_bounds__(kPartThreads) sort_count_kernel(SortParams p) {
+  extern __shared__ int s_cnt[];  // [experts]
+  const int E = p.experts;
+  for (int i = threadIdx.x; i < E; i += kPartThreads) s_cnt[i] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * p.part, end = begin + p.part < p.slots ? begin + p.part : p.slots;
+  for (int64_t s = begin + threadIdx.x; s < end; s += kPartThreads) {
+    const int e = expert_of<I>(p, s, end);
+    if (e >= 0) atomicAdd(s_cnt + e, 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < E; i += kPartThreads) p.order[(int64_t)blockIdx.x * E + i] = s_cnt[i];
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) {
+  extern __shared__ int s_cnt[];  // [waves][experts]
+  __shared__ int s_wave[kSortWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, E = p.experts;
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
+  __syncthreads();
+  // all of an expert's slots, and those of the workgroups before this one: the
+  // threads share the parts out, then one thread per expert adds up
+  const int lanes = kSortThreads / E > 0 ? kSortThreads / E : 1;  // threads per expert
+  int* s_all = s_cnt;            // [E]
+  int* s_before = s_cnt + E;     // [E]
+  if (tid < lanes * E) {
+    const int e = tid % E;
+    int all = 0, before = 0;
+    for (int b = tid / E; b < p.parts; b += lanes) {
+      const int n = p.order[(int64_t)b * E + e];
+      all += n;
+      before += b < (int)blockIdx.x ? n : 0;
+    }
+    atomicAdd(s_all + e, all);
+    atomicAdd(s_before + e, before);
+  }
+  __syncthreads();
+  const int all = tid < E ? s_all[tid] : 0, before = tid < E ? s_before[tid] : 0;
+  int total;
+  int at = block_prefix<kSortThreads>(all, s_wave, &total);
+  if (blockIdx.x == 0) {
+    if (tid < E) p.offsets[tid] = at;
+    if (tid == 0) p.offsets[E] = total;
+  }
+  __syncthreads();
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
+  __syncthreads();
+  const int64_t b0 = blockIdx.x * p.part, b1 = b0 + p.part < p.slots ? b0 + p.part : p.slots;
+  const int64_t per = (p.part + kSortThreads - 1) / kSortThreads * 64;
+  const int64_t begin = b0 + wave * per < b1 ? b0 + wave * per : b1;
+  const int64_t end = begin + per < b1 ? begin + per : b1;
+  count_slots<I>(p, begin, end, s_cnt + wave * E);
+  __syncthreads();
+  if (tid < E) {
+    at += before;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = s_cnt[w * E + tid];
+      s_cnt[w * E + tid] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  place_slots<I>(p, begin, end, s_cnt + wave * E, false);
+}
+
+__global__ void __launch_bounds__(256) sort_order_kernel(SortParams p) {
+  const int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (s >= p.slots) return;
+  const int total = p.offsets[p.experts], row = p.place[s];
+  if (row >= 0) p.order[row] = (int)s;
+  if (s >= total) p.order[s] = -1;
+}
+
+template <typename I>
+hipError_t sort_typed(SortParams p, hipStream_t stream) {
+  const int lds = kSortWaves * p.experts * (int)sizeof(int);
+  if (p.slots <= kSortSmall) {
+    if (lds > 65536 - 256) (void)hipFuncSetAttribute((const void*)sort_small_kernel<I>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    hipLaunchKernelGGL(sort_small_kernel<I>, dim3(1), dim3(kSortThreads), lds, stream, p);
+    return hipGetLastError();
+  }
+  // parts of at least 4096 slots: the counts of all parts, at most a quarter of the slots and one part's more, fit in `order`
+  p.part = (p.slots + 255) / 256;
+  if (p.part < 4096) p.part = 4096;
+  p.parts = (int)((p.slots + p.part - 1) / p.part);
+  if (lds > 65536 - 256) (void)hipFuncSetAttribute((const void*)sort_place_kernel<I>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  hipLaunchKernelGGL(sort_count_kernel<I>, dim3(p.parts), dim3(kPartThreads), p.experts * sizeof(int), stream, p);
+  hipLaunchKernelGGL(sort_place_kernel<I>, dim3(p.parts), dim3(kSortThreads), lds, stream, p);
+  hipLaunchKernelGGL(sort_order_kernel, dim3((unsigned)((p.slots + 255) / 256)), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------- rows by sorted slots
+
+// The slot of a row, -1 where it has none.
+__device__ __forceinline__ int slot_of(const int* order, int64_t row, int64_t slots) {
+  const int s = row < slots ? order[row] : -1;
+  return s >= 0 && s < slots ? s : -1;
+}
+
+template <int T, int RW, bool QUANT>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
+  constexpr int ROWS = 4 * RW;
+  __shared__ TileScales<RW> s_scale;
+  __shared__ int s_slot[ROWS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t slots = p.tokens * p.topk;
+  const int64_t kp = (p.cols + 127) / 128 * 128, ctiles = (p.cols + kRowCols - 1) / kRowCols;
+  const int64_t tiles = (slots + ROWS - 1) / ROWS * ctiles;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t rt = tile / ctiles, ct = tile - rt * ctiles;
+    const int64_t row0 = rt * ROWS + wave * RW, c = ct * kRowCols + lane * 8;
+    int slot[RW];
+    Vec8<T> v[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) slot[r] = slot_of(p.order, row0 + r, slots);
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int64_t token = slot[r] >= 0 ? (unsigned)slot[r] / (unsigned)p.topk : 0;
+      v[r] = vec8_load<T>(static_cast<const char*>(p.X) + token * p.ldx * size_of(T), c, p.cols);
+    }
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      if (QUANT) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = vec8_get(v[r], e);
+        unsigned byte;
+        const u32x2_d o = e4m3_codes(x, byte);
+        if (slot[r] >= 0 && c < kp)
+          *reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.Y) + (row0 + r) * kp + c) = o;
+        s_scale.put(lane, wave * RW + r, byte);
+        if (lane == 0) s_slot[wave * RW + r] = slot[r];
+      } else if (slot[r] >= 0) {
+        vec8_store<T>(static_cast<char*>(p.Y) + (row0 + r) * p.ldy * size_of(T), c, p.cols, v[r]);
+      }
+    }
+    if (QUANT) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < 4 * ROWS; i += kRowThreads) {
+        const int64_t g = ct * 4 + i / ROWS, row = rt * ROWS + i % ROWS;
+        if (g < kp / 128 && s_slot[i % ROWS] >= 0) p.y_scale[g * slots + row] = s_scale.b[i / ROWS][i % ROWS];
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// A wave takes 512 columns of a token: up to eight of its slots' rows at a time
+// are on their way together, summed in fp32 in the slots' order.
+constexpr int kSlotsAtOnce = 8;
+template <int T, int YT>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t slots = p.tokens * p.topk, ctiles = (p.cols + kRowCols - 1) / kRowCols;
+  const int64_t tiles = p.tokens * ctiles;
+  const int64_t step = (int64_t)gridDim.x * 4;
+  for (int64_t tile = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); tile < tiles; tile += step) {
+    const int64_t t = tile / ctiles, c = (tile - t * ctiles) * kRowCols + lane * 8;
+    float y[8] = {};
+    Vec8<YT> res;
+    if (p.R) res = vec8_load<YT>(static_cast<const char*>(p.R) + t * p.ldr * size_of(YT), c, p.cols);
+    for (int j0 = 0; j0 < p.topk; j0 += kSlotsAtOnce) {
+      Vec8<T> v[kSlotsAtOnce];
+      float w[kSlotsAtOnce];
+#pragma unroll
+      for (int j = 0; j < kSlotsAtOnce; ++j) {
+        const int64_t s = t * p.topk + j0 + j;
+        const int row = j0 + j < p.topk ? p.place[s] : -1;
+        const bool on = row >= 0 && row < slots;
+        w[j] = on ? (p.weights ? p.weights[s] : 1.0f) : 0.0f;
+        v[j] = vec8_load<T>(static_cast<const char*>(p.X) + (on ? row : 0) * p.ldx * size_of(T), c, on ? p.cols : 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kSlotsAtOnce; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(w[j], vec8_get(v[j], e), y[e]);
+    }
+    if (p.R) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] += vec8_get(res, e);
+    }
+    vec8_store<YT>(static_cast<char*>(p.Y) + t * p.ldy * size_of(YT), c, p.cols, vec8_pack<YT>(y));
+  }
+}
+
+// A wave takes RW rows, all of their columns: dx = w dy, and the dot product of
+// dy with the row for dw.
+template <int T, int RW, bool QUANT>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradParams p) {
+  constexpr int ROWS = 4 * RW;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t slots = p.tokens * p.topk, kp = (p.cols + 127) / 128 * 128;
+  const int64_t tiles = (slots + ROWS - 1) / ROWS;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t row0 = tile * ROWS + wave * RW;
+    int slot[RW];
+    float w[RW], dot[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      slot[r] = slot_of(p.order, row0 + r, slots);
+      w[r] = slot[r] >= 0 && p.weights ? p.weights[slot[r]] : 1.0f;
+      dot[r] = 0.0f;
+    }
+    for (int64_t c = lane * 8; c - lane * 8 < p.cols; c += kRowCols) {
+      Vec8<T> d[RW], x[RW];
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const int64_t token = slot[r] >= 0 ? (unsigned)slot[r] / (unsigned)p.topk : 0;
+        const int64_t n = slot[r] >= 0 ? p.cols : 0;
+        d[r] = vec8_load<T>(static_cast<const char*>(p.dY) + token * p.ldy * size_of(T), c, n);
+        if (p.dW) x[r] = vec8_load<T>(static_cast<const char*>(p.X) + (slot[r] >= 0 ? row0 + r : 0) * p.ldx * size_of(T), c, n);
+      }
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = vec8_get(d[r], e);
+          if (p.dW) dot[r] = __builtin_fmaf(y[e], vec8_get(x[r], e), dot[r]);
+          y[e] *= w[r];
+        }
+        if (QUANT) {
+          if (c + 8 > p.cols) {  // the padding is zero whatever the weight is
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c + e >= p.cols) y[e] = 0.0f;
+          }
+          unsigned byte;
+          const u32x2_d o = e4m3_codes(y, byte);
+          if (slot[r] >= 0 && c < kp) {
+            *reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.dX) + (row0 + r) * kp + c) = o;
+            if ((lane & 15) == 0) p.dx_scale[(c >> 7) * slots + row0 + r] = (uint8_t)byte;
+          }
+        } else if (slot[r] >= 0) {
+          vec8_store<T>(static_cast<char*>(p.dX) + (row0 + r) * p.lddx * size_of(T), c, p.cols, vec8_pack<T>(y));
+        }
+      }
+    }
+    if (p.dW) {
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        float v = dot[r];
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+        if (lane == 0 && slot[r] >= 0) p.dW[slot[r]] = v;
+      }
+      // slots that no row has
+      for (int i = threadIdx.x; i < ROWS; i += kRowThreads) {
+        const int64_t s = tile * ROWS + i;
+        if (s < slots && (p.place[s] < 0 || p.place[s] >= slots)) p.dW[s] = 0.0f;
+      }
+    }
+  }
+}
+
+template <int T>
+void gather_typed(const GatherParams& p, hipStream_t stream) {
+  const int64_t slots = p.tokens * p.topk;
+  const bool tall = row_tiles(slots, p.cols, 8) >= 2 * p.cus;
+  const dim3 grid = row_grid(row_tiles(slots, p.cols, tall ? 8 : 1)), block(kRowThreads);
+  if (p.y_scale) {
+    if (tall)
+      hipLaunchKernelGGL((gather_kernel<T, 8, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((gather_kernel<T, 1, true>), grid, block, 0, stream, p);
+  } else {
+    if (tall)
+      hipLaunchKernelGGL((gather_kernel<T, 8, false>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((gather_kernel<T, 1, false>), grid, block, 0, stream, p);
+  }
+}
+
+template <int T>
+void combine_typed(const CombineParams& p, hipStream_t stream) {
+  const dim3 grid = row_grid((p.tokens * ((p.cols + kRowCols - 1) / kRowCols) + 3) / 4), block(kRowThreads);
+  if (p.y_type == T)
+    hipLaunchKernelGGL((combine_kernel<T, T>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((combine_kernel<T, kTypeF32>), grid, block, 0, stream, p);
+}
+
+template <int T>
+void combine_grad_typed(const CombineGradParams& p, hipStream_t stream) {
+  const int64_t slots = p.tokens * p.topk;
+  const bool tall = (slots + 15) / 16 >= 2 * p.cus;
+  const dim3 grid = row_grid(tall ? (slots + 15) / 16 : (slots + 3) / 4), block(kRowThreads);
+  if (p.dx_scale) {
+    if (tall)
+      hipLaunchKernelGGL((combine_grad_kernel<T, 4, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((combine_grad_kernel<T, 1, true>), grid, block, 0, stream, p);
+  } else {
+    if (tall)
+      hipLaunchKernelGGL((combine_grad_kernel<T, 4, false>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((combine_grad_kernel<T, 1, false>), grid, block, 0, stream, p);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_sort(const SortParams& p, hipStream_t stream) {
+  return p.ids64 ? sort_typed<int64_t>(p, stream) : sort_typed<int32_t>(p, stream);
+}
+
+#define PGK_BY_TYPE(type, fn)       \
+  do {                              \
+    if ((type) == kTypeF32)         \
+      fn<kTypeF32>(p, stream);      \
+    else if ((type) == kTypeBF16)   \
+      fn<kTypeBF16>(p, stream);     \
+    else                            \
+      fn<kTypeF16>(p, stream);      \
+    return hipGetLastError();       \
+  } while (0)
+
+hipError_t launch_gather(const GatherParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, gather_typed); }
+hipError_t launch_combine(const CombineParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_typed); }
+hipError_t launch_combine_grad(const CombineGradParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_grad_typed); }
+
+}  // namespace pgk

@@ -1,0 +1,222 @@
+// silu(g) * u of rows X = [g | u], with X kept in e4m3 for the gradient, and the
+// gradient from what was kept.
+//
+//   s = 1 / (1 + exp(-g)),  y = g s u
+//   dg = dy u s (1 + g (1 - s)),  du = dy g s
+//
+// One pass each, row by row, bound by memory.
+#include "common.hpp"
+#include "fp8_rows.hpp"
+
+namespace pgk {
+namespace {
+
+// 1 / (1 + exp(-g)): exp past fp32's range gives infinity and so zero.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + expf(-g)); }
+
+__device__ __forceinline__ int64_t used_rows(const int* valid, int64_t rows) {
+  if (!valid) return rows;
+  const int64_t n = *valid;
+  return n < 0 ? 0 : n < rows ? n : rows;
+}
+
+template <int T, int RW, bool QUANT>
+__global__ void __launch_bounds__(kRowThreads) glu_kernel(GluParams p) {
+  constexpr int ROWS = 4 * RW;
+  __shared__ TileScales<RW> s_y, s_g, s_u;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t used = used_rows(p.valid, p.rows);
+  const int64_t kp = (p.cols + 127) / 128 * 128, ctiles = (p.cols + kRowCols - 1) / kRowCols;
+  const int64_t tiles = (used + ROWS - 1) / ROWS * ctiles;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t rt = tile / ctiles, ct = tile - rt * ctiles;
+    const int64_t row0 = rt * ROWS + wave * RW, c = ct * kRowCols + lane * 8;
+    Vec8<T> g[RW], u[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const char* x = static_cast<const char*>(p.X) + (row0 + r < used ? row0 + r : used - 1) * p.ldx * size_of(T);
+      g[r] = vec8_load<T>(x, c, p.cols);
+      u[r] = vec8_load<T>(x + p.cols * size_of(T), c, p.cols);
+    }
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int64_t row = row0 + r;
+      const bool on = row < used && c < kp;
+      float a[8], b[8], y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        a[e] = vec8_get(g[r], e);
+        b[e] = vec8_get(u[r], e);
+        y[e] = a[e] * sigmoid(a[e]) * b[e];
+      }
+      if (p.kept) {
+        unsigned byte;
+        uint8_t* k = p.kept + row * 2 * kp + c;
+        const u32x2_d qg = e4m3_codes(a, byte);
+        s_g.put(lane, wave * RW + r, byte);
+        const u32x2_d qu = e4m3_codes(b, byte);
+        s_u.put(lane, wave * RW + r, byte);
+        if (on) {
+          *reinterpret_cast<u32x2_d*>(k) = qg;
+          *reinterpret_cast<u32x2_d*>(k + kp) = qu;
+        }
+      }
+      if (QUANT) {
+        unsigned byte;
+        const u32x2_d q = e4m3_codes(y, byte);
+        s_y.put(lane, wave * RW + r, byte);
+        if (on) *reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.Y) + row * kp + c) = q;
+      } else if (row < used) {
+        vec8_store<T>(static_cast<char*>(p.Y) + row * p.ldy * size_of(T), c, p.cols, vec8_pack<T>(y));
+      }
+    }
+    if (QUANT || p.kept) {
+      __syncthreads();
+      if (QUANT) s_y.store(p.y_scale, ct * 4, kp / 128, rt * ROWS, used, p.rows);
+      if (p.kept) {
+        s_g.store(p.kept_scale, ct * 4, kp / 128, rt * ROWS, used, p.rows);
+        s_u.store(p.kept_scale + kp / 128 * p.rows, ct * 4, kp / 128, rt * ROWS, used, p.rows);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// KEPT: X is what the forward kept; otherwise the rows themselves.
+template <int T, int RW, bool KEPT, bool QUANT>
+__global__ void __launch_bounds__(kRowThreads) glu_grad_kernel(GluGradParams p) {
+  constexpr int ROWS = 4 * RW;
+  __shared__ TileScales<RW> s_g, s_u;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t used = used_rows(p.valid, p.rows);
+  const int64_t kp = (p.cols + 127) / 128 * 128, ctiles = (p.cols + kRowCols - 1) / kRowCols;
+  const int64_t tiles = (used + ROWS - 1) / ROWS * ctiles;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t rt = tile / ctiles, ct = tile - rt * ctiles;
+    const int64_t row0 = rt * ROWS + wave * RW, c = ct * kRowCols + lane * 8;
+    Vec8<T> d[RW], g[KEPT ? 1 : RW], u[KEPT ? 1 : RW];
+    u32x2_d qg[RW], qu[RW];
+    unsigned bg[RW], bu[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int64_t row = row0 + r < used ? row0 + r : used - 1;
+      d[r] = vec8_load<T>(static_cast<const char*>(p.dY) + row * p.ldy * size_of(T), c, p.cols);
+      if (KEPT) {
+        const int64_t at = c < kp ? c : 0;  // columns past the row: any codes
+        const uint8_t* k = static_cast<const uint8_t*>(p.X) + row * 2 * kp + at;
+        qg[r] = *reinterpret_cast<const u32x2_d*>(k);
+        qu[r] = *reinterpret_cast<const u32x2_d*>(k + kp);
+        bg[r] = p.x_scale[(at >> 7) * p.rows + row];
+        bu[r] = p.x_scale[((at + kp) >> 7) * p.rows + row];
+      } else {
+        const char* x = static_cast<const char*>(p.X) + row * p.ldx * size_of(T);
+        g[r] = vec8_load<T>(x, c, p.cols);
+        u[r] = vec8_load<T>(x + p.cols * size_of(T), c, p.cols);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int64_t row = row0 + r;
+      const bool on = row < used && c < kp;
+      float a[8], b[8];
+      if (KEPT) {
+        e4m3_values(qg[r], bg[r], a);
+        e4m3_values(qu[r], bu[r], b);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a[e] = vec8_get(g[r], e);
+          b[e] = vec8_get(u[r], e);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float dy = vec8_get(d[r], e), s = sigmoid(a[e]), gs = a[e] * s;
+        const float dg = dy * b[e] * __builtin_fmaf(gs, 1.0f - s, s);
+        b[e] = dy * gs;
+        a[e] = dg;
+      }
+      if (QUANT) {
+        unsigned byte;
+        uint8_t* q = static_cast<uint8_t*>(p.dX) + row * 2 * kp + c;
+        const u32x2_d og = e4m3_codes(a, byte);
+        s_g.put(lane, wave * RW + r, byte);
+        const u32x2_d ou = e4m3_codes(b, byte);
+        s_u.put(lane, wave * RW + r, byte);
+        if (on) {
+          *reinterpret_cast<u32x2_d*>(q) = og;
+          *reinterpret_cast<u32x2_d*>(q + kp) = ou;
+        }
+      } else if (row < used) {
+        char* x = static_cast<char*>(p.dX) + row * p.lddx * size_of(T);
+        vec8_store<T>(x, c, p.cols, vec8_pack<T>(a));
+        vec8_store<T>(x + p.cols * size_of(T), c, p.cols, vec8_pack<T>(b));
+      }
+    }
+    if (QUANT) {
+      __syncthreads();
+      s_g.store(p.dx_scale, ct * 4, kp / 128, rt * ROWS, used, p.rows);
+      s_u.store(p.dx_scale + kp / 128 * p.rows, ct * 4, kp / 128, rt * ROWS, used, p.rows);
+      __syncthreads();
+    }
+  }
+}
+
+template <int T, int RW>
+void glu_sized(const GluParams& p, hipStream_t stream) {
+  const dim3 grid = row_grid(row_tiles(p.rows, p.cols, RW));
+  if (p.y_scale)
+    hipLaunchKernelGGL((glu_kernel<T, RW, true>), grid, dim3(kRowThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((glu_kernel<T, RW, false>), grid, dim3(kRowThreads), 0, stream, p);
+}
+
+template <int T, int RW>
+void glu_grad_sized(const GluGradParams& p, hipStream_t stream) {
+  const dim3 grid = row_grid(row_tiles(p.rows, p.cols, RW)), block(kRowThreads);
+  if (p.x_scale) {
+    if (p.dx_scale)
+      hipLaunchKernelGGL((glu_grad_kernel<T, RW, true, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((glu_grad_kernel<T, RW, true, false>), grid, block, 0, stream, p);
+  } else {
+    if (p.dx_scale)
+      hipLaunchKernelGGL((glu_grad_kernel<T, RW, false, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((glu_grad_kernel<T, RW, false, false>), grid, block, 0, stream, p);
+  }
+}
+
+constexpr int kTall = 4;  // rows per wave where the tiles fill the device
+template <int T>
+void glu_typed(const GluParams& p, hipStream_t stream) {
+  row_tiles(p.rows, p.cols, kTall) >= 2 * p.cus ? glu_sized<T, kTall>(p, stream) : glu_sized<T, 1>(p, stream);
+}
+template <int T>
+void glu_grad_typed(const GluGradParams& p, hipStream_t stream) {
+  row_tiles(p.rows, p.cols, kTall) >= 2 * p.cus ? glu_grad_sized<T, kTall>(p, stream) : glu_grad_sized<T, 1>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_glu(const GluParams& p, hipStream_t stream) {
+  if (p.type == kTypeF32)
+    glu_typed<kTypeF32>(p, stream);
+  else if (p.type == kTypeBF16)
+    glu_typed<kTypeBF16>(p, stream);
+  else
+    glu_typed<kTypeF16>(p, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_glu_grad(const GluGradParams& p, hipStream_t stream) {
+  if (p.type == kTypeF32)
+    glu_grad_typed<kTypeF32>(p, stream);
+  else if (p.type == kTypeBF16)
+    glu_grad_typed<kTypeBF16>(p, stream);
+  else
+    glu_grad_typed<kTypeF16>(p, stream);
+  return hipGetLastError();
+}
+
+}  // namespace pgk

@@ -24,6 +24,7 @@
 // tile and (several problems per launch) each problem's first tile id and
 // tile grid.
 static_assert(PGEMM_MAX_PROBLEMS == pgk::kMaxGemmProblems, "header states the problem limit");
+static_assert(PMOE_MAX_EXPERTS == pgk::kMaxExperts, "header states the expert limit");
 constexpr int kOrderKey = 10 + 3 * pgk::kMaxGemmProblems;
 constexpr int kOrderCache = 8;
 struct OrderChoice {
@@ -1383,6 +1384,311 @@ pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_
     if (st != PGEMM_OK) return st;
   }
   return e == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ layers of experts
+
+namespace {
+
+// The buffers of a call: each must lie in one allocation and start on its
+// elements' alignment, and no output may overlap another buffer, but for pairs
+// that may be the same exactly.
+struct CallBuffersCheck {
+  struct Buffer {
+    const void* p;
+    size_t bytes;
+    bool out;
+    const void* same;  // an input that an output may be
+  };
+  CallRanges in;
+  int n = 0;
+  bool ok = true;
+  Buffer b[10];
+  explicit CallBuffersCheck(int dev) : in(dev) {}
+  void add(const void* p, size_t bytes, size_t align, bool out, const void* same = nullptr) {
+    if (bytes == 0) return;
+    ok = ok && buffer_ok(p, bytes, align, in);
+    b[n++] = {p, bytes, out, same};
+  }
+  bool good() const {
+    if (!ok) return false;
+    for (int i = 0; i < n; ++i)
+      for (int j = i + 1; j < n; ++j) {
+        if (!b[i].out && !b[j].out) continue;
+        if (b[i].p == b[j].p && (b[i].same == b[j].p || b[j].same == b[i].p)) continue;
+        if (overlaps(b[i].p, b[i].bytes, b[j].p, b[j].bytes)) return false;
+      }
+    return true;
+  }
+};
+
+// Bytes of an e4m3 operand and of its scales.
+size_t fp8_bytes(int64_t rows, int64_t cols) { return span_bytes(rows, padded(cols), 1); }
+size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return span_bytes(padded(cols) / 128, rows, 1); }
+
+bool out_ok(int out) { return out == PRMS_OUT_SAME || out == PRMS_OUT_FP8_B128 || out == PRMS_OUT_MXFP4; }
+pgemm_status done(hipError_t e) { return e == hipSuccess ? PGEMM_OK : PGEMM_ERR_LAUNCH; }
+
+bool slots_ok(int64_t tokens, int64_t topk) {
+  return tokens >= 0 && topk >= 1 && tokens <= kMaxDim && topk <= kMaxDim && tokens * topk <= kMaxDim;
+}
+
+}  // namespace
+
+extern "C" {
+
+pgemm_status pmoe_sort_run(pgemm_config* cfg, const void* ids, int ids_type, int64_t tokens, int64_t topk, int experts,
+                           int32_t* place, int32_t* order, int32_t* offsets, void* hip_stream) {
+  if (!cfg || !slots_ok(tokens, topk) || experts < 1 || (ids_type != PMOE_I32 && ids_type != PMOE_I64))
+    return PGEMM_ERR_INVALID;
+  if (experts > PMOE_MAX_EXPERTS) return PGEMM_ERR_UNSUPPORTED;
+  const int64_t slots = tokens * topk;
+  const size_t isz = ids_type == PMOE_I64 ? 8 : 4, sb = (size_t)slots * 4;
+  CallBuffersCheck in(cfg->device);
+  in.add(ids, (size_t)slots * isz, isz, false);
+  in.add(place, sb, 4, true);
+  in.add(order, sb, 4, true);
+  in.add(offsets, ((size_t)experts + 1) * 4, 4, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  int bits = 0;
+  while ((1 << bits) < experts) ++bits;
+  const pgk::SortParams p = {ids, ids_type == PMOE_I64, slots, experts, bits, place, order, offsets, 0, 0};
+  return done(pgk::launch_sort(p, (hipStream_t)hip_stream));
+}
+
+pgemm_status pmoe_gather_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx, const int32_t* order,
+                             int64_t tokens, int64_t topk, int64_t cols, int out, void* Y, int64_t ldy,
+                             uint8_t* y_scale, void* hip_stream) {
+  if (!cfg || !type_ok(x_type) || !slots_ok(tokens, topk) || cols < 1 || cols > kMaxDim || ldx < cols || !out_ok(out))
+    return PGEMM_ERR_INVALID;
+  if (out == PRMS_OUT_MXFP4) return PGEMM_ERR_UNSUPPORTED;
+  const bool quant = out == PRMS_OUT_FP8_B128;
+  if (!quant && ldy < cols) return PGEMM_ERR_INVALID;
+  if (tokens == 0) return PGEMM_OK;
+  const int64_t slots = tokens * topk;
+  const size_t es = type_size(x_type);
+  CallBuffersCheck in(cfg->device);
+  in.add(X, matrix_bytes(tokens, cols, ldx, es), es, false);
+  in.add(order, (size_t)slots * 4, 4, false);
+  in.add(Y, quant ? fp8_bytes(slots, cols) : matrix_bytes(slots, cols, ldy, es), quant ? 1 : es, true);
+  in.add(quant ? y_scale : nullptr, quant ? fp8_scale_bytes(slots, cols) : 0, 1, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if (quant && !aligned(Y, 8)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::GatherParams p = {X,      order, Y,    quant ? y_scale : nullptr, x_type, tokens,
+                               topk,   cols,  ldx,  ldy,                       cfg->num_cus};
+  return done(pgk::launch_gather(p, (hipStream_t)hip_stream));
+}
+
+pgemm_status pmoe_combine_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx, const int32_t* place,
+                              const float* weights, const void* R, int64_t ldr, void* Y, int y_type, int64_t ldy,
+                              int64_t tokens, int64_t topk, int64_t cols, void* hip_stream) {
+  if (!cfg || !type_ok(x_type) || !type_ok(y_type) || !slots_ok(tokens, topk) || cols < 1 || cols > kMaxDim ||
+      ldx < cols || ldy < cols || (R && ldr < cols))
+    return PGEMM_ERR_INVALID;
+  if (y_type != x_type && y_type != PMX_F32) return PGEMM_ERR_UNSUPPORTED;
+  if (tokens == 0) return PGEMM_OK;
+  const int64_t slots = tokens * topk;
+  const size_t xs = type_size(x_type), ys = type_size(y_type), sb = (size_t)slots * 4;
+  CallBuffersCheck in(cfg->device);
+  in.add(X, matrix_bytes(slots, cols, ldx, xs), xs, false);
+  in.add(place, sb, 4, false);
+  in.add(weights, weights ? sb : 0, 4, false);
+  in.add(R, R ? matrix_bytes(tokens, cols, ldr, ys) : 0, ys, false);
+  in.add(Y, matrix_bytes(tokens, cols, ldy, ys), ys, true, ldr == ldy ? R : nullptr);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::CombineParams p = {X, place, weights, R, Y, x_type, y_type, tokens, topk, cols, ldx, ldr, ldy};
+  return done(pgk::launch_combine(p, (hipStream_t)hip_stream));
+}
+
+pgemm_status pmoe_combine_grad_run(pgemm_config* cfg, const void* dY, int type, int64_t ldy, const void* X, int64_t ldx,
+                                   const int32_t* place, const int32_t* order, const float* weights, int64_t tokens,
+                                   int64_t topk, int64_t cols, int out, void* dX, int64_t lddx, uint8_t* dx_scale,
+                                   float* dW, void* hip_stream) {
+  if (!cfg || !type_ok(type) || !slots_ok(tokens, topk) || cols < 1 || cols > kMaxDim || ldy < cols ||
+      (dW && ldx < cols) || !out_ok(out))
+    return PGEMM_ERR_INVALID;
+  if (out == PRMS_OUT_MXFP4) return PGEMM_ERR_UNSUPPORTED;
+  const bool quant = out == PRMS_OUT_FP8_B128;
+  if (!quant && lddx < cols) return PGEMM_ERR_INVALID;
+  if (tokens == 0) return PGEMM_OK;
+  const int64_t slots = tokens * topk;
+  const size_t es = type_size(type), sb = (size_t)slots * 4;
+  CallBuffersCheck in(cfg->device);
+  in.add(dY, matrix_bytes(tokens, cols, ldy, es), es, false);
+  in.add(X, dW ? matrix_bytes(slots, cols, ldx, es) : 0, es, false);
+  in.add(place, sb, 4, false);
+  in.add(order, sb, 4, false);
+  in.add(weights, weights ? sb : 0, 4, false);
+  in.add(dX, quant ? fp8_bytes(slots, cols) : matrix_bytes(slots, cols, lddx, es), quant ? 1 : es, true);
+  in.add(quant ? dx_scale : nullptr, quant ? fp8_scale_bytes(slots, cols) : 0, 1, true);
+  in.add(dW, dW ? sb : 0, 4, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if (quant && !aligned(dX, 8)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::CombineGradParams p = {dY,   X,      place, order, weights, dX,  quant ? dx_scale : nullptr, dW, type,
+                                    tokens, topk, cols,  ldy,   ldx,     lddx, cfg->num_cus};
+  return done(pgk::launch_combine_grad(p, (hipStream_t)hip_stream));
+}
+
+pgemm_status pfp8_quant_run(pgemm_config* cfg, const void* X, int x_type, int64_t rows, int64_t cols, int64_t ldx,
+                            uint8_t* Q, uint8_t* scale, void* hip_stream) {
+  if (!cfg || !type_ok(x_type) || rows < 0 || cols < 1 || rows > kMaxDim || cols > kMaxDim || ldx < cols)
+    return PGEMM_ERR_INVALID;
+  if (rows == 0) return PGEMM_OK;
+  const size_t es = type_size(x_type);
+  CallBuffersCheck in(cfg->device);
+  in.add(X, matrix_bytes(rows, cols, ldx, es), es, false);
+  in.add(Q, fp8_bytes(rows, cols), 1, true);
+  in.add(scale, fp8_scale_bytes(rows, cols), 1, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if (!aligned(Q, 8)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::Fp8QuantParams p = {X, x_type, rows, cols, ldx, Q, scale, cfg->num_cus};
+  return done(pgk::launch_fp8_quant(p, (hipStream_t)hip_stream));
+}
+
+pgemm_status pfp8_quant_weights_run(pgemm_config* cfg, const void* W, int w_type, int64_t experts, int64_t rows,
+                                    int64_t cols, uint8_t* Q, uint8_t* scale, uint8_t* Qt, uint8_t* scale_t,
+                                    void* hip_stream) {
+  if (!cfg || !type_ok(w_type) || experts < 1 || rows < 1 || cols < 1 || experts > kMaxDim || rows > kMaxDim ||
+      cols > kMaxDim || (Qt == nullptr) != (scale_t == nullptr))
+    return PGEMM_ERR_INVALID;
+  const size_t es = type_size(w_type);
+  const size_t one = span_bytes(rows, cols, es), q = fp8_bytes(rows, cols), qt = fp8_bytes(cols, rows);
+  const size_t s = span_bytes(padded(rows) / 128, padded(cols) / 128, 1);
+  if (one > (size_t)1 << 60) return PGEMM_ERR_INVALID;  // no allocation holds it, and the products below fit
+  CallBuffersCheck in(cfg->device);
+  in.add(W, span_bytes(experts, (int64_t)one, 1), es, false);
+  in.add(Q, span_bytes(experts, (int64_t)q, 1), 1, true);
+  in.add(scale, span_bytes(experts, (int64_t)s, 1), 1, true);
+  in.add(Qt, Qt ? span_bytes(experts, (int64_t)qt, 1) : 0, 1, true);
+  in.add(scale_t, Qt ? span_bytes(experts, (int64_t)s, 1) : 0, 1, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if (!aligned(Q, 8) || !aligned(Qt, 8)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::Fp8WeightsParams p = {W, w_type, experts, rows, cols, Q, scale, Qt, scale_t};
+  return done(pgk::launch_fp8_quant_weights(p, (hipStream_t)hip_stream));
+}
+
+pgemm_status pgemm_run_experts(pgemm_config* cfg, const uint8_t* A, const uint8_t* a_scale, const uint8_t* B,
+                               const uint8_t* b_scale, void* C, int c_type, int64_t rows, int64_t N, int64_t K,
+                               int experts, const int32_t* offsets, void* hip_stream) {
+  if (!cfg || !type_ok(c_type) || rows < 0 || N < 1 || K < 1 || rows > kMaxDim || N > kMaxDim || K > kMaxDim ||
+      K % 128 != 0 || experts < 1 || (!offsets && experts != 1))
+    return PGEMM_ERR_INVALID;
+  if (c_type == PMX_F16 || experts > PMOE_MAX_EXPERTS || K >= 1 << 22) return PGEMM_ERR_UNSUPPORTED;
+  // tiles of 16 x 16 are counted in 31 bits
+  if ((rows / 16 + experts) * ((N + 15) / 16) > kMaxDim) return PGEMM_ERR_UNSUPPORTED;
+  if (rows == 0) return PGEMM_OK;
+  const size_t cs = type_size(c_type);
+  CallBuffersCheck in(cfg->device);
+  in.add(A, span_bytes(rows, K, 1), 1, false);
+  in.add(a_scale, span_bytes(K / 128, rows, 1), 1, false);
+  in.add(B, span_bytes((int64_t)experts * N, K, 1), 1, false);
+  in.add(b_scale, span_bytes((int64_t)experts * (padded(N) / 128), K / 128, 1), 1, false);
+  in.add(offsets, offsets ? ((size_t)experts + 1) * 4 : 0, 4, false);
+  in.add(C, span_bytes(rows, N, cs), cs, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if (!aligned(A, 16) || !aligned(B, 16)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::ExpertsParams p = {A,      a_scale, B,      b_scale, C,           offsets,
+                                (int)rows, (int)N,  (int)K, experts, c_type == PMX_F32, cfg->num_xcds};
+  return done(pgk::launch_gemm_experts(p, cfg->num_cus, (hipStream_t)hip_stream));
+}
+
+pgemm_status pgemm_run_experts_wgrad(pgemm_config* cfg, const void* D, int d_type, int64_t ldd, const uint8_t* d_scale,
+                                     const uint8_t* A, const uint8_t* a_scale, const void* base, void* dB, int b_type,
+                                     int64_t rows, int64_t N, int64_t K, int experts, const int32_t* offsets,
+                                     void* hip_stream) {
+  const bool fp8 = d_type == PMX_FP8_B128;
+  if (!cfg || (!fp8 && !type_ok(d_type)) || !type_ok(b_type) || rows < 0 || N < 1 || K < 1 || rows > kMaxDim ||
+      N > kMaxDim || K > kMaxDim || (!fp8 && ldd < N) || experts < 1 || (!offsets && experts != 1))
+    return PGEMM_ERR_INVALID;
+  if ((!fp8 && d_type != PMX_BF16) || b_type == PMX_F16 || experts > PMOE_MAX_EXPERTS || N >= 1 << 22 || K >= 1 << 22)
+    return PGEMM_ERR_UNSUPPORTED;
+  const size_t bs = type_size(b_type), bb = span_bytes((int64_t)experts * N, K, bs);
+  CallBuffersCheck in(cfg->device);
+  in.add(D, fp8 ? fp8_bytes(rows, N) : matrix_bytes(rows, N, ldd, 2), fp8 ? 1 : 2, false);
+  in.add(fp8 ? d_scale : nullptr, fp8 ? fp8_scale_bytes(rows, N) : 0, 1, false);
+  in.add(A, fp8_bytes(rows, K), 1, false);
+  in.add(a_scale, fp8_scale_bytes(rows, K), 1, false);
+  in.add(offsets, offsets ? ((size_t)experts + 1) * 4 : 0, 4, false);
+  in.add(base, base ? bb : 0, bs, false);
+  in.add(dB, bb, bs, true, base);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if ((fp8 && !aligned(D, 16)) || !aligned(A, 16)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::WgradParams p = {D,         fp8 ? d_scale : nullptr, A, a_scale, base, dB, offsets, (int)rows, (int)N, (int)K,
+                              experts, fp8 ? padded(N) : ldd,   b_type == PMX_F32, cfg->num_xcds};
+  return done(pgk::launch_gemm_experts_wgrad(p, cfg->num_cus, (hipStream_t)hip_stream));
+}
+
+pgemm_status pglu_run(pgemm_config* cfg, const void* X, int x_type, int64_t ldx, int64_t rows, int64_t cols,
+                      const int32_t* valid, int out, void* Y, int64_t ldy, uint8_t* y_scale, uint8_t* kept,
+                      uint8_t* kept_scale, void* hip_stream) {
+  if (!cfg || !type_ok(x_type) || rows < 0 || cols < 1 || rows > kMaxDim || cols > kMaxDim / 2 || ldx < 2 * cols ||
+      !out_ok(out) || (kept == nullptr) != (kept_scale == nullptr))
+    return PGEMM_ERR_INVALID;
+  if (out == PRMS_OUT_MXFP4) return PGEMM_ERR_UNSUPPORTED;
+  const bool quant = out == PRMS_OUT_FP8_B128;
+  if (!quant && ldy < cols) return PGEMM_ERR_INVALID;
+  if (rows == 0) return PGEMM_OK;
+  const size_t es = type_size(x_type);
+  CallBuffersCheck in(cfg->device);
+  in.add(X, matrix_bytes(rows, 2 * cols, ldx, es), es, false);
+  in.add(valid, valid ? 4 : 0, 4, false);
+  in.add(Y, quant ? fp8_bytes(rows, cols) : matrix_bytes(rows, cols, ldy, es), quant ? 1 : es, true);
+  in.add(quant ? y_scale : nullptr, quant ? fp8_scale_bytes(rows, cols) : 0, 1, true);
+  in.add(kept, kept ? fp8_bytes(rows, 2 * padded(cols)) : 0, 1, true);
+  in.add(kept_scale, kept ? fp8_scale_bytes(rows, 2 * padded(cols)) : 0, 1, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if ((quant && !aligned(Y, 8)) || !aligned(kept, 8)) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::GluParams p = {X, x_type, rows, cols, ldx, ldy, Y, quant ? y_scale : nullptr, kept, kept_scale, valid,
+                            cfg->num_cus};
+  return done(pgk::launch_glu(p, (hipStream_t)hip_stream));
+}
+
+pgemm_status pglu_grad_run(pgemm_config* cfg, const void* dY, int type, int64_t ldy, const void* X, int64_t ldx,
+                           const uint8_t* x_scale, int64_t rows, int64_t cols, const int32_t* valid, int out, void* dX,
+                           int64_t lddx, uint8_t* dx_scale, void* hip_stream) {
+  if (!cfg || !type_ok(type) || rows < 0 || cols < 1 || rows > kMaxDim || cols > kMaxDim / 2 || ldy < cols ||
+      (!x_scale && ldx < 2 * cols) || !out_ok(out))
+    return PGEMM_ERR_INVALID;
+  if (out == PRMS_OUT_MXFP4) return PGEMM_ERR_UNSUPPORTED;
+  const bool quant = out == PRMS_OUT_FP8_B128;
+  if (!quant && lddx < 2 * cols) return PGEMM_ERR_INVALID;
+  if (quant && cols % 128 != 0) return PGEMM_ERR_UNSUPPORTED;
+  if (rows == 0) return PGEMM_OK;
+  const size_t es = type_size(type);
+  CallBuffersCheck in(cfg->device);
+  in.add(dY, matrix_bytes(rows, cols, ldy, es), es, false);
+  in.add(X, x_scale ? fp8_bytes(rows, 2 * padded(cols)) : matrix_bytes(rows, 2 * cols, ldx, es), x_scale ? 1 : es, false);
+  in.add(x_scale, x_scale ? fp8_scale_bytes(rows, 2 * padded(cols)) : 0, 1, false);
+  in.add(valid, valid ? 4 : 0, 4, false);
+  in.add(dX, quant ? fp8_bytes(rows, 2 * cols) : matrix_bytes(rows, 2 * cols, lddx, es), quant ? 1 : es, true);
+  in.add(quant ? dx_scale : nullptr, quant ? fp8_scale_bytes(rows, 2 * cols) : 0, 1, true);
+  if (!in.good()) return PGEMM_ERR_INVALID;
+  if ((quant && !aligned(dX, 8)) || (x_scale && !aligned(X, 8))) return PGEMM_ERR_UNSUPPORTED;
+  DeviceGuard g(cfg->device);
+  if (!g.ok) return PGEMM_ERR_DEVICE;
+  const pgk::GluGradParams p = {dY,   X,  x_scale, type, rows, cols, ldy, ldx, lddx, dX, quant ? dx_scale : nullptr, valid,
+                                cfg->num_cus};
+  return done(pgk::launch_glu_grad(p, (hipStream_t)hip_stream));
 }
 
 }  // extern "C"
