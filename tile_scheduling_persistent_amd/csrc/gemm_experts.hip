@@ -12,6 +12,10 @@
 // The rows are sorted by expert and the experts' row counts are in device memory:
 // each program of the grid adds up the tiles that the experts have and walks the
 // tiles with a stride of the grid.
+#include <atomic>
+#include <type_traits>
+#include <utility>
+
 #include "common.hpp"
 #include "experts_device.hpp"
 #include "fp8_rows.hpp"
@@ -24,7 +28,11 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
+typedef unsigned u32_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
@@ -183,14 +191,435 @@ __global__ void __launch_bounds__(WAVES * 64) gemm_experts_stream_kernel(Experts
   }
 }
 
+// ------------------------------------------------------------ tiles in LDS
+//
+// 2 x WN waves, each TM x TN of a tile.  A slab is 128 deep: one scale group, 128
+// bytes of each row of A and of B, so every global access is whole lines.  A ring of
+// NST slabs in LDS is filled by hand-issued buffer_load ... lds (gemm_device.hpp);
+// the loads of slab g + NST - 1 are spread over the MFMAs of a slab period, across
+// tiles too.  A's scale bytes travel with their slab, each into a word of its own
+// (rows of an expert start anywhere, so that wider loads would not be aligned); B's
+// one byte per block of 128 columns is the same for a whole wave and comes through
+// the scalar cache.
+//
+// Which rows make up an MFMA block is free: block b of a wave holds every SM-th
+// (SN-th) row, from row b on, so that a lane reads the scale words of all its blocks
+// at once and stores SN consecutive columns.  Which k an MFMA's lanes take is free
+// too, as long as both operands agree and a scale covers them all.
+template <int BM, int BN, int NST_, int WN_>
+struct Shape {
+  static constexpr int NST = NST_;
+  static constexpr int WN = WN_, WAVES = 2 * WN;
+  static constexpr int TM = BM / 2, TN = BN / WN;
+  static constexpr int SM = TM / 32, SN = TN / 32;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SA_BYTES = BM * 4;
+  static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES;
+  static constexpr int SPARE = NST * STAGE;                // what waves without scales of their own load
+  static constexpr int LDS_BYTES = SPARE + 256;            // and the experts' tables behind it
+  static constexpr int NA = BM / 8 / WAVES, NB = BN / 8 / WAVES;  // 1 KB operand loads per wave per slab
+  static constexpr int NL = NA + NB + 1;                   // + 64 scale bytes
+  static constexpr int NMF = SM * SN;                      // MFMA blocks
+  static_assert((SM == 2 || SM == 4) && (SN == 2 || SN == 4), "a row's scale words in one LDS read");
+  static_assert(NA % 2 == 0 && NB % 2 == 0 && BM / 64 <= WAVES && TN <= 128, "whole loads per wave");
+};
+
+// LDS layout of an operand.  Block i of a wave's BLOCKS 32-row blocks is made of the
+// rows l * BLOCKS + i (l = 0 .. 31) of the wave's part.  Eight consecutive rows, 128
+// bytes each, are a 1 KB chunk; within it rows of one block stand together, and a
+// row's 16-byte pieces are permuted by l >> 1.  So a ds_read_b128, served 16 lanes
+// (16 consecutive l of one block and piece) at a time, meets all 16 slots of a
+// 256-byte window.
+template <int BLOCKS>
+__device__ __forceinline__ int slot_row(int slot) {  // row of a slot of the chunk
+  return BLOCKS == 4 ? 4 * (slot & 1) + (slot >> 1) : 2 * (slot & 3) + (slot >> 2);
+}
+template <int BLOCKS>
+__device__ __forceinline__ int row_slot(int l) {  // bytes to row l of block 0 (block i: + i * 1024 / BLOCKS)
+  return BLOCKS == 4 ? (l >> 1) * 1024 + (l & 1) * 128 : (l >> 2) * 1024 + (l & 3) * 128;
+}
+// The part of l >> 1 (mod 8) that the chunk's index gives.
+template <int BLOCKS>
+__device__ __forceinline__ constexpr unsigned piece_flip(int chunk) {
+  return BLOCKS == 4 ? (unsigned)chunk & 7u : 2u * ((unsigned)chunk & 3u);
+}
+
+template <class F, int... I>
+__device__ __forceinline__ void static_for_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// W (2 or 4) columns at p, those before `left`; non-temporal where NT.
+#define PGK_STORE(NT, type, p, ...)                                         \
+  do {                                                                      \
+    if constexpr (NT)                                                       \
+      __builtin_nontemporal_store(__VA_ARGS__, reinterpret_cast<type*>(p)); \
+    else                                                                    \
+      *reinterpret_cast<type*>(p) = __VA_ARGS__;                            \
+  } while (0)
+template <int W, bool NT>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[W], int left) {
+  if (left >= W) {
+    if constexpr (W == 4)
+      PGK_STORE(NT, u32x4_a4, p, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
+    else
+      PGK_STORE(NT, u32x2_a4, p, __builtin_bit_cast(u32x2, f32x2{v[0], v[1]}));
+  } else {
+#pragma unroll
+    for (int e = 0; e < W - 1; ++e)
+      if (e < left) p[e] = v[e];
+  }
+}
+template <int W, bool NT>
+__device__ __forceinline__ void store_row(unsigned short* p, const float (&v)[W], int left) {
+  unsigned o[W / 2];
+#pragma unroll
+  for (int e = 0; e < W / 2; ++e) o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  if (left >= W) {
+    if constexpr (W == 4)
+      PGK_STORE(NT, u32x2_a2, p, u32x2{o[0], o[1]});
+    else
+      PGK_STORE(NT, u32_a2, p, o[0]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < W - 1; ++e)
+      if (e < left) p[e] = (unsigned short)(o[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+constexpr int kGroupRows = 8;  // rows of tiles per group of an expert's grouped order
+
+template <int BM, int BN, int NST, int WN, bool F32>
+__global__ void __launch_bounds__(128 * WN) gemm_experts_tile_kernel(ExpertsParams p) {
+  using S = Shape<BM, BN, NST, WN>;
+  constexpr int NA = S::NA, NB = S::NB, NO = NA + NB, NL = S::NL, NMF = S::NMF;
+  constexpr int SM = S::SM, SN = S::SN;
+  // Of a period's 2 * NMF block positions the loads take the first SPREAD: half of
+  // them where the ring's second stage has to have landed by the next period.
+  constexpr int SPREAD = NST > 2 ? 2 * NMF : NMF;
+
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  int* s_lo = reinterpret_cast<int*>(smem + S::LDS_BYTES);
+  int* s_n = s_lo + p.experts;
+  int* s_tile = s_n + p.experts;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l32 = lane & 31, kb = lane >> 5;
+  const int G = (int)gridDim.x;
+  const int nk = p.K >> 7, nb = (p.N + 127) >> 7;
+  const int npn = (p.N + BN - 1) / BN;
+
+  expert_tiles(p.offsets, p.experts, p.rows, BM, npn, s_lo, s_n, s_tile);
+  const int total = __builtin_amdgcn_readfirstlane(s_tile[p.experts]);
+
+  // A tile: its expert, rows and columns.
+  struct Tile {
+    int t, e, lo, n, m0, n0;
+  };
+  auto open = [&](int t, Tile& x) {
+    x.t = t;
+    if (t >= total) return;
+    x.e = __builtin_amdgcn_readfirstlane(expert_of_tile(s_tile, p.experts, t, x.e));
+    x.lo = __builtin_amdgcn_readfirstlane(s_lo[x.e]);
+    x.n = __builtin_amdgcn_readfirstlane(s_n[x.e]);
+    const int npm = (x.n + BM - 1) / BM;
+    int pm, pn;
+    pgs::decode(pgs::kGrouped, t - __builtin_amdgcn_readfirstlane(s_tile[x.e]), npm, npn, kGroupRows, pm, pn);
+    x.m0 = __builtin_amdgcn_readfirstlane(pm) * BM;
+    x.n0 = __builtin_amdgcn_readfirstlane(pn) * BN;
+  };
+
+  // Global -> LDS.  Operands: instruction q covers rows 8q .. 8q + 7, lane i
+  // slot i / 8 of LDS chunk q; instruction d of wave w is q = w * N + d.
+  const int r8 = lane >> 3;
+  const unsigned rowb = (unsigned)p.K;
+  const unsigned aoff = (unsigned)(wave * NA * 8 + slot_row<SM>(r8)) * rowb;
+  const unsigned boff = (unsigned)(wave * NB * 8 + slot_row<SN>(r8)) * rowb;
+  // 16-byte piece of the lane in instruction 0, in bytes; d flips bits of it
+  const unsigned apiece = ((unsigned)((lane & 7) ^ (SM == 2 ? r8 >> 1 & 1 : 0)) ^ piece_flip<SM>(wave * NA)) * 16u;
+  const unsigned bpiece = ((unsigned)((lane & 7) ^ (SN == 2 ? r8 >> 1 & 1 : 0)) ^ piece_flip<SN>(wave * NB)) * 16u;
+  const bool scales_here = wave < BM / 64;  // 64 rows' scales
+  const unsigned lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+  // LDS reads: piece 2 q + kb of row l32 of a block; step h takes q = 2 h and 2 h + 1.
+  unsigned rd_a[4], rd_b[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const unsigned c = (unsigned)((2 * q + kb) ^ (l32 >> 1 & 7)) * 16u;
+    rd_a[q] = (unsigned)(wm * S::TM * 128 + row_slot<SM>(l32)) + c;
+    rd_b[q] = (unsigned)(S::A_BYTES + wn * S::TN * 128 + row_slot<SN>(l32)) + c;
+  }
+  const unsigned rd_sa = (unsigned)(S::A_BYTES + S::B_BYTES + (wm * S::TM + l32 * SM) * 4);
+
+  // ---- loader ----
+  Tile lt = {0, 0, 0, 0, 0, 0};
+  int lk = 0;  // next slab
+  rsrc_words_t rA, rB, rS;
+  unsigned long long a_ptr = 0, b_ptr = 0, s_ptr = 0, sb_ptr = 0;
+  unsigned a_rec = 0, b_rec = 0, s_rec = 0;
+  unsigned sbw[NST - 1] = {}, sbs[NST - 1] = {};  // words with B's scale byte, of the slabs on their way, and its place
+
+  auto begin_tile = [&](int t) {
+    open(t, lt);
+    lk = 0;
+    if (t >= total) return;
+    const int ra = lt.n - lt.m0 < BM ? lt.n - lt.m0 : BM, rb = p.N - lt.n0 < BN ? p.N - lt.n0 : BN;
+    a_ptr = reinterpret_cast<unsigned long long>(p.A + ((int64_t)lt.lo + lt.m0) * p.K);
+    b_ptr = reinterpret_cast<unsigned long long>(p.B + ((int64_t)lt.e * p.N + lt.n0) * p.K);
+    a_rec = (unsigned)ra * rowb;
+    b_rec = (unsigned)rb * rowb;
+    const int sr = ra - wave * 64;
+    s_ptr = reinterpret_cast<unsigned long long>(p.sa + lt.lo + lt.m0 + wave * 64);
+    s_rec = scales_here && sr > 0 ? (unsigned)sr : 0u;
+    const int blk = (lt.n0 >> 7) + wn * S::TN / 128;
+    sb_ptr = reinterpret_cast<unsigned long long>(p.sb + ((int64_t)lt.e * nb + (blk < nb ? blk : nb - 1)) * nk);
+  };
+  // The next slab's resources; without one they are empty and the loads read
+  // zeros into a stage no one reads.
+  auto prep = [&]() {
+    if (lt.t < total && lk == nk) begin_tile(lt.t + G);
+    const bool load = lt.t < total;
+    const unsigned k0 = (unsigned)lk * 128u;
+    rA = rsrc_words_u64(a_ptr + k0, load ? a_rec - k0 : 0u);
+    rB = rsrc_words_u64(b_ptr + k0, load ? b_rec - k0 : 0u);
+    rS = rsrc_words_u64(s_ptr + (unsigned long long)lk * (unsigned long long)p.rows, load ? s_rec : 0u);
+#pragma unroll
+    for (int i = 0; i + 1 < NST - 1; ++i) {
+      sbw[i] = sbw[i + 1];
+      sbs[i] = sbs[i + 1];
+    }
+    if (load) {
+      // the aligned word that holds the byte, which is taken out when the slab's turn
+      // comes: a wait here would hold up the MFMAs
+      const unsigned long long at = sb_ptr + (unsigned)lk;
+      sbw[NST - 2] = *reinterpret_cast<const __attribute__((address_space(4))) unsigned*>(at & ~3ull);
+      sbs[NST - 2] = 8u * ((unsigned)at & 3u);
+      ++lk;
+    }
+  };
+  auto dma = [&](int st, int d) PGK_INLINE {
+    const unsigned sb = lds0 + (unsigned)(st * S::STAGE);
+    if (d < NA) {
+      load_lds16(rA, sb + (unsigned)((wave * NA + d) * 1024), aoff + (unsigned)d * 8u * rowb + (apiece ^ (piece_flip<SM>(d) * 16u)));
+    } else if (d < NO) {
+      const int e = d - NA;
+      load_lds16(rB, sb + (unsigned)(S::A_BYTES + (wave * NB + e) * 1024),
+                 boff + (unsigned)e * 8u * rowb + (bpiece ^ (piece_flip<SN>(e) * 16u)));
+    } else {
+      load_lds_u8(rS, scales_here ? sb + (unsigned)(S::A_BYTES + S::B_BYTES + wave * 256) : lds0 + (unsigned)S::SPARE,
+                  (unsigned)lane);
+    }
+  };
+
+  f32x16 acc[SN][SM];
+  u32x4 aq[2][SM][2], bq[2][SN][2];  // fragments, by the step
+  unsigned wa[2][SM];                // A's scale words, of the slab and the one before
+  unsigned wb[2] = {};               // B's
+
+  // LDS read r of step h: B block 0, the A blocks, the other B blocks (the order the
+  // MFMAs consume them), two pieces each; step 0 the scale words first.
+  constexpr int NR = 2 * (SM + SN);
+  auto read = [&](int st, auto hc, int r) PGK_INLINE {
+    constexpr int h = hc;
+    const unsigned char* s = smem + st * S::STAGE;
+    const int i = r >> 1, q = 2 * h + (r & 1);
+    if (i == 0)
+      bq[h][0][r & 1] = *reinterpret_cast<const u32x4*>(s + rd_b[q]);
+    else if (i <= SM)
+      aq[h][i - 1][r & 1] = *reinterpret_cast<const u32x4*>(s + rd_a[q] + (i - 1) * (1024 / SM));
+    else
+      bq[h][i - SM][r & 1] = *reinterpret_cast<const u32x4*>(s + rd_b[q] + (i - SM) * (1024 / SN));
+  };
+  auto read_scales = [&](int st, int par) PGK_INLINE {
+    const unsigned* w = reinterpret_cast<const unsigned*>(smem + st * S::STAGE + rd_sa);
+#pragma unroll
+    for (int i = 0; i < SM; ++i) wa[par][i] = w[i];
+  };
+  auto mfma = [&](auto hc, auto jc, int par) PGK_INLINE {
+    constexpr int h = hc, sn = jc / SM, sm = jc % SM;
+    const u32x4 a0 = aq[h][sm][0], a1 = aq[h][sm][1], b0 = bq[h][sn][0], b1 = bq[h][sn][1];
+    if constexpr (F32) {
+      const Exact a(aq[h][sm], scale_value(wa[par][sm])), b(bq[h][sn], scale_value(wb[par]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[sn][sm] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v[i], b.v[i], acc[sn][sm], 0, 0, 0);
+    } else {
+      acc[sn][sm] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          i32x8{(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]},
+          i32x8{(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]},
+          acc[sn][sm], kFmtE4M3, kFmtE4M3, 0, (int)wa[par][sm], 0, (int)wb[par]);
+    }
+  };
+  // Step h on the matrix cores (of a period that runs step 1 of the slab before,
+  // then step 0); the next step's reads (of stage st_rd) and the loads that fall on
+  // this half of the period.
+  auto step = [&](auto hc, int par, int st_rd, int st_dma) PGK_INLINE {
+    static_for<NMF>([&](auto jc) PGK_INLINE {
+      constexpr int h = hc, j = jc, nx = 1 - h;
+      mfma(hc, jc, par);
+      static_for<NR>([&](auto rc) PGK_INLINE {
+        if constexpr (rc * NMF / NR == j) read(st_rd, std::integral_constant<int, nx>{}, rc);
+      });
+      static_for<NL>([&](auto dc) PGK_INLINE {
+        if constexpr (dc * SPREAD / NL == (1 - h) * NMF + j) dma(st_dma, dc);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  // Lane l holds SN consecutive columns, l % 32 * SN of the wave's, one per
+  // block; registers 4 g + e hold rows (8 g + 4 (l / 32) + e) * SM + block: a
+  // store of the wave covers two rows' 32 * SN consecutive columns.
+  typedef std::conditional_t<F32, float, unsigned short> out_t;
+  auto put_tile = [&](const Tile& x, auto edge, auto nt) {
+    const int n = x.n0 + wn * S::TN + l32 * SN, m = x.m0 + wm * S::TM + 4 * kb * SM;
+    out_t* base = static_cast<out_t*>(p.C) + ((int64_t)x.lo + m) * p.N + n;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < SM; ++i) {
+          const int r = (8 * g + e) * SM + i;
+          if (edge && m + r >= x.n) continue;
+          float v[SN];
+#pragma unroll
+          for (int j = 0; j < SN; ++j) v[j] = acc_read(acc[j][i][4 * g + e]);
+          store_row<SN, nt>(base + (int64_t)r * p.N, v, edge ? p.N - n : SN);
+        }
+  };
+  auto epilogue = [&](const Tile& x) {
+    const bool edge = x.m0 + BM > x.n || x.n0 + BN > p.N;
+    const bool lines = (p.N & (F32 ? 31 : 63)) == 0 && (reinterpret_cast<uintptr_t>(p.C) & 127) == 0;
+    const std::integral_constant<bool, true> yes;
+    const std::integral_constant<bool, false> no;
+    if (edge)
+      put_tile(x, yes, no);
+    else if (lines)
+      put_tile(x, no, yes);
+    else
+      put_tile(x, no, no);
+  };
+
+  // programs of one XCD take consecutive tiles: they share operand panels in its L2
+  const int first = pgs::program_of(blockIdx.x, G, p.xcds, 1);
+  Tile ct = {0, 0, 0, 0, 0, 0};
+  open(first, ct);
+  if (first >= total) return;
+  begin_tile(first);
+#pragma unroll
+  for (int j = 0; j < NST - 1; ++j) {
+    prep();
+#pragma unroll
+    for (int d = 0; d < NL; ++d) dma(j, d);
+  }
+  // Slab g has landed once this wave's loads of it are done (those of the NST - 2
+  // slabs after it may be in flight) and every wave has passed the barrier; every wave
+  // has then finished its LDS reads of slab g - 1, which frees that stage for slab g +
+  // NST - 1.
+  int g = 0;
+  const std::integral_constant<int, 0> step0;
+  const std::integral_constant<int, 1> step1;
+  auto slab_start = [&](int& st, int& st_dma) {
+    wait_vm<(NST - 2) * NL>();
+    slab_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    st = g % NST;
+    st_dma = st == 0 ? NST - 1 : st - 1;
+    wb[0] = wb[1];
+    wb[1] = sbw[0] >> sbs[0] & 0xffu;
+#pragma unroll
+    for (int i = 0; i < SM; ++i) wa[0][i] = wa[1][i];
+    ++g;
+  };
+  while (ct.t < total) {
+#pragma unroll
+    for (int j = 0; j < SN; ++j)
+#pragma unroll
+      for (int i = 0; i < SM; ++i) acc[j][i] = f32x16{};
+    int st, st_dma;
+    slab_start(st, st_dma);
+    read_scales(st, 1);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read(st, step0, r);
+    __builtin_amdgcn_sched_barrier(0);
+    prep();
+#pragma unroll
+    for (int d = 0; d < NL; ++d)
+      if (d * SPREAD / NL < NMF) dma(st_dma, d);
+    step(step0, 1, st, st_dma);
+    for (int ck = 1; ck < nk; ++ck) {
+      slab_start(st, st_dma);
+      read_scales(st, 1);
+      prep();
+      __builtin_amdgcn_sched_barrier(0);
+      step(step1, 0, st, st_dma);
+      step(step0, 1, st, st_dma);
+    }
+    static_for<NMF>([&](auto jc) PGK_INLINE { mfma(step1, jc, 1); });
+    mfma_results_ready();
+    epilogue(ct);
+    open(ct.t + G, ct);
+  }
+  // the loads of stages that no one reads have to land before the workgroup's LDS is
+  // given away
+  wait_vm<0>();
+}
+
+}  // namespace
+
+namespace {
+
+constexpr int kDevices = 64;
+int tables_bytes(int experts) { return (3 * experts + 1) * (int)sizeof(int); }
+
+// Resident workgroups per CU, asked for once per kernel and device (the answer, and
+// the LDS limit it sets, cost microseconds of a short call); with the largest tables.
+struct Instance {
+  int bm, bn, threads, lds;
+  void (*kern)(ExpertsParams);
+  mutable std::atomic<int> resident[kDevices] = {};
+  int per_cu() const {
+    int dev = 0;
+    const int most = lds + tables_bytes(kMaxExperts);
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices)
+      return occupancy_of(reinterpret_cast<const void*>(kern), threads, most);
+    int n = resident[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+      n = occupancy_of(reinterpret_cast<const void*>(kern), threads, most);
+      resident[dev].store(n, std::memory_order_release);
+    }
+    return n;
+  }
+};
+
+template <int BM, int BN, int NST, int WN, bool F32>
+Instance tiled() {
+  return {BM, BN, 128 * WN, Shape<BM, BN, NST, WN>::LDS_BYTES, gemm_experts_tile_kernel<BM, BN, NST, WN, F32>};
+}
+
 }  // namespace
 
 hipError_t launch_gemm_experts(const ExpertsParams& p, int cus, hipStream_t stream) {
-  const int lds = (3 * p.experts + 1) * (int)sizeof(int);
+  const int tables = tables_bytes(p.experts);
+  if (p.rows > 64LL * p.experts) {
+    static const Instance big[2] = {tiled<256, 256, 2, 2, false>(), tiled<256, 256, 2, 2, true>()};
+    static const Instance small[2] = {tiled<128, 128, 2, 2, false>(), tiled<128, 128, 2, 2, true>()};
+    const Instance& i = (p.rows > 256LL * p.experts ? big : small)[p.out_f32 ? 1 : 0];
+    const int grid = cus * i.per_cu();
+    hipLaunchKernelGGL(i.kern, dim3(grid), dim3(i.threads), i.lds + tables, stream, p);
+    return hipGetLastError();
+  }
   if (p.out_f32)
-    hipLaunchKernelGGL((gemm_experts_stream_kernel<1, 1, 4, 8, true>), dim3(2 * cus), dim3(512), lds, stream, p);
+    hipLaunchKernelGGL((gemm_experts_stream_kernel<1, 1, 4, 8, true>), dim3(2 * cus), dim3(512), tables, stream, p);
   else
-    hipLaunchKernelGGL((gemm_experts_stream_kernel<1, 1, 4, 8, false>), dim3(2 * cus), dim3(512), lds, stream, p);
+    hipLaunchKernelGGL((gemm_experts_stream_kernel<1, 1, 4, 8, false>), dim3(2 * cus), dim3(512), tables, stream, p);
   return hipGetLastError();
 }
 
