@@ -646,7 +646,8 @@ PGEMM_API pgemm_status pgemm_run_experts(pgemm_config* cfg, const uint8_t* A, co
  * (NULL: zeros) and dB [experts][N][K] of b_type (PMX_BF16 or PMX_F32), base may be
  * dB exactly.  Elements times their scales are exact in bf16 (down to 2^-126); fp32
  * accumulate.  Experts without rows get base or zeros.  A and an e4m3 D 16-byte
- * aligned, N and K below 2^22 (PGEMM_ERR_UNSUPPORTED otherwise); any N and K. */
+ * aligned, N and K below 2^22, ldd below 2^24 (PGEMM_ERR_UNSUPPORTED otherwise); any N
+ * and K, fastest where a bf16 D's rows start on 16 bytes. */
 PGEMM_API pgemm_status pgemm_run_experts_wgrad(pgemm_config* cfg, const void* D, int d_type, int64_t ldd,
                                      const uint8_t* d_scale, const uint8_t* A, const uint8_t* a_scale,
                                      const void* base, void* dB, int b_type, int64_t rows, int64_t N, int64_t K,

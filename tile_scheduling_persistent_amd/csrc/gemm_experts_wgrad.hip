@@ -8,6 +8,10 @@
 // power of two), and v_mfma_f32_16x16x32_bf16 sums in fp32.  Both operands lie in
 // LDS as they do in memory, rows r of columns, and are read transposed
 // (ds_read_b64_tr_b16).
+#include <atomic>
+#include <type_traits>
+#include <utility>
+
 #include "common.hpp"
 #include "experts_device.hpp"
 #include "fp8_rows.hpp"
@@ -21,15 +25,47 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+#define PGK_INLINE __attribute__((always_inline))
 
 constexpr int kThreads = 256;
-constexpr int BR = 64;  // rows per slab
+constexpr int BR = 64;  // rows per slab: two steps of 32
 
-// Physical 16-byte chunk of logical chunk c in row r: 32 lanes of a transposing
-// read touch rows r .. r + 3 and r + 8 .. r + 11 at two adjacent chunks, 16
-// chunks that this puts in distinct slots of a 256-byte window.
-__device__ __forceinline__ int swz(int r, int c) { return c ^ (4 * (r & 3)) ^ (2 * ((r >> 3) & 1)); }
+template <class F, int... I>
+__device__ __forceinline__ void static_for_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// Written out so that the accumulators stay in AGPRs (left to itself the register
+// allocator moved them to VGPRs and spilled those).  The compiler's hazard logic does
+// not look into it: a block's accumulator is next read NMF MFMAs later, the fragments
+// come straight from LDS reads, which the compiler waits for, the accumulators are
+// zeroed with padding after them, and read only after mfma_results_ready.
+__device__ __forceinline__ void mfma16(f32x4& acc, bf16x8 a, bf16x8 b) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+
+// Between the writes that zero the accumulators and the first MFMA that reads them.
+__device__ __forceinline__ void acc_written() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 7" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Physical 16-byte chunk of logical chunk c in row r.  A transposing read of 32
+// lanes touches rows r .. r + 3 and r + 8 .. r + 11 at two adjacent chunks: bits 2-3
+// from r & 3 and bit 1 from bit 3 of r put those 16 chunks in distinct slots of a
+// 256-byte window.  Bit 0 does the same for the writes of every second chunk that
+// the conversion makes.
+__device__ __forceinline__ int swz(int r, int c) {
+  return c ^ (4 * (r & 3)) ^ (2 * ((r >> 3) & 1)) ^ (((c >> 4) ^ r) & 1);
+}
 
 // Sixteen e4m3 codes times 2^(byte - 127), as bf16.
 __device__ __forceinline__ void codes_bf16(u32x4 q, unsigned byte, u32x4& lo, u32x4& hi) {
@@ -49,160 +85,342 @@ __device__ __forceinline__ void codes_bf16(u32x4 q, unsigned byte, u32x4& lo, u3
   }
 }
 
-// An operand's slab on its way: BR rows of W columns, 32 bytes of bf16 (two
-// chunks) per thread and part.
-template <int W, bool FP8>
+// The slab that the loads are at: rows r0 .. of the n from row lo on, of a tile.
+struct Place {
+  int64_t t;
+  int lo, n, r0, n0, k0, e;
+};
+
+// An operand's slab on its way through registers: BR rows of W columns, in parts of
+// 16 bytes per thread (16 codes, or 8 elements of bf16).  Loads go through buffer
+// resources that end with the slab's last row: rows past it read as zeros.
+// How an operand lies in memory: bf16 whose rows start on 16 bytes, bf16 of any
+// alignment, or e4m3.
+constexpr int kWide = 0, kNarrow = 1, kCodes = 2;
+template <int W, int FORM>
 struct Slab {
-  static constexpr int PARTS = BR * W / 16 / kThreads;
-  u32x4 q[PARTS][FP8 ? 1 : 2];
-  unsigned byte[PARTS];
-  // Rows r0 .. of `rows` (those past the end: zeros), columns c0 .. of the matrix
-  // at `x` with `cols` columns (FP8: padded) and `ld` elements between rows.
-  __device__ __forceinline__ void load(const void* x, const uint8_t* scale, int64_t ld, int64_t sld, int64_t row0, int r0,
-                                       int rows, int c0, int cols) {
-#pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-      const int at = i * kThreads + threadIdx.x, r = at / (W / 16), c = c0 + at % (W / 16) * 16;
-      const bool on = r0 + r < rows;
-      const int64_t row = row0 + (on ? r0 + r : 0);
-      if (FP8) {
-        const bool in = on && c < cols;  // columns are whole groups
-        q[i][0] = u32x4{0, 0, 0, 0};
-        byte[i] = 0;
-        if (in) {
-          q[i][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(x) + row * ld + c);
-          byte[i] = scale[(int64_t)(c >> 7) * sld + row];
-        }
-      } else {
-        const unsigned short* p = static_cast<const unsigned short*>(x) + row * ld + c;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          q[i][h] = u32x4{0, 0, 0, 0};
-          if (on && c + 8 * h + 8 <= cols) q[i][h] = *reinterpret_cast<const Quad<2>::type*>(p + 8 * h);
-          else if (on && c + 8 * h < cols) {
-            for (int e = 0; e < 7; ++e)
-              if (c + 8 * h + e < cols) {
-                const unsigned v = (unsigned)p[8 * h + e] << (16 * (e & 1));
-                if (e < 2) q[i][h][0] |= v;
-                else if (e < 4) q[i][h][1] |= v;
-                else if (e < 6) q[i][h][2] |= v;
-                else q[i][h][3] |= v;
-              }
-          }
-        }
-      }
+  static constexpr bool FP8 = FORM == kCodes;
+  static constexpr int COLS = FP8 ? 16 : 8;          // of a part
+  static constexpr int STEP = kThreads * COLS / W;   // rows from one part to the next
+  static constexpr int PARTS = BR / STEP;
+  static constexpr int ESZ = FP8 ? 1 : 2;
+  u32x4 q[PARTS];
+  unsigned byte[FP8 ? PARTS : 1];
+  unsigned off, soff;  // of part 0, in bytes
+  unsigned wr[2];      // LDS: FP8 its two chunks, else of even and odd parts
+  unsigned row;        // of part 0
+  unsigned long long x, s;  // the slab and its scales, and their ranges
+  unsigned xr, sr;
+  __device__ __forceinline__ void init(unsigned ld, unsigned sld) {
+    const int c = (int)threadIdx.x % (W / COLS) * COLS;
+    row = threadIdx.x / (W / COLS);
+    off = row * ld * ESZ + c * ESZ;
+    soff = (unsigned)(c >> 7) * sld + row;
+    const int r = (int)row, k = c >> 3;
+    wr[0] = (unsigned)(r * W * 2 + swz(r, k) * 16);
+    wr[1] = FP8 ? (unsigned)(r * W * 2 + swz(r, k + 1) * 16) : (unsigned)((r + STEP) * W * 2 + swz(r + STEP, k) * 16);
+  }
+  // The slab at `at`, columns c0 .. of `cols`; left: its rows, 0: nothing is read.
+  __device__ __forceinline__ void aim(const Place& at, int left, const void* mat, const uint8_t* scale, int64_t ld,
+                                      int64_t sld, int c0, int cols) {
+    const int64_t r = (int64_t)at.lo + at.r0;
+    const int rows = left < BR ? left : BR;
+    x = reinterpret_cast<unsigned long long>(mat) + (unsigned long long)(r * ld + c0) * ESZ;
+    // up to the last column of the last row
+    xr = rows > 0 ? ((unsigned)(rows - 1) * (unsigned)ld + (unsigned)(cols - c0)) * ESZ : 0u;
+    if (FP8) {
+      s = reinterpret_cast<unsigned long long>(scale) + (unsigned long long)((int64_t)(c0 >> 7) * sld + r);
+      const int groups = (cols - c0) / 128 < W / 128 ? (cols - c0) / 128 : W / 128;
+      sr = rows > 0 ? (unsigned)(groups - 1) * (unsigned)sld + (unsigned)rows : 0u;
     }
   }
-  __device__ __forceinline__ void put(unsigned char* s) const {
+  __device__ __forceinline__ void load(int i, unsigned ld) {
+    const auto rX = rsrc(reinterpret_cast<const void*>(x), xr);
+    // in the vector offset: the range check leaves a scalar one out
+    const unsigned at = off + (unsigned)(i * STEP) * ld * ESZ;
+    if (FORM != kNarrow) {
+      q[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rX, at, 0, 0));
+    } else {
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-      const int at = i * kThreads + threadIdx.x, r = at / (W / 16), c = at % (W / 16) * 2;
-      u32x4 lo, hi;
-      if (FP8) {
-        codes_bf16(q[i][0], byte[i], lo, hi);
-      } else {
-        lo = q[i][0];
-        hi = q[i][FP8 ? 0 : 1];
+      for (int e = 0; e < 4; ++e) {
+        const unsigned lo = __builtin_amdgcn_raw_buffer_load_b16(rX, at + 4 * e, 0, 0);
+        q[i][e] = lo | (unsigned)__builtin_amdgcn_raw_buffer_load_b16(rX, at + 4 * e + 2, 0, 0) << 16;
       }
-      *reinterpret_cast<u32x4*>(s + r * W * 2 + swz(r, c) * 16) = lo;
-      *reinterpret_cast<u32x4*>(s + r * W * 2 + swz(r, c + 1) * 16) = hi;
+    }
+    if (FP8)
+      byte[i] = __builtin_amdgcn_raw_buffer_load_b8(rsrc(reinterpret_cast<const void*>(s), sr), soff + i * STEP, 0, 0);
+  }
+  // Part i into the stage at s; left: rows of the slab.  Another row's scale may stand
+  // behind the slab's last one.
+  __device__ __forceinline__ void put(int i, unsigned char* st, int left) const {
+    if (FP8) {
+      u32x4 lo, hi;
+      codes_bf16(q[i], (int)row + i * STEP < left ? byte[FP8 ? i : 0] : 0u, lo, hi);
+      *reinterpret_cast<u32x4*>(st + wr[0] + i * STEP * W * 2) = lo;
+      *reinterpret_cast<u32x4*>(st + wr[1] + i * STEP * W * 2) = hi;
+    } else {
+      *reinterpret_cast<u32x4*>(st + wr[i & 1] + (i & ~1) * STEP * W * 2) = q[i];
     }
   }
 };
 
-// A tile of BN x BK of one expert's gradient, four waves of BN/2 x BK/2.
-template <int BN, int BK, bool DFP8>
+// A tile is BN x BK of one expert's gradient; four waves of BN/2 x BK/2.
+//
+// Slabs go from memory to registers, are multiplied by their scales there and
+// written to one of two LDS stages while the matrix cores work on the other; a part's
+// next load goes out as soon as it is written.  One barrier per slab, between its
+// two steps: behind it the second step's fragments are in registers already and the
+// next slab's first are read.  The slabs of a program's tiles follow one another
+// without a break.
+template <int BN, int BK, int DFORM, bool F32>
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
-  constexpr int TN = BN / 2, TK = BK / 2, SN = TN / 16, SK = TK / 16;
-  constexpr int D_BYTES = BR * BN * 2, A_BYTES = BR * BK * 2;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[D_BYTES + A_BYTES];
+  constexpr int TN = BN / 2, TK = BK / 2, SN = TN / 16, SK = TK / 16, NMF = SN * SK;
+  constexpr int D_BYTES = BR * BN * 2, STAGE = D_BYTES + BR * BK * 2;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];  // [2][STAGE]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave >> 1, wk = wave & 1;
-  const int npn = (p.N + BN - 1) / BN, npk = (p.K + BK - 1) / BK;
+  const int npn = (p.N + BN - 1) / BN, npk = (p.K + BK - 1) / BK, per = npn * npk;
   const int np = (p.N + 127) / 128 * 128, kp = (p.K + 127) / 128 * 128;
-  const int64_t total = (int64_t)p.experts * npn * npk;
+  const int64_t total = (int64_t)p.experts * per;
+  const int G = (int)gridDim.x;
 
-  // transposing reads: lane i of a group of 16 points at row i / 4 (+ 8 per
-  // group), columns 4 (i % 4) .. of the block
-  const int g = lane >> 4, i16 = lane & 15, a4 = i16 & 3, e4 = i16 >> 2;
-  const int r_lane = g * 8 + e4;
-  auto frag = [&](const unsigned char* s, int W, int col, int r0, i16x4 (&f)[2]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = r0 + r_lane + 4 * h, n = col + 4 * a4;
-      const unsigned char* at = s + r * W * 2 + swz(r, n >> 3) * 16 + 8 * (a4 & 1);
-      f[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at);
-    }
+  // The tile of program `prog` in round i: programs of one XCD take consecutive
+  // tiles, which share operand panels in its L2, and a round's blocks of tiles move
+  // on by one XCD from round to round, so that an XCD does not keep one part of the
+  // experts.
+  const int per_xcd = p.xcds > 1 && G % p.xcds == 0 ? G / p.xcds : 0;
+  auto tile_of = [&](int64_t i) -> int64_t {
+    int at = (int)blockIdx.x;
+    if (per_xcd) at = (int)(((unsigned)at + (unsigned)(i % p.xcds)) % (unsigned)p.xcds) * per_xcd + at / p.xcds;
+    return i * G + at;
   };
-  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-    const int e = (int)(t / (npn * npk)), i = (int)(t - (int64_t)e * npn * npk);
-    const int n0 = i / npk * BN, k0 = i % npk * BK;
-    const ExpertRows rows = expert_rows(p.offsets, e, p.rows);
-    f32x4 acc[SN][SK] = {};
-    Slab<BN, DFP8> d;
-    Slab<BK, true> a;
-    auto load = [&](int r0) __attribute__((always_inline)) {
-      d.load(p.D, p.sd, p.ldd, p.rows, rows.lo, r0, rows.n, n0, DFP8 ? np : p.N);
-      a.load(p.A, p.sa, kp, p.rows, rows.lo, r0, rows.n, k0, kp);
-    };
-    if (rows.n > 0) load(0);
-    for (int r0 = 0; r0 < rows.n; r0 += BR) {
-      __syncthreads();
-      d.put(smem);
-      a.put(smem + D_BYTES);
-      __syncthreads();
-      if (r0 + BR < rows.n) load(r0 + BR);
-#pragma unroll
-      for (int s = 0; s < BR / 32; ++s) {
-        i16x4 fd[SN][2], fa[SK][2];
-#pragma unroll
-        for (int j = 0; j < SN; ++j) frag(smem, BN, wn * TN + j * 16, s * 32, fd[j]);
-#pragma unroll
-        for (int j = 0; j < SK; ++j) frag(smem + D_BYTES, BK, wk * TK + j * 16, s * 32, fa[j]);
-#pragma unroll
-        for (int x = 0; x < SN; ++x)
-#pragma unroll
-          for (int y = 0; y < SK; ++y)
-            acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, __builtin_shufflevector(fa[y][0], fa[y][1], 0, 1, 2, 3, 4, 5, 6, 7)),
-                __builtin_bit_cast(bf16x8, __builtin_shufflevector(fd[x][0], fd[x][1], 0, 1, 2, 3, 4, 5, 6, 7)), acc[x][y], 0,
-                0, 0);
-      }
+  auto open = [&](int64_t t, Place& x) {
+    x.t = t;
+    x.r0 = 0;
+    if (t >= total) return;
+    x.e = __builtin_amdgcn_readfirstlane((int)(t / per));
+    int pn, pk;
+    pgs::decode(pgs::kGrouped, (int)(t - (int64_t)x.e * per), npn, npk, 8, pn, pk);
+    x.n0 = __builtin_amdgcn_readfirstlane(pn) * BN;
+    x.k0 = __builtin_amdgcn_readfirstlane(pk) * BK;
+    const ExpertRows rows = expert_rows(p.offsets, x.e, p.rows);
+    x.lo = __builtin_amdgcn_readfirstlane(rows.lo);
+    x.n = __builtin_amdgcn_readfirstlane(rows.n);
+  };
+
+  Slab<BN, DFORM> d;
+  Slab<BK, kCodes> a;
+  constexpr int PD = Slab<BN, DFORM>::PARTS, PA = Slab<BK, kCodes>::PARTS, NP = PD + PA;
+  const unsigned ldd = (unsigned)p.ldd;
+  d.init(ldd, (unsigned)p.rows);
+  a.init((unsigned)kp, (unsigned)p.rows);
+  // loads: f the slab that they are at, `left` the rows of the one that the registers
+  // hold
+  Place f;
+  int64_t round = 0;
+  int left = 0;
+  auto load = [&](int i) PGK_INLINE {
+    if (i < PD)
+      d.load(i, ldd);
+    else
+      a.load(i - PD, (unsigned)kp);
+  };
+  auto put = [&](int i, unsigned char* s) PGK_INLINE {
+    if (i < PD)
+      d.put(i, s, left);
+    else
+      a.put(i - PD, s + D_BYTES, left);
+  };
+  auto aim = [&]() {
+    const int rows = f.t < total ? f.n - f.r0 : 0;
+    d.aim(f, rows, p.D, p.sd, p.ldd, p.rows, f.n0, DFORM == kCodes ? np : p.N);
+    a.aim(f, rows, p.A, p.sa, kp, p.rows, f.k0, kp);
+  };
+  // An expert without rows has one slab of zeros.
+  auto advance = [&]() {
+    left = f.t < total ? f.n - f.r0 : 0;
+    if (f.t < total) {
+      f.r0 += BR;
+      if (f.r0 >= f.n) open(tile_of(++round), f);
     }
-    // lane: row n of the tile i16, columns k 4 g .. 4 g + 3 of each block
+    aim();
+  };
+
+  // Fragments: lane i of a group of 16 points at row i / 4 (+ 8 per group), columns
+  // 4 (i % 4) .. of a block, and receives four rows of column i.
+  const int g4 = lane >> 4, i16 = lane & 15, a4 = i16 & 3, e4 = i16 >> 2;
+  const int rl = g4 * 8 + e4;
+  unsigned rd_d[SN], rd_a[SK];  // + 4 and 32 rows: the swizzle is unchanged
 #pragma unroll
-    for (int x = 0; x < SN; ++x) {
-      const int n = n0 + wn * TN + x * 16 + i16;
-      if (n >= p.N) continue;
-      const int64_t at = ((int64_t)e * p.N + n) * p.K;
+  for (int j = 0; j < SN; ++j) rd_d[j] = (unsigned)(rl * BN * 2 + swz(rl, (wn * TN + j * 16 + 4 * a4) >> 3) * 16 + 8 * (a4 & 1));
 #pragma unroll
-      for (int y = 0; y < SK; ++y)
+  for (int j = 0; j < SK; ++j)
+    rd_a[j] = (unsigned)(D_BYTES + rl * BK * 2 + swz(rl, (wk * TK + j * 16 + 4 * a4) >> 3) * 16 + 8 * (a4 & 1));
+  i16x4 fd[2][SN][2], fa[2][SK][2];
+  constexpr int NR = 2 * (SN + SK);
+  auto read = [&](const unsigned char* s, auto hc, int i) PGK_INLINE {
+    constexpr int h = hc;  // step
+    const int j = i >> 1, q = i & 1;
+    // swz(r + 4, c) and swz(r, c) agree: r & 3, bit 3 and bit 0 do (r % 8 is below 4)
+    if (j < SK)
+      fa[h][j][q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(s + rd_a[j] + (h * 32 + q * 4) * BK * 2));
+    else
+      fd[h][j - SK][q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(s + rd_d[j - SK] + (h * 32 + q * 4) * BN * 2));
+  };
+  f32x4 acc[SN][SK];
+  auto mfma = [&](auto hc, auto jc) PGK_INLINE {
+    constexpr int h = hc, x = jc / SK, y = jc % SK;
+    const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(fa[h][y][0], fa[h][y][1], 0, 1, 2, 3, 4, 5, 6, 7));
+    const bf16x8 vd = __builtin_bit_cast(bf16x8, __builtin_shufflevector(fd[h][x][0], fd[h][x][1], 0, 1, 2, 3, 4, 5, 6, 7));
+    mfma16(acc[x][y], va, vd);
+  };
+
+  // Lane: row n of the block i16, columns k 4 g4 .. + 3.
+  typedef std::conditional_t<F32, float, unsigned short> out_t;
+  auto store = [&](const Place& x) {
+    const int n = x.n0 + wn * TN + i16, k = x.k0 + wk * TK + 4 * g4;
+    const int64_t at = ((int64_t)x.e * p.N + n) * p.K + k;
+    out_t* out = static_cast<out_t*>(p.dB) + at;
+    const out_t* base = static_cast<const out_t*>(p.base) + at;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int k = k0 + wk * TK + y * 16 + 4 * g + q;
-          if (k >= p.K) continue;
-          float v = acc[x][y][q];
-          if (p.out_f32) {
-            if (p.base) v += static_cast<const float*>(p.base)[at + k];
-            static_cast<float*>(p.dB)[at + k] = v;
+    for (int i = 0; i < SN; ++i) {
+      if (n + i * 16 >= p.N) continue;
+#pragma unroll
+      for (int j = 0; j < SK; ++j) {
+        const int64_t o = (int64_t)i * 16 * p.K + j * 16;
+        const int cols = p.K - k - j * 16;
+        f32x4 v = {acc_read(acc[i][j][0]), acc_read(acc[i][j][1]), acc_read(acc[i][j][2]), acc_read(acc[i][j][3])};
+        if (cols >= 4) {
+          if constexpr (F32) {
+            if (p.base) v += __builtin_bit_cast(f32x4, (u32x4)*reinterpret_cast<const u32x4_a4*>(base + o));
+            *reinterpret_cast<u32x4_a4*>(out + o) = __builtin_bit_cast(u32x4, v);
           } else {
-            if (p.base)
-              v += __builtin_bit_cast(float, (unsigned)static_cast<const unsigned short*>(p.base)[at + k] << 16);
-            static_cast<unsigned short*>(p.dB)[at + k] = (unsigned short)pack_bf16x2(v, v);
+            if (p.base) {
+              const u32x2 b = *reinterpret_cast<const u32x2_a2*>(base + o);
+              v += f32x4{__builtin_bit_cast(float, b[0] << 16), __builtin_bit_cast(float, b[0] & 0xffff0000u),
+                         __builtin_bit_cast(float, b[1] << 16), __builtin_bit_cast(float, b[1] & 0xffff0000u)};
+            }
+            *reinterpret_cast<u32x2_a2*>(out + o) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            if (q >= cols) continue;
+            float w = v[q];
+            if constexpr (F32) {
+              if (p.base) w += base[o + q];
+              out[o + q] = w;
+            } else {
+              if (p.base) w += __builtin_bit_cast(float, (unsigned)base[o + q] << 16);
+              out[o + q] = (unsigned short)pack_bf16x2(w, w);
+            }
           }
         }
+      }
     }
+  };
+
+  const std::integral_constant<int, 0> step0;
+  const std::integral_constant<int, 1> step1;
+  Place ct = {};
+  open(tile_of(0), ct);
+  if (ct.t >= total) return;
+  f = ct;
+  aim();
+#pragma unroll
+  for (int i = 0; i < NP; ++i) load(i);
+  advance();
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    put(i, smem);
+    load(i);
   }
+  advance();
+  slab_barrier();
+#pragma unroll
+  for (int i = 0; i < NR; ++i) read(smem, step0, i);
+  int turn = 0;
+  int64_t ct_round = 0;
+  while (ct.t < total) {
+#pragma unroll
+    for (int i = 0; i < SN; ++i)
+#pragma unroll
+      for (int j = 0; j < SK; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    acc_written();
+    const int slabs = ct.n > 0 ? (ct.n + BR - 1) / BR : 1;
+    for (int s = 0; s < slabs; ++s, turn ^= 1) {
+      unsigned char* now = smem + turn * STAGE;
+      unsigned char* next = smem + (turn ^ 1) * STAGE;
+      static_for<NMF>([&](auto jc) PGK_INLINE {
+        mfma(step0, jc);
+        static_for<NR>([&](auto rc) PGK_INLINE {
+          if constexpr (rc * NMF / NR == jc) read(now, step1, rc);
+        });
+        static_for<NP>([&](auto ic) PGK_INLINE {
+          if constexpr (ic * NMF / NP == jc) {
+            put(ic, next);
+            load(ic);
+          }
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      advance();
+      slab_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<NMF>([&](auto jc) PGK_INLINE {
+        mfma(step1, jc);
+        static_for<NR>([&](auto rc) PGK_INLINE {
+          if constexpr (rc * NMF / NR == jc) read(next, step0, rc);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    }
+    mfma_results_ready();
+    store(ct);
+    open(tile_of(++ct_round), ct);
+  }
+}
+
+// Resident workgroups per CU, asked for once per kernel and device.
+constexpr int kDevices = 64;
+struct Instance {
+  int lds;
+  void (*kern)(WgradParams);
+  mutable std::atomic<int> resident[kDevices] = {};
+  int per_cu() const {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices)
+      return occupancy_of(reinterpret_cast<const void*>(kern), kThreads, lds);
+    int n = resident[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+      n = occupancy_of(reinterpret_cast<const void*>(kern), kThreads, lds);
+      resident[dev].store(n, std::memory_order_release);
+    }
+    return n;
+  }
+};
+template <int BN, int BK, int DFORM, bool F32>
+Instance tiled() {
+  return {2 * BR * (BN + BK) * 2, wgrad_kernel<BN, BK, DFORM, F32>};
 }
 
 }  // namespace
 
 hipError_t launch_gemm_experts_wgrad(const WgradParams& p, int cus, hipStream_t stream) {
-  if (p.sd)
-    hipLaunchKernelGGL((wgrad_kernel<128, 128, true>), dim3(2 * cus), dim3(kThreads), 0, stream, p);
+  static const Instance big[2][2] = {{tiled<256, 256, kWide, false>(), tiled<256, 256, kWide, true>()},
+                                     {tiled<256, 256, kCodes, false>(), tiled<256, 256, kCodes, true>()}};
+  static const Instance small[3][2] = {{tiled<128, 128, kWide, false>(), tiled<128, 128, kWide, true>()},
+                                       {tiled<128, 128, kCodes, false>(), tiled<128, 128, kCodes, true>()},
+                                       {tiled<128, 128, kNarrow, false>(), tiled<128, 128, kNarrow, true>()}};
+  const int64_t tiles = (int64_t)p.experts * ((p.N + 255) / 256) * ((p.K + 255) / 256);
+  const int f32 = p.out_f32 ? 1 : 0;
+  const Instance* i;
+  if (!p.sd && ((reinterpret_cast<uintptr_t>(p.D) & 15) != 0 || (p.ldd & 7) != 0))
+    i = &small[2][f32];
   else
-    hipLaunchKernelGGL((wgrad_kernel<128, 128, false>), dim3(2 * cus), dim3(kThreads), 0, stream, p);
+    i = &(tiles >= cus ? big : small)[p.sd ? 1 : 0][f32];
+  hipLaunchKernelGGL(i->kern, dim3(cus * i->per_cu()), dim3(kThreads), i->lds, stream, p);
   return hipGetLastError();
 }
 

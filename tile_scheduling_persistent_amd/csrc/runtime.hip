@@ -1616,7 +1616,8 @@ pgemm_status pgemm_run_experts_wgrad(pgemm_config* cfg, const void* D, int d_typ
   if (!cfg || (!fp8 && !type_ok(d_type)) || !type_ok(b_type) || rows < 0 || N < 1 || K < 1 || rows > kMaxDim ||
       N > kMaxDim || K > kMaxDim || (!fp8 && ldd < N) || experts < 1 || (!offsets && experts != 1))
     return PGEMM_ERR_INVALID;
-  if ((!fp8 && d_type != PMX_BF16) || b_type == PMX_F16 || experts > PMOE_MAX_EXPERTS || N >= 1 << 22 || K >= 1 << 22)
+  if ((!fp8 && d_type != PMX_BF16) || b_type == PMX_F16 || experts > PMOE_MAX_EXPERTS || N >= 1 << 22 || K >= 1 << 22 ||
+      (!fp8 && ldd >= 1 << 24))
     return PGEMM_ERR_UNSUPPORTED;
   const size_t bs = type_size(b_type), bb = span_bytes((int64_t)experts * N, K, bs);
   CallBuffersCheck in(cfg->device);
