@@ -62,7 +62,7 @@ def check(C, offsets, ref, terms, k, dtype):
 # rows per expert from none to many: every kernel and tile
 SHAPES = [(1, 128, 128, 1), (1, 70, 256, 5), (8, 256, 384, 64), (17, 129, 128, 2), (40, 1000, 640, 3), (64, 513, 1024, 1),
           (130, 300, 1152, 4), (200, 256, 2048, 6), (700, 300, 512, 3), (1100, 777, 256, 2), (2000, 512, 384, 9),
-          (3000, 1030, 128, 5)]
+          (3000, 1030, 128, 5), (5000, 4200, 256, 3), (4000, 3000, 128, 20)]
 
 
 @pytest.mark.parametrize("rows,n,k,experts", SHAPES)
@@ -136,7 +136,8 @@ def test_nan_codes_and_scales_stay_in_their_rows(rows):
 
 
 WGRAD = [(1, 1, 1, 1), (5, 130, 100, 3), (64, 128, 128, 1), (100, 260, 390, 4), (300, 72, 513, 2), (700, 256, 256, 5),
-         (2000, 520, 260, 3), (1000, 640, 1100, 2)]
+         (2000, 520, 260, 3), (1000, 640, 1100, 2),
+         (1500, 1032, 1100, 14), (600, 64, 130, 300)]
 
 
 @pytest.mark.parametrize("rows,n,k,experts", WGRAD)

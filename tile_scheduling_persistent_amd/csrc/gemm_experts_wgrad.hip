@@ -32,6 +32,7 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
 constexpr int kThreads = 256;
 constexpr int BR = 64;  // rows per slab: two steps of 32
+constexpr int kRanked = 256;  // up to so many experts are taken in the order of their rows
 
 template <class F, int... I>
 __device__ __forceinline__ void static_for_of(F&& f, std::integer_sequence<int, I...>) {
@@ -85,12 +86,6 @@ __device__ __forceinline__ void codes_bf16(u32x4 q, unsigned byte, u32x4& lo, u3
   }
 }
 
-// The slab that the loads are at: rows r0 .. of the n from row lo on, of a tile.
-struct Place {
-  int64_t t;
-  int lo, n, r0, n0, k0, e;
-};
-
 // An operand's slab on its way through registers: BR rows of W columns, in parts of
 // 16 bytes per thread (16 codes, or 8 elements of bf16).  Loads go through buffer
 // resources that end with the slab's last row: rows past it read as zeros.
@@ -120,10 +115,10 @@ struct Slab {
     wr[0] = (unsigned)(r * W * 2 + swz(r, k) * 16);
     wr[1] = FP8 ? (unsigned)(r * W * 2 + swz(r, k + 1) * 16) : (unsigned)((r + STEP) * W * 2 + swz(r + STEP, k) * 16);
   }
-  // The slab at `at`, columns c0 .. of `cols`; left: its rows, 0: nothing is read.
-  __device__ __forceinline__ void aim(const Place& at, int left, const void* mat, const uint8_t* scale, int64_t ld,
+  // The slab from row r on, columns c0 .. of `cols`; left: rows from there to the
+  // last (none: nothing is read).
+  __device__ __forceinline__ void aim(int64_t r, int left, const void* mat, const uint8_t* scale, int64_t ld,
                                       int64_t sld, int c0, int cols) {
-    const int64_t r = (int64_t)at.lo + at.r0;
     const int rows = left < BR ? left : BR;
     x = reinterpret_cast<unsigned long long>(mat) + (unsigned long long)(r * ld + c0) * ESZ;
     // up to the last column of the last row
@@ -170,8 +165,10 @@ struct Slab {
 // written to one of two LDS stages while the matrix cores work on the other; a part's
 // next load goes out as soon as it is written.  One barrier per slab, between its
 // two steps: behind it the second step's fragments are in registers already and the
-// next slab's first are read.  The slabs of a program's tiles follow one another
-// without a break.
+// next slab's first are read.
+//
+// A workgroup takes one tile: a tile's time goes with its expert's rows, which only
+// the device knows, and the hardware hands the next workgroup to the next free CU.
 template <int BN, int BK, int DFORM, bool F32>
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   constexpr int TN = BN / 2, TK = BK / 2, SN = TN / 16, SK = TK / 16, NMF = SN * SK;
@@ -182,32 +179,35 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   const int wn = wave >> 1, wk = wave & 1;
   const int npn = (p.N + BN - 1) / BN, npk = (p.K + BK - 1) / BK, per = npn * npk;
   const int np = (p.N + 127) / 128 * 128, kp = (p.K + 127) / 128 * 128;
-  const int64_t total = (int64_t)p.experts * per;
-  const int G = (int)gridDim.x;
 
-  // The tile of program `prog` in round i: programs of one XCD take consecutive
-  // tiles, which share operand panels in its L2, and a round's blocks of tiles move
-  // on by one XCD from round to round, so that an XCD does not keep one part of the
-  // experts.
-  const int per_xcd = p.xcds > 1 && G % p.xcds == 0 ? G / p.xcds : 0;
-  auto tile_of = [&](int64_t i) -> int64_t {
-    int at = (int)blockIdx.x;
-    if (per_xcd) at = (int)(((unsigned)at + (unsigned)(i % p.xcds)) % (unsigned)p.xcds) * per_xcd + at / p.xcds;
-    return i * G + at;
-  };
-  auto open = [&](int64_t t, Place& x) {
-    x.t = t;
-    x.r0 = 0;
-    if (t >= total) return;
-    x.e = __builtin_amdgcn_readfirstlane((int)(t / per));
-    int pn, pk;
-    pgs::decode(pgs::kGrouped, (int)(t - (int64_t)x.e * per), npn, npk, 8, pn, pk);
-    x.n0 = __builtin_amdgcn_readfirstlane(pn) * BN;
-    x.k0 = __builtin_amdgcn_readfirstlane(pk) * BK;
-    const ExpertRows rows = expert_rows(p.offsets, x.e, p.rows);
-    x.lo = __builtin_amdgcn_readfirstlane(rows.lo);
-    x.n = __builtin_amdgcn_readfirstlane(rows.n);
-  };
+  // The tile.  Workgroups go to the XCDs in turn, so that each XCD gets an equal part
+  // of every expert, a compact block of its tiles whose operand panels meet in the
+  // XCD's L2; and the experts with the most rows come first, so that the last
+  // workgroups are short.
+  __shared__ int s_rows[kRanked];
+  int e = (int)(blockIdx.x / (unsigned)per);
+  if (p.experts <= kRanked) {
+    for (int i = tid; i < p.experts; i += kThreads) s_rows[i] = expert_rows(p.offsets, i, p.rows).n;
+    __syncthreads();
+    int* s_e = reinterpret_cast<int*>(smem);
+    for (int i = tid; i < p.experts; i += kThreads) {
+      const int n = s_rows[i];
+      int before = 0;
+      for (int j = 0; j < p.experts; ++j) before += s_rows[j] > n || (s_rows[j] == n && j < i) ? 1 : 0;
+      if (before == e) *s_e = i;
+    }
+    __syncthreads();
+    e = *s_e;
+    __syncthreads();
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  int i_tile = (int)(blockIdx.x % (unsigned)per);
+  if (p.xcds > 1 && per % p.xcds == 0) i_tile = i_tile % p.xcds * (per / p.xcds) + i_tile / p.xcds;
+  int pn, pk;
+  pgs::decode(pgs::kGrouped, i_tile, npn, npk, 8, pn, pk);
+  const int n0 = __builtin_amdgcn_readfirstlane(pn) * BN, k0 = __builtin_amdgcn_readfirstlane(pk) * BK;
+  const ExpertRows rows = expert_rows(p.offsets, e, p.rows);
+  const int lo = __builtin_amdgcn_readfirstlane(rows.lo), n_rows = __builtin_amdgcn_readfirstlane(rows.n);
 
   Slab<BN, DFORM> d;
   Slab<BK, kCodes> a;
@@ -215,11 +215,9 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   const unsigned ldd = (unsigned)p.ldd;
   d.init(ldd, (unsigned)p.rows);
   a.init((unsigned)kp, (unsigned)p.rows);
-  // loads: f the slab that they are at, `left` the rows of the one that the registers
-  // hold
-  Place f;
-  int64_t round = 0;
-  int left = 0;
+  // loads: the slab that they are at starts at row r0; `left`: rows from the start of
+  // the slab that the registers hold
+  int r0 = 0, left = 0;
   auto load = [&](int i) PGK_INLINE {
     if (i < PD)
       d.load(i, ldd);
@@ -233,17 +231,12 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
       a.put(i - PD, s + D_BYTES, left);
   };
   auto aim = [&]() {
-    const int rows = f.t < total ? f.n - f.r0 : 0;
-    d.aim(f, rows, p.D, p.sd, p.ldd, p.rows, f.n0, DFORM == kCodes ? np : p.N);
-    a.aim(f, rows, p.A, p.sa, kp, p.rows, f.k0, kp);
+    d.aim(lo + r0, n_rows - r0, p.D, p.sd, p.ldd, p.rows, n0, DFORM == kCodes ? np : p.N);
+    a.aim(lo + r0, n_rows - r0, p.A, p.sa, kp, p.rows, k0, kp);
   };
-  // An expert without rows has one slab of zeros.
   auto advance = [&]() {
-    left = f.t < total ? f.n - f.r0 : 0;
-    if (f.t < total) {
-      f.r0 += BR;
-      if (f.r0 >= f.n) open(tile_of(++round), f);
-    }
+    left = n_rows - r0;
+    r0 += BR;
     aim();
   };
 
@@ -278,9 +271,9 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
 
   // Lane: row n of the block i16, columns k 4 g4 .. + 3.
   typedef std::conditional_t<F32, float, unsigned short> out_t;
-  auto store = [&](const Place& x) {
-    const int n = x.n0 + wn * TN + i16, k = x.k0 + wk * TK + 4 * g4;
-    const int64_t at = ((int64_t)x.e * p.N + n) * p.K + k;
+  auto store = [&]() {
+    const int n = n0 + wn * TN + i16, k = k0 + wk * TK + 4 * g4;
+    const int64_t at = ((int64_t)e * p.N + n) * p.K + k;
     out_t* out = static_cast<out_t*>(p.dB) + at;
     const out_t* base = static_cast<const out_t*>(p.base) + at;
 #pragma unroll
@@ -323,33 +316,27 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
 
   const std::integral_constant<int, 0> step0;
   const std::integral_constant<int, 1> step1;
-  Place ct = {};
-  open(tile_of(0), ct);
-  if (ct.t >= total) return;
-  f = ct;
-  aim();
 #pragma unroll
-  for (int i = 0; i < NP; ++i) load(i);
-  advance();
+  for (int i = 0; i < SN; ++i)
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    put(i, smem);
-    load(i);
-  }
-  advance();
-  slab_barrier();
+    for (int j = 0; j < SK; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  acc_written();
+  if (n_rows > 0) {
+    aim();
 #pragma unroll
-  for (int i = 0; i < NR; ++i) read(smem, step0, i);
-  int turn = 0;
-  int64_t ct_round = 0;
-  while (ct.t < total) {
+    for (int i = 0; i < NP; ++i) load(i);
+    advance();
 #pragma unroll
-    for (int i = 0; i < SN; ++i)
+    for (int i = 0; i < NP; ++i) {
+      put(i, smem);
+      load(i);
+    }
+    advance();
+    slab_barrier();
 #pragma unroll
-      for (int j = 0; j < SK; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    acc_written();
-    const int slabs = ct.n > 0 ? (ct.n + BR - 1) / BR : 1;
-    for (int s = 0; s < slabs; ++s, turn ^= 1) {
+    for (int i = 0; i < NR; ++i) read(smem, step0, i);
+    int turn = 0;
+    for (int s = 0; s < n_rows; s += BR, turn ^= 1) {
       unsigned char* now = smem + turn * STAGE;
       unsigned char* next = smem + (turn ^ 1) * STAGE;
       static_for<NMF>([&](auto jc) PGK_INLINE {
@@ -376,33 +363,33 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
         __builtin_amdgcn_sched_barrier(0);
       });
     }
-    mfma_results_ready();
-    store(ct);
-    open(tile_of(++ct_round), ct);
   }
+  mfma_results_ready();
+  store();
 }
 
-// Resident workgroups per CU, asked for once per kernel and device.
+// A built tile: its kernel and dynamic LDS; the limit of the latter is raised once per
+// device.
 constexpr int kDevices = 64;
 struct Instance {
-  int lds;
+  int bn, bk, lds;
   void (*kern)(WgradParams);
-  mutable std::atomic<int> resident[kDevices] = {};
-  int per_cu() const {
+  mutable std::atomic<bool> ready[kDevices] = {};
+  hipError_t launch(const WgradParams& p, hipStream_t stream) const {
     int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices)
-      return occupancy_of(reinterpret_cast<const void*>(kern), kThreads, lds);
-    int n = resident[dev].load(std::memory_order_acquire);
-    if (n == 0) {
-      n = occupancy_of(reinterpret_cast<const void*>(kern), kThreads, lds);
-      resident[dev].store(n, std::memory_order_release);
+    const bool known = hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kDevices;
+    if (!known || !ready[dev].load(std::memory_order_acquire)) {
+      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (known) ready[dev].store(true, std::memory_order_release);
     }
-    return n;
+    const int64_t tiles = (int64_t)p.experts * ((p.N + bn - 1) / bn) * ((p.K + bk - 1) / bk);
+    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(kThreads), lds, stream, p);
+    return hipGetLastError();
   }
 };
 template <int BN, int BK, int DFORM, bool F32>
 Instance tiled() {
-  return {2 * BR * (BN + BK) * 2, wgrad_kernel<BN, BK, DFORM, F32>};
+  return {BN, BK, 2 * BR * (BN + BK) * 2, wgrad_kernel<BN, BK, DFORM, F32>};
 }
 
 }  // namespace
@@ -415,13 +402,8 @@ hipError_t launch_gemm_experts_wgrad(const WgradParams& p, int cus, hipStream_t 
                                        {tiled<128, 128, kNarrow, false>(), tiled<128, 128, kNarrow, true>()}};
   const int64_t tiles = (int64_t)p.experts * ((p.N + 255) / 256) * ((p.K + 255) / 256);
   const int f32 = p.out_f32 ? 1 : 0;
-  const Instance* i;
-  if (!p.sd && ((reinterpret_cast<uintptr_t>(p.D) & 15) != 0 || (p.ldd & 7) != 0))
-    i = &small[2][f32];
-  else
-    i = &(tiles >= cus ? big : small)[p.sd ? 1 : 0][f32];
-  hipLaunchKernelGGL(i->kern, dim3(cus * i->per_cu()), dim3(kThreads), i->lds, stream, p);
-  return hipGetLastError();
+  if (!p.sd && ((reinterpret_cast<uintptr_t>(p.D) & 15) != 0 || (p.ldd & 7) != 0)) return small[2][f32].launch(p, stream);
+  return (tiles >= cus ? big : small)[p.sd ? 1 : 0][f32].launch(p, stream);
 }
 
 }  // namespace pgk

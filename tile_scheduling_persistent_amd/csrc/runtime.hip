@@ -1619,6 +1619,8 @@ pgemm_status pgemm_run_experts_wgrad(pgemm_config* cfg, const void* D, int d_typ
   if ((!fp8 && d_type != PMX_BF16) || b_type == PMX_F16 || experts > PMOE_MAX_EXPERTS || N >= 1 << 22 || K >= 1 << 22 ||
       (!fp8 && ldd >= 1 << 24))
     return PGEMM_ERR_UNSUPPORTED;
+  // a workgroup each for tiles of 128 x 128, of 2^32 threads in all at most
+  if ((unsigned __int128)experts * ((N + 127) / 128) * ((K + 127) / 128) >= 1 << 24) return PGEMM_ERR_UNSUPPORTED;
   const size_t bs = type_size(b_type), bb = span_bytes((int64_t)experts * N, K, bs);
   CallBuffersCheck in(cfg->device);
   in.add(D, fp8 ? fp8_bytes(rows, N) : matrix_bytes(rows, N, ldd, 2), fp8 ? 1 : 2, false);
