@@ -26,9 +26,10 @@ def sort(ids, experts: int):
     row = 0
     for e in range(experts):
         offsets[e] = row
-        for s in np.flatnonzero(flat == e):
-            place[s], order[row] = row, s
-            row += 1
+        slots = np.flatnonzero(flat == e)
+        place[slots] = row + np.arange(len(slots))
+        order[row:row + len(slots)] = slots
+        row += len(slots)
     offsets[experts] = row
     return place.reshape(ids.shape), order, offsets
 

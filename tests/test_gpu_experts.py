@@ -51,7 +51,8 @@ def routed(rng, tokens, topk, experts, dropped=0.2):
 
 @pytest.mark.parametrize("tokens,topk,experts", [(0, 2, 3), (1, 1, 1), (1, 8, 64), (7, 3, 2), (64, 8, 64), (333, 6, 160),
                                                  (2048, 8, 1024), (16384, 1, 5), (16385, 1, 5), (5000, 8, 256),
-                                                 (40000, 4, 1024)])
+                                                 (65536, 1, 70), (65537, 1, 1024), (131072 + 5, 2, 1024),
+                                                 (300000, 1, 3)])
 @pytest.mark.parametrize("wide", [False, True])
 def test_sort(tokens, topk, experts, wide):
     note(f"sort {tokens} {topk} {experts} {wide}")
@@ -66,7 +67,7 @@ def test_sort(tokens, topk, experts, wide):
     assert np.array_equal(place.cpu(), want[0]) and np.array_equal(order.cpu(), want[1])
 
 
-@pytest.mark.parametrize("tokens", [100, 30000])
+@pytest.mark.parametrize("tokens", [100, 30000, 140000])
 @pytest.mark.parametrize("what", ["one expert", "no rows", "last expert"])
 def test_sort_when_slots_agree(tokens, what):
     note(f"sort {tokens} {what}")

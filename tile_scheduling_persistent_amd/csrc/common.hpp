@@ -183,7 +183,7 @@ struct Fp8WeightsParams {
 
 // Tokens routed to experts (pmoe_*).
 constexpr int kMaxExperts = 1024;
-constexpr int64_t kSortSmall = 16384;  // slots that one workgroup sorts
+constexpr int64_t kSortOnce = 32768;  // slots up to which the sort is one launch
 struct SortParams {
   const void* ids;  // [slots] int32 or int64
   int ids64;

@@ -14,16 +14,13 @@ namespace {
 
 // ------------------------------------------------------------------- the sort
 //
-// A wave takes a stretch of consecutive slots.  Its lanes' counts per expert go
-// through LDS atomics (a sum, in any order); then, with the first row of each
-// wave's slots of each expert known, it walks its stretch again, 64 slots at a
-// time, and a slot's row is that first row plus the number of equal lanes below.
+// A slot's row is its expert's first row, plus the slots of that expert in earlier
+// parts of the slots (a part to a workgroup) and in earlier waves of the part, plus
+// the equal lanes below it in its wave.
 
 template <typename I>
-__device__ __forceinline__ int expert_of(const SortParams& p, int64_t slot, int64_t end) {
-  if (slot >= end) return -1;
-  const int64_t e = (int64_t)static_cast<const I*>(p.ids)[slot];
-  return e >= 0 && e < p.experts ? (int)e : -1;
+__device__ __forceinline__ int expert_in(const SortParams& p, I id) {
+  return id >= 0 && id < p.experts ? (int)id : -1;
 }
 
 // Lanes with the same expert as this one (experts below 2^bits).
@@ -37,33 +34,17 @@ __device__ __forceinline__ unsigned long long same_lanes(int e, int bits) {
   return m;
 }
 
-// Adds the slots [begin, end) to the wave's counts.
-template <typename I>
-__device__ __forceinline__ void count_slots(const SortParams& p, int64_t begin, int64_t end, int* cnt) {
-  for (int64_t s = begin + (threadIdx.x & 63); s < end; s += 64) {
-    const int e = expert_of<I>(p, s, end);
-    if (e >= 0) atomicAdd(cnt + e, 1);
-  }
+// Adds a slot to counts in LDS, kCopies of each: atomics on one word take turns, and
+// routers have favourites.
+constexpr int kCopies = 4;
+__device__ __forceinline__ void count_slot(int e, int* cnt) {
+  if (e >= 0) atomicAdd(cnt + e * kCopies + (threadIdx.x & (kCopies - 1)), 1);
 }
-
-// Rows of the slots [begin, end), from the wave's first rows `cnt`.
-template <typename I>
-__device__ __forceinline__ void place_slots(const SortParams& p, int64_t begin, int64_t end, int* cnt, bool order) {
-  const int lane = threadIdx.x & 63;
-  const unsigned long long below = (1ull << lane) - 1ull;
-  for (int64_t s0 = begin; s0 < end; s0 += 64) {
-    const int64_t s = s0 + lane;
-    const int e = expert_of<I>(p, s, end);
-    const unsigned long long m = same_lanes(e, p.bits);
-    const int first = e >= 0 ? __ffsll(m) - 1 : lane;
-    int row = 0;
-    if (e >= 0 && lane == first) row = atomicAdd(cnt + e, __popcll(m));
-    row = __shfl(row, first) + __popcll(m & below);
-    if (s < end) {
-      p.place[s] = e >= 0 ? row : -1;
-      if (order && e >= 0) p.order[row] = (int)s;
-    }
-  }
+__device__ __forceinline__ int counted(const int* cnt, int e) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) n += cnt[e * kCopies + i];
+  return n;
 }
 
 // Exclusive prefix sums over the workgroup's threads; *total: the sum.
@@ -89,71 +70,103 @@ __device__ __forceinline__ int block_prefix(int v, int* s_wave, int* total) {
 }
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-// Experts: one thread each.
 static_assert(kMaxExperts <= kSortThreads, "a thread per expert");
 
-// Few slots: one workgroup, one launch.
+// Rows of the slots of one part, a slot per thread, from each expert's first row of
+// the part (`at`, thread e's), by way of s_cnt [waves][experts].
 template <typename I>
-__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortParams p) {
-  extern __shared__ int s_cnt[];  // [waves][experts]
-  __shared__ int s_wave[kSortWaves];
-  const int tid = threadIdx.x, wave = tid >> 6, E = p.experts;
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
-  __syncthreads();
-  const int64_t per = (p.slots + kSortThreads - 1) / kSortThreads * 64;
-  const int64_t begin = wave * per < p.slots ? wave * per : p.slots;
-  const int64_t end = begin + per < p.slots ? begin + per : p.slots;
-  count_slots<I>(p, begin, end, s_cnt + wave * E);
-  __syncthreads();
-  int mine = 0;
-  if (tid < E)
-    for (int w = 0; w < kSortWaves; ++w) mine += s_cnt[w * E + tid];
-  int total;
-  int at = block_prefix<kSortThreads>(mine, s_wave, &total);
-  if (tid < E) {
-    p.offsets[tid] = at;
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int n = s_cnt[w * E + tid];
-      s_cnt[w * E + tid] = at;
-      at += n;
+__device__ __forceinline__ void place_part(const SortParams& p, int64_t begin, int64_t end, int at, int* s_cnt, bool order) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = p.experts;
+  for (int64_t s0 = begin; s0 < end; s0 += kSortThreads) {
+    for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
+    __syncthreads();
+    const int64_t s = s0 + tid;
+    const int e = s < end ? expert_in(p, static_cast<const I*>(p.ids)[s]) : -1;
+    const unsigned long long m = same_lanes(e, p.bits);
+    const int below = __popcll(m & ((1ull << lane) - 1ull));
+    if (e >= 0 && below == 0) s_cnt[wave * E + e] = __popcll(m);
+    __syncthreads();
+    if (tid < E)
+      for (int w = 0; w < kSortWaves; ++w) {
+        const int n = s_cnt[w * E + tid];
+        s_cnt[w * E + tid] = at;
+        at += n;
+      }
+    __syncthreads();
+    if (s < end) {
+      const int row = e >= 0 ? s_cnt[wave * E + e] + below : -1;
+      p.place[s] = row;
+      if (order && e >= 0) p.order[row] = (int)s;
     }
+    __syncthreads();
   }
-  if (tid == 0) p.offsets[E] = total;
-  __syncthreads();
-  place_slots<I>(p, begin, end, s_cnt + wave * E, true);
-  for (int64_t r = total + tid; r < p.slots; r += kSortThreads) p.order[r] = -1;
 }
 
-// Many slots: a count per workgroup and expert, kept in `order` until the last
-// of three launches writes that.
-constexpr int kPartThreads = 256, kPartWaves = kPartThreads / 64;
+// One launch: every workgroup counts all slots, those before its part and the
+// others, in LDS.  Counting again what the others count costs less than launches that
+// pass counts on up to some ten thousand slots (64 experts, us: 32768 slots 8.8; 65536
+// slots 13.3, and 12.0 in three launches).
 template <typename I>
-__global__ void __launch_bounds__(kPartThreads) sort_count_kernel(SortParams p) {
-  extern __shared__ int s_cnt[];  // [experts]
-  const int E = p.experts;
-  for (int i = threadIdx.x; i < E; i += kPartThreads) s_cnt[i] = 0;
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(SortParams p) {
+  extern __shared__ int s_cnt[];  // [waves][experts]; before that [2][experts][copies]
+  __shared__ int s_wave[kSortWaves];
+  const int tid = threadIdx.x, E = p.experts;
+  int* s_before = s_cnt;
+  int* s_rest = s_cnt + E * kCopies;
+  for (int i = tid; i < 2 * E * kCopies; i += kSortThreads) s_cnt[i] = 0;
   __syncthreads();
-  const int64_t begin = blockIdx.x * p.part, end = begin + p.part < p.slots ? begin + p.part : p.slots;
-  for (int64_t s = begin + threadIdx.x; s < end; s += kPartThreads) {
-    const int e = expert_of<I>(p, s, end);
-    if (e >= 0) atomicAdd(s_cnt + e, 1);
+  const int64_t begin = (int64_t)blockIdx.x * kSortThreads;
+  const int64_t end = begin + kSortThreads < p.slots ? begin + kSortThreads : p.slots;
+  constexpr int AT_ONCE = 4;  // loads on their way together
+  for (int64_t s0 = 0; s0 < p.slots; s0 += AT_ONCE * kSortThreads) {
+    I id[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int64_t s = s0 + i * kSortThreads + tid;
+      id[i] = s < p.slots ? static_cast<const I*>(p.ids)[s] : (I)-1;
+    }
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) count_slot(expert_in(p, id[i]), s0 + i * kSortThreads < begin ? s_before : s_rest);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < E; i += kPartThreads) p.order[(int64_t)blockIdx.x * E + i] = s_cnt[i];
+  const int before = tid < E ? counted(s_before, tid) : 0, all = tid < E ? before + counted(s_rest, tid) : 0;
+  int total;
+  const int at = block_prefix<kSortThreads>(all, s_wave, &total);
+  if (blockIdx.x == 0) {
+    if (tid < E) p.offsets[tid] = at;
+    if (tid == 0) p.offsets[E] = total;
+  }
+  place_part<I>(p, begin, end, at + before, s_cnt, true);
+  if (begin + tid < end && begin + tid >= total) p.order[begin + tid] = -1;
+}
+
+// More slots: a count per workgroup and expert, kept in `order` until the last of
+// three launches writes that.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortParams p) {
+  extern __shared__ int s_cnt[];  // [experts][copies]
+  const int E = p.experts;
+  for (int i = threadIdx.x; i < E * kCopies; i += kSortThreads) s_cnt[i] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * p.part, end = begin + p.part < p.slots ? begin + p.part : p.slots;
+  for (int64_t s0 = begin; s0 < end; s0 += kSortThreads) {
+    const int64_t s = s0 + threadIdx.x;
+    count_slot(s < end ? expert_in(p, static_cast<const I*>(p.ids)[s]) : -1, s_cnt);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < E; i += kSortThreads) p.order[(int64_t)blockIdx.x * E + i] = counted(s_cnt, i);
 }
 
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) {
-  extern __shared__ int s_cnt[];  // [waves][experts]
+  extern __shared__ int s_cnt[];  // [waves][experts]; before that [2][experts]
   __shared__ int s_wave[kSortWaves];
-  const int tid = threadIdx.x, wave = tid >> 6, E = p.experts;
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
+  const int tid = threadIdx.x, E = p.experts;
+  int* s_before = s_cnt;
+  int* s_all = s_cnt + E;
+  if (tid < E) s_before[tid] = s_all[tid] = 0;
   __syncthreads();
-  // all of an expert's slots, and those of the workgroups before this one: the
-  // threads share the parts out, then one thread per expert adds up
-  const int lanes = kSortThreads / E > 0 ? kSortThreads / E : 1;  // threads per expert
-  int* s_all = s_cnt;            // [E]
-  int* s_before = s_cnt + E;     // [E]
+  const int lanes = kSortThreads / E;  // threads per expert
   if (tid < lanes * E) {
     const int e = tid % E;
     int all = 0, before = 0;
@@ -168,30 +181,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) 
   __syncthreads();
   const int all = tid < E ? s_all[tid] : 0, before = tid < E ? s_before[tid] : 0;
   int total;
-  int at = block_prefix<kSortThreads>(all, s_wave, &total);
+  const int at = block_prefix<kSortThreads>(all, s_wave, &total);
   if (blockIdx.x == 0) {
     if (tid < E) p.offsets[tid] = at;
     if (tid == 0) p.offsets[E] = total;
   }
-  __syncthreads();
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
-  __syncthreads();
-  const int64_t b0 = blockIdx.x * p.part, b1 = b0 + p.part < p.slots ? b0 + p.part : p.slots;
-  const int64_t per = (p.part + kSortThreads - 1) / kSortThreads * 64;
-  const int64_t begin = b0 + wave * per < b1 ? b0 + wave * per : b1;
-  const int64_t end = begin + per < b1 ? begin + per : b1;
-  count_slots<I>(p, begin, end, s_cnt + wave * E);
-  __syncthreads();
-  if (tid < E) {
-    at += before;
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int n = s_cnt[w * E + tid];
-      s_cnt[w * E + tid] = at;
-      at += n;
-    }
-  }
-  __syncthreads();
-  place_slots<I>(p, begin, end, s_cnt + wave * E, false);
+  const int64_t begin = blockIdx.x * p.part, end = begin + p.part < p.slots ? begin + p.part : p.slots;
+  place_part<I>(p, begin, end, at + before, s_cnt, false);
 }
 
 __global__ void __launch_bounds__(256) sort_order_kernel(SortParams p) {
@@ -205,17 +201,23 @@ __global__ void __launch_bounds__(256) sort_order_kernel(SortParams p) {
 template <typename I>
 hipError_t sort_typed(SortParams p, hipStream_t stream) {
   const int lds = kSortWaves * p.experts * (int)sizeof(int);
-  if (p.slots <= kSortSmall) {
-    if (lds > 65536 - 256) (void)hipFuncSetAttribute((const void*)sort_small_kernel<I>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    hipLaunchKernelGGL(sort_small_kernel<I>, dim3(1), dim3(kSortThreads), lds, stream, p);
+  static_assert(kSortWaves >= 2 * kCopies, "the first counts fit where the waves' counts go");
+  auto allow = [&](const void* kern) {
+    if (lds > 65536 - 256) (void)hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  };
+  if (p.slots <= kSortOnce) {
+    allow((const void*)sort_kernel<I>);
+    const unsigned grid = p.slots > 0 ? (unsigned)((p.slots + kSortThreads - 1) / kSortThreads) : 1u;
+    hipLaunchKernelGGL(sort_kernel<I>, dim3(grid), dim3(kSortThreads), lds, stream, p);
     return hipGetLastError();
   }
-  // parts of at least 4096 slots: the counts of all parts, at most a quarter of the slots and one part's more, fit in `order`
-  p.part = (p.slots + 255) / 256;
-  if (p.part < 4096) p.part = 4096;
+  // at most 256 parts, of at least two slots per expert: their counts fit in `order`
+  p.part = (p.slots + 255) / 256 > 2 * p.experts ? (p.slots + 255) / 256 : 2 * p.experts;
+  p.part = (p.part + kSortThreads - 1) / kSortThreads * kSortThreads;
+  static_assert(kSortOnce >= 2 * kMaxExperts, "and those of the last one");
   p.parts = (int)((p.slots + p.part - 1) / p.part);
-  if (lds > 65536 - 256) (void)hipFuncSetAttribute((const void*)sort_place_kernel<I>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  hipLaunchKernelGGL(sort_count_kernel<I>, dim3(p.parts), dim3(kPartThreads), p.experts * sizeof(int), stream, p);
+  allow((const void*)sort_place_kernel<I>);
+  hipLaunchKernelGGL(sort_count_kernel<I>, dim3(p.parts), dim3(kSortThreads), p.experts * kCopies * sizeof(int), stream, p);
   hipLaunchKernelGGL(sort_place_kernel<I>, dim3(p.parts), dim3(kSortThreads), lds, stream, p);
   hipLaunchKernelGGL(sort_order_kernel, dim3((unsigned)((p.slots + 255) / 256)), dim3(256), 0, stream, p);
   return hipGetLastError();
@@ -229,12 +231,14 @@ __device__ __forceinline__ int slot_of(const int* order, int64_t row, int64_t sl
   return s >= 0 && s < slots ? s : -1;
 }
 
-template <int T, int RW, bool QUANT>
+// NT: codes non-temporal.  A token's row is read once for each of its slots, and codes
+// in the caches would push the tokens out.
+template <int T, int RW, bool QUANT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
   constexpr int ROWS = 4 * RW;
   __shared__ TileScales<RW> s_scale;
   __shared__ int s_slot[ROWS];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slots = p.tokens * p.topk;
   const int64_t kp = (p.cols + 127) / 128 * 128, ctiles = (p.cols + kRowCols - 1) / kRowCols;
   const int64_t tiles = (slots + ROWS - 1) / ROWS * ctiles;
@@ -258,8 +262,13 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
         for (int e = 0; e < 8; ++e) x[e] = vec8_get(v[r], e);
         unsigned byte;
         const u32x2_d o = e4m3_codes(x, byte);
-        if (slot[r] >= 0 && c < kp)
-          *reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.Y) + (row0 + r) * kp + c) = o;
+        if (slot[r] >= 0 && c < kp) {
+          u32x2_d* q = reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.Y) + (row0 + r) * kp + c);
+          if constexpr (NT)
+            __builtin_nontemporal_store(o, q);
+          else
+            *q = o;
+        }
         s_scale.put(lane, wave * RW + r, byte);
         if (lane == 0) s_slot[wave * RW + r] = slot[r];
       } else if (slot[r] >= 0) {
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
 template <int T, int RW, bool QUANT>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradParams p) {
   constexpr int ROWS = 4 * RW;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slots = p.tokens * p.topk, kp = (p.cols + 127) / 128 * 128;
   const int64_t tiles = (slots + ROWS - 1) / ROWS;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -385,21 +394,26 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradPa
   }
 }
 
+// Codes go past the caches where they would fill most of the Infinity Cache.
+constexpr int64_t kPastCaches = 128ll << 20;
+
 template <int T>
 void gather_typed(const GatherParams& p, hipStream_t stream) {
   const int64_t slots = p.tokens * p.topk;
   const bool tall = row_tiles(slots, p.cols, 8) >= 2 * p.cus;
   const dim3 grid = row_grid(row_tiles(slots, p.cols, tall ? 8 : 1)), block(kRowThreads);
   if (p.y_scale) {
-    if (tall)
-      hipLaunchKernelGGL((gather_kernel<T, 8, true>), grid, block, 0, stream, p);
+    if (tall && slots * p.cols >= kPastCaches)
+      hipLaunchKernelGGL((gather_kernel<T, 8, true, true>), grid, block, 0, stream, p);
+    else if (tall)
+      hipLaunchKernelGGL((gather_kernel<T, 8, true, false>), grid, block, 0, stream, p);
     else
-      hipLaunchKernelGGL((gather_kernel<T, 1, true>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((gather_kernel<T, 1, true, false>), grid, block, 0, stream, p);
   } else {
     if (tall)
-      hipLaunchKernelGGL((gather_kernel<T, 8, false>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((gather_kernel<T, 8, false, false>), grid, block, 0, stream, p);
     else
-      hipLaunchKernelGGL((gather_kernel<T, 1, false>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((gather_kernel<T, 1, false, false>), grid, block, 0, stream, p);
   }
 }
 
