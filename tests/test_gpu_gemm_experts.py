@@ -60,7 +60,7 @@ def check(C, offsets, ref, terms, k, dtype):
 
 
 # rows per expert from none to many: every kernel and tile
-SHAPES = [(1, 128, 128, 1), (1, 70, 256, 5), (8, 256, 384, 64), (17, 129, 128, 2), (40, 1000, 640, 3), (64, 513, 1024, 1),
+SHAPES = [(1, 128, 128, 1), (24, 300, 1280, 1), (50, 1100, 384, 20), (60, 4100, 256, 6), (1, 70, 256, 5), (8, 256, 384, 64), (17, 129, 128, 2), (40, 1000, 640, 3), (64, 513, 1024, 1),
           (130, 300, 1152, 4), (200, 256, 2048, 6), (700, 300, 512, 3), (1100, 777, 256, 2), (2000, 512, 384, 9),
           (3000, 1030, 128, 5), (5000, 4200, 256, 3), (4000, 3000, 128, 20)]
 

@@ -606,20 +606,58 @@ Instance tiled() {
 
 }  // namespace
 
+// The kernel and tile of a call, from its sizes alone (the experts' row counts are in
+// device memory).  `few`: experts that can have rows.
+//
+// Streaming, for up to 12 rows per expert: rows of B at 6 TB/s (us, 4096 x 4096, 64
+// experts, 32 / 64 columns a tile, against 128 x 128 tiles: 8 rows 28.5 / 24.8, 128
+// rows 152 / 151 and more than 218, 512 rows 198 / 191 and 220, 1024 rows 282 / 243
+// and 229; one matrix of 8192 x 8192, 1 row 15.5 / 20.4 and 32.5).  64 columns where
+// their tiles give every CU one.  Up to 64 rows too where 128 x 128 tiles would leave
+// half of the CUs idle, with tiles of 32 or 64 rows (8192 x 8192, 32 rows 19.6 against
+// 33.7; 64 rows 29.2 against 35.5).
+//
+// Tiles: the least of the estimated times, rounds of tiles times what a CU needs for
+// one, us for a 128-deep slab and for the rest (128 x 128 0.57 and 2, 128 x 256 0.83
+// and 3, both on rings of three slabs; 256 x 256 1.45 and 8).  us measured, 128 x 128 /
+// 128 x 256 / 256 x 256: 64 experts x 4096 x 4096, 4096 rows 245 / 247 / 281, 16384
+// rows 421 / 350 / 380, 32768 rows 712 / 580 / 586; one of 8192 x 8192, 512 rows 39 / 56
+// / 96, 1024 rows 77 / 59 / 96, 4096 rows 280 / 217 / 202.
 hipError_t launch_gemm_experts(const ExpertsParams& p, int cus, hipStream_t stream) {
-  const int tables = tables_bytes(p.experts);
-  if (p.rows > 64LL * p.experts) {
-    static const Instance big[2] = {tiled<256, 256, 2, 2, false>(), tiled<256, 256, 2, 2, true>()};
-    static const Instance small[2] = {tiled<128, 128, 2, 2, false>(), tiled<128, 128, 2, 2, true>()};
-    const Instance& i = (p.rows > 256LL * p.experts ? big : small)[p.out_f32 ? 1 : 0];
-    const int grid = cus * i.per_cu();
-    hipLaunchKernelGGL(i.kern, dim3(grid), dim3(i.threads), i.lds + tables, stream, p);
+  const int tables = tables_bytes(p.experts), f32 = p.out_f32 ? 1 : 0;
+  const int64_t few = p.rows < p.experts ? p.rows : p.experts;
+  auto columns = [&](int bn) { return (int64_t)(p.N + bn - 1) / bn; };
+  if (p.rows <= 12LL * p.experts || (p.rows <= 64LL * p.experts && 2 * few * columns(128) <= cus)) {
+    typedef void (*kern_t)(ExpertsParams);
+    static const kern_t all[4][2] = {
+        {gemm_experts_stream_kernel<1, 2, 4, 4, false>, gemm_experts_stream_kernel<1, 2, 4, 4, true>},
+        {gemm_experts_stream_kernel<1, 4, 2, 4, false>, gemm_experts_stream_kernel<1, 4, 2, 4, true>},
+        {gemm_experts_stream_kernel<2, 2, 2, 4, false>, gemm_experts_stream_kernel<2, 2, 2, 4, true>},
+        {gemm_experts_stream_kernel<4, 2, 2, 4, false>, gemm_experts_stream_kernel<4, 2, 2, 4, true>}};
+    const int i = p.rows > 32LL * p.experts ? 3 : p.rows > 16LL * p.experts ? 2 : few * columns(64) >= cus ? 1 : 0;
+    hipLaunchKernelGGL(all[i][f32], dim3(4 * cus), dim3(256), tables, stream, p);
     return hipGetLastError();
   }
-  if (p.out_f32)
-    hipLaunchKernelGGL((gemm_experts_stream_kernel<1, 1, 4, 8, true>), dim3(2 * cus), dim3(512), tables, stream, p);
-  else
-    hipLaunchKernelGGL((gemm_experts_stream_kernel<1, 1, 4, 8, false>), dim3(2 * cus), dim3(512), tables, stream, p);
+  static const Instance all[3][2] = {{tiled<128, 128, 3, 2, false>(), tiled<128, 128, 3, 2, true>()},
+                                     {tiled<128, 256, 3, 2, false>(), tiled<128, 256, 3, 2, true>()},
+                                     {tiled<256, 256, 2, 2, false>(), tiled<256, 256, 2, 2, true>()}};
+  static const double cost[3][2] = {{0.57, 2}, {0.83, 3}, {1.45, 8}};
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 3; ++i) {
+    const Instance& x = all[i][0];
+    // an expert's last tile is half full, but has one tile at least
+    int64_t row_tiles = p.experts == 1 ? (p.rows + x.bm - 1) / x.bm : p.rows / x.bm + p.experts / 2;
+    if (row_tiles < few) row_tiles = few;
+    const int64_t rounds = (row_tiles * columns(x.bn) + cus - 1) / cus;
+    const double us = (double)rounds * (cost[i][0] * (p.K >> 7) + cost[i][1]);
+    if (i == 0 || us < least) {
+      least = us;
+      best = i;
+    }
+  }
+  const Instance& x = all[best][f32];
+  hipLaunchKernelGGL(x.kern, dim3(cus * x.per_cu()), dim3(x.threads), x.lds + tables, stream, p);
   return hipGetLastError();
 }
 
