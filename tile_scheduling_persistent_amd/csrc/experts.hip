@@ -231,56 +231,64 @@ __device__ __forceinline__ int slot_of(const int* order, int64_t row, int64_t sl
   return s >= 0 && s < slots ? s : -1;
 }
 
-// NT: codes non-temporal.  A token's row is read once for each of its slots, and codes
-// in the caches would push the tokens out.
-template <int T, int RW, bool QUANT, bool NT>
+// A workgroup takes 128 columns of 16 * R rows, 16 lanes to a row.  The tiles of eight
+// stretches of 128 columns go round the XCDs, all rows before the next eight: an
+// XCD's workgroups then read the same 256 bytes of every token (16 bits), 2 MiB of
+// 8192 tokens, which stay in its L2 although a token is read for each of its slots in
+// the order of the experts (8192 x 8 x 4096 to e4m3, with the sort: a row's columns side
+// by side 105.6 us, XX).  The output is written in whole lines, past the caches where it
+// would fill them (NT).
+template <int T, int R, bool QUANT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
-  constexpr int ROWS = 4 * RW;
-  __shared__ TileScales<RW> s_scale;
+  constexpr int ROWS = 16 * R;
+  __shared__ unsigned char s_scale[ROWS];
   __shared__ int s_slot[ROWS];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t slots = p.tokens * p.topk;
-  const int64_t kp = (p.cols + 127) / 128 * 128, ctiles = (p.cols + kRowCols - 1) / kRowCols;
-  const int64_t tiles = (slots + ROWS - 1) / ROWS * ctiles;
+  const int tid = threadIdx.x, lane16 = tid & 15, sub = tid >> 4;
+  const int64_t slots = p.tokens * p.topk, groups = (p.cols + 127) / 128, kp = groups * 128;
+  const int64_t rtiles = (slots + ROWS - 1) / ROWS, tiles = rtiles * groups;
+  const double per_topk = 1.0 / (double)p.topk;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t rt = tile / ctiles, ct = tile - rt * ctiles;
-    const int64_t row0 = rt * ROWS + wave * RW, c = ct * kRowCols + lane * 8;
-    int slot[RW];
-    Vec8<T> v[RW];
+    const int64_t eight = tile / (8 * rtiles), in = tile - eight * 8 * rtiles;
+    const int64_t wide = groups - eight * 8 < 8 ? groups - eight * 8 : 8;
+    const int64_t rt = in / wide, g = eight * 8 + in - rt * wide;
+    const int64_t c = g * 128 + lane16 * 8;
+    int slot[R];
+    Vec8<T> v[R];
 #pragma unroll
-    for (int r = 0; r < RW; ++r) slot[r] = slot_of(p.order, row0 + r, slots);
+    for (int r = 0; r < R; ++r) slot[r] = slot_of(p.order, rt * ROWS + r * 16 + sub, slots);
 #pragma unroll
-    for (int r = 0; r < RW; ++r) {
-      const int64_t token = slot[r] >= 0 ? (unsigned)slot[r] / (unsigned)p.topk : 0;
+    for (int r = 0; r < R; ++r) {
+      // slot / topk: a 64-bit product is off by less than the half
+      const int token = slot[r] >= 0 ? (int)(((double)slot[r] + 0.5) * per_topk) : 0;
       v[r] = vec8_load<T>(static_cast<const char*>(p.X) + token * p.ldx * size_of(T), c, p.cols);
     }
 #pragma unroll
-    for (int r = 0; r < RW; ++r) {
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = rt * ROWS + r * 16 + sub;
       if (QUANT) {
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = vec8_get(v[r], e);
         unsigned byte;
         const u32x2_d o = e4m3_codes(x, byte);
-        if (slot[r] >= 0 && c < kp) {
-          u32x2_d* q = reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.Y) + (row0 + r) * kp + c);
+        if (slot[r] >= 0) {
+          u32x2_d* q = reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.Y) + row * kp + c);
           if constexpr (NT)
             __builtin_nontemporal_store(o, q);
           else
             *q = o;
         }
-        s_scale.put(lane, wave * RW + r, byte);
-        if (lane == 0) s_slot[wave * RW + r] = slot[r];
+        if (lane16 == 0) {
+          s_scale[r * 16 + sub] = (unsigned char)byte;
+          s_slot[r * 16 + sub] = slot[r];
+        }
       } else if (slot[r] >= 0) {
-        vec8_store<T>(static_cast<char*>(p.Y) + (row0 + r) * p.ldy * size_of(T), c, p.cols, v[r]);
+        vec8_store<T, false, NT>(static_cast<char*>(p.Y) + row * p.ldy * size_of(T), c, p.cols, v[r]);
       }
     }
     if (QUANT) {
       __syncthreads();
-      for (int i = threadIdx.x; i < 4 * ROWS; i += kRowThreads) {
-        const int64_t g = ct * 4 + i / ROWS, row = rt * ROWS + i % ROWS;
-        if (g < kp / 128 && s_slot[i % ROWS] >= 0) p.y_scale[g * slots + row] = s_scale.b[i / ROWS][i % ROWS];
-      }
+      if (tid < ROWS && s_slot[tid] >= 0) p.y_scale[g * slots + rt * ROWS + tid] = s_scale[tid];
       __syncthreads();
     }
   }
@@ -394,27 +402,22 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradPa
   }
 }
 
-// Codes go past the caches where they would fill most of the Infinity Cache.
 constexpr int64_t kPastCaches = 128ll << 20;
 
-template <int T>
+template <int T, bool QUANT>
 void gather_typed(const GatherParams& p, hipStream_t stream) {
-  const int64_t slots = p.tokens * p.topk;
-  const bool tall = row_tiles(slots, p.cols, 8) >= 2 * p.cus;
-  const dim3 grid = row_grid(row_tiles(slots, p.cols, tall ? 8 : 1)), block(kRowThreads);
-  if (p.y_scale) {
-    if (tall && slots * p.cols >= kPastCaches)
-      hipLaunchKernelGGL((gather_kernel<T, 8, true, true>), grid, block, 0, stream, p);
-    else if (tall)
-      hipLaunchKernelGGL((gather_kernel<T, 8, true, false>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((gather_kernel<T, 1, true, false>), grid, block, 0, stream, p);
-  } else {
-    if (tall)
-      hipLaunchKernelGGL((gather_kernel<T, 8, false, false>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((gather_kernel<T, 1, false, false>), grid, block, 0, stream, p);
-  }
+  const int64_t slots = p.tokens * p.topk, groups = (p.cols + 127) / 128, tall = (slots + 127) / 128 * groups;
+  const dim3 block(kRowThreads);
+  if (tall >= 4 * p.cus && (QUANT || slots * p.cols * size_of(T) >= kPastCaches))
+    hipLaunchKernelGGL((gather_kernel<T, 8, QUANT, true>), row_grid(tall), block, 0, stream, p);
+  else if (!QUANT && tall >= 4 * p.cus)
+    hipLaunchKernelGGL((gather_kernel<T, 8, false, false>), row_grid(tall), block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((gather_kernel<T, 1, QUANT, false>), row_grid((slots + 15) / 16 * groups), block, 0, stream, p);
+}
+template <int T>
+void gather_out(const GatherParams& p, hipStream_t stream) {
+  p.y_scale ? gather_typed<T, true>(p, stream) : gather_typed<T, false>(p, stream);
 }
 
 template <int T>
@@ -461,7 +464,7 @@ hipError_t launch_sort(const SortParams& p, hipStream_t stream) {
     return hipGetLastError();       \
   } while (0)
 
-hipError_t launch_gather(const GatherParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, gather_typed); }
+hipError_t launch_gather(const GatherParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, gather_out); }
 hipError_t launch_combine(const CombineParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_typed); }
 hipError_t launch_combine_grad(const CombineGradParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_grad_typed); }
 
