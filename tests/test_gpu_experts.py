@@ -79,7 +79,8 @@ def test_sort_when_slots_agree(tokens, what):
         assert np.array_equal(got.cpu(), ref)
 
 
-SHAPES = [(1, 1, 1, 1), (1, 8, 16, 130), (5, 2, 3, 127), (33, 3, 4, 512), (64, 8, 64, 1000), (700, 6, 9, 520), (3000, 2, 8, 640)]
+SHAPES = [(1, 1, 1, 1), (1, 8, 16, 130), (5, 2, 3, 127), (33, 3, 4, 512), (64, 8, 64, 1000), (700, 6, 9, 520), (3000, 2, 8, 640),
+          (9000, 2, 8, 1300)]
 
 
 @pytest.mark.parametrize("tokens,topk,experts,cols", SHAPES)
@@ -214,3 +215,40 @@ def test_rows_past_four_gib():
     pg.pmoe_combine_run(config(), Y, place, Z, tokens, topk, cols, weights=torch.full((tokens, topk), 0.5, device="cuda:0"))
     sync()
     assert torch.equal(Y[:, ::4093], X[order.long() // topk][:, ::4093]) and torch.equal(Z, X)
+
+
+def test_rows_past_the_caches():
+    """Rows of more than 128 MiB, which are loaded and stored past the caches."""
+    tokens, topk, cols = 2100, 8, 4096
+    slots = tokens * topk
+    note("combine past the caches")
+    g = torch.Generator(device="cuda:0").manual_seed(2)
+    ids = torch.randint(-1, 16, (tokens, topk), generator=g, device="cuda:0", dtype=torch.int32)
+    place, order, offsets = run_sort(ids, 16)
+    X = torch.randn((slots, cols), generator=g, device="cuda:0").bfloat16()
+    dY = torch.randn((tokens, cols), generator=g, device="cuda:0").bfloat16()
+    w = torch.rand((tokens, topk), generator=g, device="cuda:0")
+    Y, dX, dW = torch.empty_like(dY), torch.zeros_like(X), torch.empty_like(w)
+    Q, S = torch.zeros((slots, cols), dtype=torch.uint8, device="cuda:0"), torch.zeros(cols // 128 * slots, dtype=torch.uint8, device="cuda:0")
+    Q2, S2 = torch.zeros_like(Q), torch.zeros_like(S)
+    pg.pmoe_combine_run(config(), X, place, Y, tokens, topk, cols, weights=w, R=dY)
+    pg.pmoe_combine_grad_run(config(), dY, X, place, order, dX, tokens, topk, cols, weights=w, dW=dW)
+    pg.pmoe_combine_grad_run(config(), dY, None, place, order, Q, tokens, topk, cols, weights=w, out="fp8_b128", dx_scale=S)
+    sync()
+    on, slot = order >= 0, order.clamp(min=0).long()
+    prod = dY.float()[slot // topk] * w.view(-1)[slot][:, None]
+    assert torch.equal(dX, (prod * on[:, None]).bfloat16())
+    pg.pfp8_quant_run(config(), prod, Q2, S2, slots, cols)
+    sync()
+    n = int(offsets[-1])
+    assert torch.equal(Q[:n], Q2[:n]) and torch.equal(S.view(-1, slots)[:, :n], S2.view(-1, slots)[:, :n])
+    for lo in range(0, tokens, 300):
+        p = place[lo:lo + 300].long()
+        rows = X[p.clamp(min=0)].double() * (p >= 0)[..., None]
+        ref = (rows * w[lo:lo + 300].double()[..., None]).sum(1) + dY[lo:lo + 300].double()
+        mag = (rows.abs() * w[lo:lo + 300].double()[..., None]).sum(1) + dY[lo:lo + 300].double().abs()
+        bound = (topk + 1) * U * mag
+        assert bool(((Y[lo:lo + 300].double() - ref).abs() <= bound + (ref.abs() + bound) * 2.0 ** -8).all())
+        ref = (rows * dY[lo:lo + 300, None].double()).sum(-1)
+        mag = (rows * dY[lo:lo + 300, None].double()).abs().sum(-1)
+        assert bool(((dW[lo:lo + 300].double() - ref).abs() <= (cols + 1) * U * mag).all())

@@ -51,7 +51,7 @@ def u8(n):
     return torch.full((n,), 0x55, dtype=torch.uint8, device="cuda:0")
 
 
-SHAPES = [(1, 1), (1, 128), (3, 130), (40, 512), (67, 1000), (300, 2056), (2100, 1025)]
+SHAPES = [(1, 1), (1, 128), (3, 130), (40, 512), (67, 1000), (300, 2056), (2100, 1025), (3001, 1600)]
 
 
 def inputs(rows, cols, x, seed):
@@ -88,13 +88,15 @@ def test_glu(rows, cols, x, out, kept):
         assert np.array_equal(kw["kept_scale"].cpu().numpy().reshape(-1, rows), np.concatenate([sg, su]))
 
 
-@pytest.mark.parametrize("rows,cols", SHAPES + [(33, 640), (1500, 1024)])
+GRAD = [(s, out) for s in SHAPES + [(33, 640), (1500, 1024), (4100, 768)] for out in ("same", "fp8_b128")
+        if out == "same" or s[1] % 128 == 0]
+
+
+@pytest.mark.parametrize("shape,out", GRAD)
 @pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("out", ["same", "fp8_b128"])
 @pytest.mark.parametrize("kept", [True, False])
-def test_glu_grad(rows, cols, x, out, kept):
-    if out == "fp8_b128" and cols % 128:
-        pytest.skip("refused: a test of its own")
+def test_glu_grad(shape, x, out, kept):
+    rows, cols = shape
     note(f"glu_grad {rows} {cols} {x} {out} {kept}")
     X = inputs(rows, cols, x, rows)
     dY = torch.from_numpy(np.random.default_rng(7).standard_normal((rows, cols + 1))).to("cuda:0", TYPES[x])[:, :cols]
@@ -153,3 +155,29 @@ def test_infinities_and_nan_stay_in_their_block():
     assert bad.nonzero().tolist() == [[0, 2], [1, 1]]
     bad = KS.view(6, rows).cpu() == 255
     assert bad.nonzero().tolist() == [[1, 1], [3, 2]]
+
+
+def test_many_rows_equal_few():
+    """Inputs past the size that is loaded through the caches: the bits of calls on
+    1000 rows each."""
+    rows, cols = 8200, 8192
+    note("glu past the caches")
+    g = torch.Generator(device="cuda:0").manual_seed(1)
+    X = torch.randn((rows, 2 * cols), generator=g, device="cuda:0").bfloat16()
+    dY = torch.randn((rows, cols), generator=g, device="cuda:0").bfloat16()
+
+    def run(x, dy):
+        n = len(x)
+        out = [u8(n * cols), u8(cols // 128 * n), u8(n * 2 * cols), u8(2 * cols // 128 * n), u8(n * 2 * cols),
+               u8(2 * cols // 128 * n), torch.empty((n, 2 * cols), dtype=torch.bfloat16, device="cuda:0")]
+        pg.pglu_run(config(), x, out[0], n, cols, out="fp8_b128", y_scale=out[1], kept=out[2], kept_scale=out[3])
+        pg.pglu_grad_run(config(), dy, out[2], out[4], n, cols, x_scale=out[3], out="fp8_b128", dx_scale=out[5])
+        pg.pglu_grad_run(config(), dy, x, out[6], n, cols)
+        return [t.view(n, -1) if i % 2 == 0 else t.view(-1, n).t() for i, t in enumerate(out)]
+    many = run(X, dY)
+    sync()
+    for lo in range(0, rows, 1000):
+        few = run(X[lo:lo + 1000], dY[lo:lo + 1000])
+        sync()
+        for a, b in zip(many, few):
+            assert torch.equal(a[lo:lo + 1000], b)

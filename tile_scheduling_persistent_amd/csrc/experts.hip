@@ -296,8 +296,11 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
 
 // A wave takes 512 columns of a token: up to eight of its slots' rows at a time
 // are on their way together, summed in fp32 in the slots' order.
+// NT: rows and result past the caches, where the rows fill most of the Infinity Cache
+// (us, with a norm of the result: 8192 x 8 x 4096 bf16 162 -> 139, alone 130 -> 108;
+// 2048 tokens 43.2 -> 40.2; 1024 tokens, whose rows may still be there, 22.2 -> 25.0).
 constexpr int kSlotsAtOnce = 8;
-template <int T, int YT>
+template <int T, int YT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t slots = p.tokens * p.topk, ctiles = (p.cols + kRowCols - 1) / kRowCols;
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
         const int row = j0 + j < p.topk ? p.place[s] : -1;
         const bool on = row >= 0 && row < slots;
         w[j] = on ? (p.weights ? p.weights[s] : 1.0f) : 0.0f;
-        v[j] = vec8_load<T>(static_cast<const char*>(p.X) + (on ? row : 0) * p.ldx * size_of(T), c, on ? p.cols : 0);
+        v[j] = vec8_load<T, false, NT>(static_cast<const char*>(p.X) + (on ? row : 0) * p.ldx * size_of(T), c, on ? p.cols : 0);
       }
 #pragma unroll
       for (int j = 0; j < kSlotsAtOnce; ++j)
@@ -328,13 +331,15 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] += vec8_get(res, e);
     }
-    vec8_store<YT>(static_cast<char*>(p.Y) + t * p.ldy * size_of(YT), c, p.cols, vec8_pack<YT>(y));
+    vec8_store<YT, false, NT>(static_cast<char*>(p.Y) + t * p.ldy * size_of(YT), c, p.cols, vec8_pack<YT>(y));
   }
 }
 
 // A wave takes RW rows, all of their columns: dx = w dy, and the dot product of
-// dy with the row for dw.
-template <int T, int RW, bool QUANT>
+// dy with the row for dw.  NT: rows in and out past the caches, which leaves those to dy
+// that is read for each slot (us: 8192 x 8 x 4096 to e4m3 215 -> 208, 5000 x 2 x 7000 46.8
+// -> 43.0; rows that fit in the Infinity Cache, 512 x 8 x 4096, 15.3 -> 17.0).
+template <int T, int RW, bool QUANT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradParams p) {
   constexpr int ROWS = 4 * RW;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradPa
         const int64_t token = slot[r] >= 0 ? (unsigned)slot[r] / (unsigned)p.topk : 0;
         const int64_t n = slot[r] >= 0 ? p.cols : 0;
         d[r] = vec8_load<T>(static_cast<const char*>(p.dY) + token * p.ldy * size_of(T), c, n);
-        if (p.dW) x[r] = vec8_load<T>(static_cast<const char*>(p.X) + (slot[r] >= 0 ? row0 + r : 0) * p.ldx * size_of(T), c, n);
+        if (p.dW) x[r] = vec8_load<T, false, NT>(static_cast<const char*>(p.X) + (slot[r] >= 0 ? row0 + r : 0) * p.ldx * size_of(T), c, n);
       }
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
@@ -377,11 +382,15 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradPa
           unsigned byte;
           const u32x2_d o = e4m3_codes(y, byte);
           if (slot[r] >= 0 && c < kp) {
-            *reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.dX) + (row0 + r) * kp + c) = o;
+            u32x2_d* q = reinterpret_cast<u32x2_d*>(static_cast<uint8_t*>(p.dX) + (row0 + r) * kp + c);
+            if constexpr (NT)
+              __builtin_nontemporal_store(o, q);
+            else
+              *q = o;
             if ((lane & 15) == 0) p.dx_scale[(c >> 7) * slots + row0 + r] = (uint8_t)byte;
           }
         } else if (slot[r] >= 0) {
-          vec8_store<T>(static_cast<char*>(p.dX) + (row0 + r) * p.lddx * size_of(T), c, p.cols, vec8_pack<T>(y));
+          vec8_store<T, false, NT>(static_cast<char*>(p.dX) + (row0 + r) * p.lddx * size_of(T), c, p.cols, vec8_pack<T>(y));
         }
       }
     }
@@ -420,31 +429,33 @@ void gather_out(const GatherParams& p, hipStream_t stream) {
   p.y_scale ? gather_typed<T, true>(p, stream) : gather_typed<T, false>(p, stream);
 }
 
-template <int T>
+template <int T, int YT>
 void combine_typed(const CombineParams& p, hipStream_t stream) {
   const dim3 grid = row_grid((p.tokens * ((p.cols + kRowCols - 1) / kRowCols) + 3) / 4), block(kRowThreads);
-  if (p.y_type == T)
-    hipLaunchKernelGGL((combine_kernel<T, T>), grid, block, 0, stream, p);
+  if (p.tokens * p.topk * p.cols * size_of(T) >= kPastCaches)
+    hipLaunchKernelGGL((combine_kernel<T, YT, true>), grid, block, 0, stream, p);
   else
-    hipLaunchKernelGGL((combine_kernel<T, kTypeF32>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((combine_kernel<T, YT, false>), grid, block, 0, stream, p);
+}
+template <int T>
+void combine_out(const CombineParams& p, hipStream_t stream) {
+  p.y_type == T ? combine_typed<T, T>(p, stream) : combine_typed<T, kTypeF32>(p, stream);
 }
 
-template <int T>
+template <int T, bool QUANT>
 void combine_grad_typed(const CombineGradParams& p, hipStream_t stream) {
   const int64_t slots = p.tokens * p.topk;
-  const bool tall = (slots + 15) / 16 >= 2 * p.cus;
-  const dim3 grid = row_grid(tall ? (slots + 15) / 16 : (slots + 3) / 4), block(kRowThreads);
-  if (p.dx_scale) {
-    if (tall)
-      hipLaunchKernelGGL((combine_grad_kernel<T, 4, true>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((combine_grad_kernel<T, 1, true>), grid, block, 0, stream, p);
-  } else {
-    if (tall)
-      hipLaunchKernelGGL((combine_grad_kernel<T, 4, false>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((combine_grad_kernel<T, 1, false>), grid, block, 0, stream, p);
-  }
+  const dim3 block(kRowThreads);
+  if ((slots + 15) / 16 < 2 * p.cus)
+    hipLaunchKernelGGL((combine_grad_kernel<T, 1, QUANT, false>), row_grid((slots + 3) / 4), block, 0, stream, p);
+  else if (slots * p.cols * size_of(T) < kPastCaches)
+    hipLaunchKernelGGL((combine_grad_kernel<T, 4, QUANT, false>), row_grid((slots + 15) / 16), block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((combine_grad_kernel<T, 4, QUANT, true>), row_grid((slots + 15) / 16), block, 0, stream, p);
+}
+template <int T>
+void combine_grad_out(const CombineGradParams& p, hipStream_t stream) {
+  p.dx_scale ? combine_grad_typed<T, true>(p, stream) : combine_grad_typed<T, false>(p, stream);
 }
 
 }  // namespace
@@ -465,7 +476,7 @@ hipError_t launch_sort(const SortParams& p, hipStream_t stream) {
   } while (0)
 
 hipError_t launch_gather(const GatherParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, gather_out); }
-hipError_t launch_combine(const CombineParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_typed); }
-hipError_t launch_combine_grad(const CombineGradParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_grad_typed); }
+hipError_t launch_combine(const CombineParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_out); }
+hipError_t launch_combine_grad(const CombineGradParams& p, hipStream_t stream) { PGK_BY_TYPE(p.type, combine_grad_out); }
 
 }  // namespace pgk

