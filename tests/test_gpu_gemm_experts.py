@@ -62,7 +62,7 @@ def check(C, offsets, ref, terms, k, dtype):
 # rows per expert from none to many: every kernel and tile
 SHAPES = [(1, 128, 128, 1), (24, 300, 1280, 1), (50, 1100, 384, 20), (60, 4100, 256, 6), (1, 70, 256, 5), (8, 256, 384, 64), (17, 129, 128, 2), (40, 1000, 640, 3), (64, 513, 1024, 1),
           (130, 300, 1152, 4), (200, 256, 2048, 6), (700, 300, 512, 3), (1100, 777, 256, 2), (2000, 512, 384, 9),
-          (3000, 1030, 128, 5), (5000, 4200, 256, 3), (4000, 3000, 128, 20)]
+          (3000, 1030, 128, 5), (5000, 4200, 256, 3), (4000, 3000, 128, 20), (2000, 150, 128, 1024), (13000, 130, 128, 1000)]
 
 
 @pytest.mark.parametrize("rows,n,k,experts", SHAPES)
@@ -118,15 +118,16 @@ def test_offsets_outside_the_rows(rows):
     assert np.allclose(host(C)[rows // 3:], ref, rtol=1e-5, atol=1e-5 * np.abs(ref).max())
 
 
-@pytest.mark.parametrize("rows", [20, 500])
-def test_nan_codes_and_scales_stay_in_their_rows(rows):
+@pytest.mark.parametrize("rows", [20, 300, 1200])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_nan_codes_and_scales_stay_in_their_rows(rows, out):
     rng = np.random.default_rng(8)
     n, k = 260, 384
     qa, sa, qb, sb = operands(rng, rows, n, k, 2)
     qa[3, 200], sa[1, 7] = 0x7f, 255
     sb[1, 1, 0] = 255  # expert 1's columns 128 .. 255
     offsets = np.array([0, rows - 6, rows], np.int32)
-    C = torch.empty((rows, n), device="cuda:0")
+    C = torch.empty((rows, n), dtype=TYPES[out], device="cuda:0")
     pg.pgemm_run_experts(config(), gpu(qa), gpu(qb), C, rows, n, k, gpu(sa), gpu(sb), experts=2, offsets=gpu(offsets))
     sync()
     want = np.zeros((rows, n), bool)
@@ -137,7 +138,7 @@ def test_nan_codes_and_scales_stay_in_their_rows(rows):
 
 WGRAD = [(1, 1, 1, 1), (5, 130, 100, 3), (64, 128, 128, 1), (100, 260, 390, 4), (300, 72, 513, 2), (700, 256, 256, 5),
          (2000, 520, 260, 3), (1000, 640, 1100, 2),
-         (1500, 1032, 1100, 14), (600, 64, 130, 300)]
+         (1500, 1032, 1100, 14), (600, 64, 130, 300), (40, 130, 8, 1024)]
 
 
 @pytest.mark.parametrize("rows,n,k,experts", WGRAD)

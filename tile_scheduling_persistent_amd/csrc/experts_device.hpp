@@ -23,25 +23,25 @@ __device__ __forceinline__ ExpertRows expert_rows(const int* offsets, int e, int
 // By the whole workgroup; ends with a barrier.
 __device__ __forceinline__ void expert_tiles(const int* offsets, int experts, int rows, int bm, int per, int* s_lo,
                                              int* s_n, int* s_tile) {
+  for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+    const ExpertRows r = expert_rows(offsets, e, rows);
+    s_lo[e] = r.lo;
+    s_n[e] = r.n;
+  }
+  __syncthreads();
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
     int before = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
       const int e = e0 + lane;
-      ExpertRows r = {0, 0};
-      if (e < experts) r = expert_rows(offsets, e, rows);
-      const int t = (r.n + bm - 1) / bm * per;
+      const int t = e < experts ? (s_n[e] + bm - 1) / bm * per : 0;
       int x = t;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const int y = __shfl_up(x, d);
         if (lane >= d) x += y;
       }
-      if (e < experts) {
-        s_lo[e] = r.lo;
-        s_n[e] = r.n;
-        s_tile[e] = before + x - t;
-      }
+      if (e < experts) s_tile[e] = before + x - t;
       before += __shfl(x, 63);
     }
     if (lane == 0) s_tile[experts] = before;
@@ -49,9 +49,17 @@ __device__ __forceinline__ void expert_tiles(const int* offsets, int experts, in
   __syncthreads();
 }
 
-// The expert of tile t, at or after expert e.
+// The expert of tile t, at or after expert e: the last one whose tiles start at or
+// before t (experts without rows start where the next one does).
 __device__ __forceinline__ int expert_of_tile(const int* s_tile, int experts, int t, int e) {
-  while (e + 1 < experts && t >= s_tile[e + 1]) ++e;
+  int end = experts;
+  while (end - e > 1) {
+    const int mid = (e + end) >> 1;
+    if (s_tile[mid] <= t)
+      e = mid;
+    else
+      end = mid;
+  }
   return e;
 }
 
