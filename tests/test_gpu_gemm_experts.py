@@ -138,7 +138,8 @@ def test_nan_codes_and_scales_stay_in_their_rows(rows, out):
 
 WGRAD = [(1, 1, 1, 1), (5, 130, 100, 3), (64, 128, 128, 1), (100, 260, 390, 4), (300, 72, 513, 2), (700, 256, 256, 5),
          (2000, 520, 260, 3), (1000, 640, 1100, 2),
-         (1500, 1032, 1100, 14), (600, 64, 130, 300), (40, 130, 8, 1024)]
+         (1500, 1032, 1100, 14), (600, 64, 130, 300), (40, 130, 8, 1024),
+         (4600, 2064, 2050, 4), (3300, 130, 260, 1)]  # several stretches of 512 rows, on both tiles
 
 
 @pytest.mark.parametrize("rows,n,k,experts", WGRAD)

@@ -8,6 +8,12 @@
 // power of two), and v_mfma_f32_16x16x32_bf16 sums in fp32.  Both operands lie in
 // LDS as they do in memory, rows r of columns, and are read transposed
 // (ds_read_b64_tr_b16).
+//
+// Measured: 8192^3 811 us (1.36 PFLOP/s; a library product of bf16 reaches 1.41), 32768
+// rows of 16 experts x 4096 x 2048 530 us, with e4m3 D 504; 5000 rows of 8 x 1000 x 1408
+// with a base 43.  Bound by the matrix cores together with LDS, which takes 512 cycles of
+// writes and 1024 of reads for a slab's 2048 of MFMAs: without the conversions the time
+// stays, without the LDS writes it falls by 5 to 10%, without the loads by 11 to 19%.
 #include <atomic>
 #include <type_traits>
 #include <utility>
@@ -33,6 +39,7 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 constexpr int kThreads = 256;
 constexpr int BR = 64;  // rows per slab: two steps of 32
 constexpr int kRanked = 256;  // up to so many experts are taken in the order of their rows
+constexpr int kScaleSlabs = 8, kScaleRows = kScaleSlabs * BR;  // a stretch of rows whose scales are fetched together
 
 template <class F, int... I>
 __device__ __forceinline__ void static_for_of(F&& f, std::integer_sequence<int, I...>) {
@@ -52,6 +59,13 @@ __device__ __forceinline__ void mfma16(f32x4& acc, bf16x8 a, bf16x8 b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 
+// Zeros that are in their registers from here on: left to itself the compiler copied
+// one set of them to each block right before its first MFMA.
+__device__ __forceinline__ void zero_acc(f32x4& acc) {
+  acc = f32x4{0, 0, 0, 0};
+  asm volatile("" : "+a"(acc));
+}
+
 // Between the writes that zero the accumulators and the first MFMA that reads them.
 __device__ __forceinline__ void acc_written() {
   __builtin_amdgcn_sched_barrier(0);
@@ -68,27 +82,6 @@ __device__ __forceinline__ int swz(int r, int c) {
   return c ^ (4 * (r & 3)) ^ (2 * ((r >> 3) & 1)) ^ (((c >> 4) ^ r) & 1);
 }
 
-// Sixteen e4m3 codes times 2^(byte - 127), as bf16.
-__device__ __forceinline__ void codes_bf16(u32x4 q, unsigned byte, u32x4& lo, u32x4& hi) {
-  const float sc = scale_value(byte);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned w = i == 0 ? q[0] : i == 1 ? q[1] : i == 2 ? q[2] : q[3];
-    const unsigned a = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, sc, false));
-    const unsigned b = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, sc, true));
-    if (i < 2) {
-      lo[2 * i] = a;
-      lo[2 * i + 1] = b;
-    } else {
-      hi[2 * (i - 2)] = a;
-      hi[2 * (i - 2) + 1] = b;
-    }
-  }
-}
-
-// An operand's slab on its way through registers: BR rows of W columns, in parts of
-// 16 bytes per thread (16 codes, or 8 elements of bf16).  Loads go through buffer
-// resources that end with the slab's last row: rows past it read as zeros.
 // How an operand lies in memory: bf16 whose rows start on 16 bytes, bf16 of any
 // alignment, or e4m3.
 constexpr int kWide = 0, kNarrow = 1, kCodes = 2;
@@ -99,37 +92,53 @@ struct Slab {
   static constexpr int STEP = kThreads * COLS / W;   // rows from one part to the next
   static constexpr int PARTS = BR / STEP;
   static constexpr int ESZ = FP8 ? 1 : 2;
+  static constexpr int GROUPS = W / 128;
+  // floats: the scales of two stretches of rows, the one in use and the next
+  static constexpr int SCALES = FP8 ? 2 * GROUPS * kScaleRows : 0;
+  static constexpr int FETCH = GROUPS * kScaleRows / kThreads;  // scale bytes per thread and stretch
   u32x4 q[PARTS];
-  unsigned byte[FP8 ? PARTS : 1];
-  unsigned off, soff;  // of part 0, in bytes
-  unsigned wr[2];      // LDS: FP8 its two chunks, else of even and odd parts
-  unsigned row;        // of part 0
-  unsigned long long x, s;  // the slab and its scales, and their ranges
-  unsigned xr, sr;
-  __device__ __forceinline__ void init(unsigned ld, unsigned sld) {
-    const int c = (int)threadIdx.x % (W / COLS) * COLS;
-    row = threadIdx.x / (W / COLS);
-    off = row * ld * ESZ + c * ESZ;
-    soff = (unsigned)(c >> 7) * sld + row;
-    const int r = (int)row, k = c >> 3;
+  float sc[FP8 ? PARTS : 1];           // scales of the parts in q
+  unsigned char fetched[FP8 ? FETCH : 1];
+  float* scales;                       // LDS [2][GROUPS][kScaleRows]
+  unsigned sc_at;                      // of part 0 of a slab, in floats
+  unsigned off;                        // of part 0, in bytes
+  unsigned wr[2];                      // LDS: FP8 its two chunks, else of even and odd parts
+  unsigned long long x;                // the slab and its range
+  unsigned xr;
+  __device__ __forceinline__ void init(unsigned ld, float* lds) {
+    const int c = (int)threadIdx.x % (W / COLS) * COLS, r = (int)threadIdx.x / (W / COLS), k = c >> 3;
+    off = (unsigned)r * ld * ESZ + c * ESZ;
+    scales = lds;
+    sc_at = (unsigned)((c >> 7) * kScaleRows + r);
     wr[0] = (unsigned)(r * W * 2 + swz(r, k) * 16);
     wr[1] = FP8 ? (unsigned)(r * W * 2 + swz(r, k + 1) * 16) : (unsigned)((r + STEP) * W * 2 + swz(r + STEP, k) * 16);
   }
   // The slab from row r on, columns c0 .. of `cols`; left: rows from there to the
   // last (none: nothing is read).
-  __device__ __forceinline__ void aim(int64_t r, int left, const void* mat, const uint8_t* scale, int64_t ld,
-                                      int64_t sld, int c0, int cols) {
+  __device__ __forceinline__ void aim(int64_t r, int left, const void* mat, int64_t ld, int c0, int cols) {
     const int rows = left < BR ? left : BR;
     x = reinterpret_cast<unsigned long long>(mat) + (unsigned long long)(r * ld + c0) * ESZ;
     // up to the last column of the last row
     xr = rows > 0 ? ((unsigned)(rows - 1) * (unsigned)ld + (unsigned)(cols - c0)) * ESZ : 0u;
-    if (FP8) {
-      s = reinterpret_cast<unsigned long long>(scale) + (unsigned long long)((int64_t)(c0 >> 7) * sld + r);
-      const int groups = (cols - c0) / 128 < W / 128 ? (cols - c0) / 128 : W / 128;
-      sr = rows > 0 ? (unsigned)(groups - 1) * (unsigned)sld + (unsigned)rows : 0u;
+  }
+  // Scale bytes of the stretch of rows r .. (left of them, the others zero) and groups
+  // g0 .. of `groups`, and what they stand for into half `half`.
+  __device__ __forceinline__ void fetch(const uint8_t* scale, int64_t sld, int64_t r, int left, int g0, int groups) {
+    if (!FP8) return;
+#pragma unroll
+    for (int i = 0; i < FETCH; ++i) {
+      const int at = i * kThreads + (int)threadIdx.x, row = at % kScaleRows, g = at / kScaleRows;
+      fetched[FP8 ? i : 0] = row < left && g0 + g < groups ? scale[(int64_t)(g0 + g) * sld + r + row] : 0;
     }
   }
-  __device__ __forceinline__ void load(int i, unsigned ld) {
+  __device__ __forceinline__ void keep(int half) {
+    if (!FP8) return;
+#pragma unroll
+    for (int i = 0; i < FETCH; ++i)
+      scales[half * GROUPS * kScaleRows + i * kThreads + (int)threadIdx.x] = scale_value(fetched[FP8 ? i : 0]);
+  }
+  // Part i of the slab aimed at, slab number s of the tile.
+  __device__ __forceinline__ void load(int i, unsigned ld, int s) {
     const auto rX = rsrc(reinterpret_cast<const void*>(x), xr);
     // in the vector offset: the range check leaves a scalar one out
     const unsigned at = off + (unsigned)(i * STEP) * ld * ESZ;
@@ -143,18 +152,34 @@ struct Slab {
       }
     }
     if (FP8)
-      byte[i] = __builtin_amdgcn_raw_buffer_load_b8(rsrc(reinterpret_cast<const void*>(s), sr), soff + i * STEP, 0, 0);
+      sc[FP8 ? i : 0] = scales[(s / kScaleSlabs & 1) * GROUPS * kScaleRows + s % kScaleSlabs * BR + sc_at + i * STEP];
   }
-  // Part i into the stage at s; left: rows of the slab.  Another row's scale may stand
-  // behind the slab's last one.
-  __device__ __forceinline__ void put(int i, unsigned char* st, int left) const {
-    if (FP8) {
-      u32x4 lo, hi;
-      codes_bf16(q[i], (int)row + i * STEP < left ? byte[FP8 ? i : 0] : 0u, lo, hi);
-      *reinterpret_cast<u32x4*>(st + wr[0] + i * STEP * W * 2) = lo;
-      *reinterpret_cast<u32x4*>(st + wr[1] + i * STEP * W * 2) = hi;
+  // What becomes of part i, as operations of an instruction or two each, which the main
+  // loop spreads over its MFMAs.  Codes: eight times two values by their scale, which is exact in bf16;
+  // two writes of eight values; the next slab's load.  bf16: the write and the load.  ld:
+  // of the matrix, in elements; s: the next slab's number.
+  static constexpr int OPS = FP8 ? 11 : 2;  // per part
+  u32x4 lo, hi;                             // the part under conversion
+  template <int OP>
+  __device__ __forceinline__ void run(unsigned char* st, unsigned ld, int s) {
+    constexpr int i = OP / OPS, o = OP % OPS;
+    if constexpr (!FP8) {
+      if constexpr (o == 0)
+        *reinterpret_cast<u32x4*>(st + wr[i & 1] + (i & ~1) * STEP * W * 2) = q[i];
+      else
+        load(i, ld, s);
+    } else if constexpr (o < 8) {
+      const unsigned w = q[i][o >> 1];
+      const unsigned v =
+          __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, sc[i], (o & 1) != 0));
+      if constexpr (o < 4)
+        lo[o] = v;
+      else
+        hi[o - 4] = v;
+    } else if constexpr (o < 10) {
+      *reinterpret_cast<u32x4*>(st + wr[o - 8] + i * STEP * W * 2) = o == 8 ? lo : hi;
     } else {
-      *reinterpret_cast<u32x4*>(st + wr[i & 1] + (i & ~1) * STEP * W * 2) = q[i];
+      load(i, ld, s);
     }
   }
 };
@@ -163,9 +188,11 @@ struct Slab {
 //
 // Slabs go from memory to registers, are multiplied by their scales there and
 // written to one of two LDS stages while the matrix cores work on the other; a part's
-// next load goes out as soon as it is written.  One barrier per slab, between its
-// two steps: behind it the second step's fragments are in registers already and the
-// next slab's first are read.
+// next load goes out as soon as it is written, a whole period before it is needed.  One
+// barrier per slab, between its two steps: behind it the second step's fragments are in
+// registers already and the next slab's first are read.  Scales come by stretches of 512
+// rows, a byte or two per thread, and lie in LDS as floats: a byte load beside every
+// part's own cost as much as the conversions and the LDS writes (8192^3 863 us, so 811).
 //
 // A workgroup takes one tile: a tile's time goes with its expert's rows, which only
 // the device knows, and the hardware hands the next workgroup to the next free CU.
@@ -173,7 +200,7 @@ template <int BN, int BK, int DFORM, bool F32>
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   constexpr int TN = BN / 2, TK = BK / 2, SN = TN / 16, SK = TK / 16, NMF = SN * SK;
   constexpr int D_BYTES = BR * BN * 2, STAGE = D_BYTES + BR * BK * 2;
-  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];  // [2][STAGE]
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];  // [2][STAGE], D's scales, A's
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave >> 1, wk = wave & 1;
@@ -213,31 +240,40 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   Slab<BK, kCodes> a;
   constexpr int PD = Slab<BN, DFORM>::PARTS, PA = Slab<BK, kCodes>::PARTS, NP = PD + PA;
   const unsigned ldd = (unsigned)p.ldd;
-  d.init(ldd, (unsigned)p.rows);
-  a.init((unsigned)kp, (unsigned)p.rows);
-  // loads: the slab that they are at starts at row r0; `left`: rows from the start of
-  // the slab that the registers hold
-  int r0 = 0, left = 0;
+  float* const s_scales = reinterpret_cast<float*>(smem + 2 * STAGE);
+  d.init(ldd, s_scales);
+  a.init((unsigned)kp, s_scales + Slab<BN, DFORM>::SCALES);
+  // The loads are at slab number `at`.
+  int at = 0;
   auto load = [&](int i) PGK_INLINE {
     if (i < PD)
-      d.load(i, ldd);
+      d.load(i, ldd, at);
     else
-      a.load(i - PD, (unsigned)kp);
-  };
-  auto put = [&](int i, unsigned char* s) PGK_INLINE {
-    if (i < PD)
-      d.put(i, s, left);
-    else
-      a.put(i - PD, s + D_BYTES, left);
+      a.load(i - PD, (unsigned)kp, at);
   };
   auto aim = [&]() {
-    d.aim(lo + r0, n_rows - r0, p.D, p.sd, p.ldd, p.rows, n0, DFORM == kCodes ? np : p.N);
-    a.aim(lo + r0, n_rows - r0, p.A, p.sa, kp, p.rows, k0, kp);
+    const int r0 = at * BR;
+    d.aim(lo + r0, n_rows - r0, p.D, p.ldd, n0, DFORM == kCodes ? np : p.N);
+    a.aim(lo + r0, n_rows - r0, p.A, kp, k0, kp);
   };
-  auto advance = [&]() {
-    left = n_rows - r0;
-    r0 += BR;
-    aim();
+  auto fetch = [&](int stretch) {
+    const int r0 = stretch * kScaleRows;
+    d.fetch(p.sd, p.rows, lo + r0, n_rows - r0, n0 >> 7, np >> 7);
+    a.fetch(p.sa, p.rows, lo + r0, n_rows - r0, k0 >> 7, kp >> 7);
+  };
+  auto keep = [&](int stretch) {
+    d.keep(stretch & 1);
+    a.keep(stretch & 1);
+  };
+
+  // Operation o of the slab that the registers hold, into the stage at s.
+  constexpr int OD = PD * Slab<BN, DFORM>::OPS, OPS = OD + PA * Slab<BK, kCodes>::OPS;
+  auto run = [&](auto oc, unsigned char* s) PGK_INLINE {
+    constexpr int o = oc;
+    if constexpr (o < OD)
+      d.template run<o>(s, ldd, at);
+    else
+      a.template run<o - OD>(s + D_BYTES, (unsigned)kp, at);
   };
 
   // Fragments: lane i of a group of 16 points at row i / 4 (+ 8 per group), columns
@@ -341,50 +377,66 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
 #pragma unroll
   for (int i = 0; i < SN; ++i)
 #pragma unroll
-    for (int j = 0; j < SK; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < SK; ++j) zero_acc(acc[i][j]);
   acc_written();
+  // Step h of a slab on the matrix cores, among them the LDS reads of the next step (of
+  // the stage at `from`) and this half of a period's operations (into the stage at `to`).
+  // The second step comes first in a period.
+  auto step = [&](auto hc, const unsigned char* from, unsigned char* to, auto both) PGK_INLINE {
+    static_for<NMF>([&](auto jc) PGK_INLINE {
+      constexpr int h = hc, j = jc, at = both ? (1 - h) * NMF + j : j, all = both ? 2 * NMF : NMF;
+      mfma(hc, jc);
+      constexpr int r0 = (j * NR + NMF - 1) / NMF, r1 = ((j + 1) * NR + NMF - 1) / NMF;
+      static_for<r1 - r0>([&](auto rc) PGK_INLINE { read(from, std::integral_constant<int, 1 - h>{}, r0 + rc); });
+      constexpr int o0 = (at * OPS + all - 1) / all, o1 = ((at + 1) * OPS + all - 1) / all;
+      static_for<o1 - o0>([&](auto oc) PGK_INLINE { run(std::integral_constant<int, o0 + oc>{}, to); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  const std::integral_constant<bool, true> shared;
+  const std::integral_constant<bool, false> alone;
   if (n_rows > 0) {
+    unsigned char* const stage0 = smem;
+    unsigned char* const stage1 = smem + STAGE;
+    fetch(0);
+    keep(0);
+    fetch(1);
+    keep(1);
+    slab_barrier();
     aim();
 #pragma unroll
     for (int i = 0; i < NP; ++i) load(i);
-    advance();
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      put(i, smem);
-      load(i);
-    }
-    advance();
+    ++at;
+    aim();
+    static_for<OPS>([&](auto oc) PGK_INLINE { run(oc, stage0); });
+    ++at;
+    aim();
     slab_barrier();
 #pragma unroll
-    for (int i = 0; i < NR; ++i) read(smem, step0, i);
-    int turn = 0;
-    for (int s = 0; s < n_rows; s += BR, turn ^= 1) {
-      unsigned char* now = smem + turn * STAGE;
-      unsigned char* next = smem + (turn ^ 1) * STAGE;
-      static_for<NMF>([&](auto jc) PGK_INLINE {
-        mfma(step0, jc);
-        static_for<NR>([&](auto rc) PGK_INLINE {
-          if constexpr (rc * NMF / NR == jc) read(now, step1, rc);
-        });
-        static_for<NP>([&](auto ic) PGK_INLINE {
-          if constexpr (ic * NMF / NP == jc) {
-            put(ic, next);
-            load(ic);
-          }
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      advance();
+    for (int i = 0; i < NR; ++i) read(stage0, step0, i);
+    __builtin_amdgcn_sched_barrier(0);
+    step(step0, stage0, stage1, alone);
+    slab_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    // A period: the second step of slab s, then the first of slab s + 1, whose stage
+    // is complete; slab s + 2 goes where slab s was, which no wave reads any more, and
+    // slab s + 3, `at`, is loaded.  Where that is the second of a stretch, the scales of
+    // the stretch after take the place of those of the one before, which the slab before
+    // it was the last to read in another period.
+    for (int s = 0; (s + 1) * BR < n_rows; ++s) {
+      unsigned char* now = s & 1 ? stage1 : stage0;
+      unsigned char* next = s & 1 ? stage0 : stage1;
+      ++at;
+      aim();
+      const bool turn = at % kScaleSlabs == 1 && at > 1;
+      if (turn) fetch(at / kScaleSlabs + 1);
+      step(step1, next, now, shared);
+      step(step0, next, now, shared);
+      if (turn) keep(at / kScaleSlabs + 1);
       slab_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      static_for<NMF>([&](auto jc) PGK_INLINE {
-        mfma(step1, jc);
-        static_for<NR>([&](auto rc) PGK_INLINE {
-          if constexpr (rc * NMF / NR == jc) read(next, step0, rc);
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      });
     }
+    static_for<NMF>([&](auto jc) PGK_INLINE { mfma(step1, jc); });
   }
   mfma_results_ready();
   store();
@@ -411,7 +463,8 @@ struct Instance {
 };
 template <int BN, int BK, int DFORM, bool F32>
 Instance tiled() {
-  return {BN, BK, 2 * BR * (BN + BK) * 2, wgrad_kernel<BN, BK, DFORM, F32>};
+  return {BN, BK, 2 * BR * (BN + BK) * 2 + 4 * (Slab<BN, DFORM>::SCALES + Slab<BK, kCodes>::SCALES),
+          wgrad_kernel<BN, BK, DFORM, F32>};
 }
 
 }  // namespace
