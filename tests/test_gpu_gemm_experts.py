@@ -180,6 +180,31 @@ def test_wgrad(rows, n, k, experts, d, out, base, how):
     assert np.all(np.abs(host(dB) - ref) <= bound)
 
 
+@pytest.mark.parametrize("rows,n,k,experts", [(3, 5, 130, 1), (70, 131, 260, 3), (700, 2053, 2050, 4), (1300, 4095, 1030, 5)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("ldd", ["n to 8", "more"])
+def test_wgrad_rows_on_vectors(rows, n, k, experts, out, ldd):
+    """bf16 rows that start on 16 bytes and end inside a vector, on both tiles; the last
+    row ends where the memory that belongs to the matrix does."""
+    note(f"wgrad rows on vectors {rows} {n} {k} {experts} {out} {ldd}")
+    rng = np.random.default_rng(n)
+    ld = (n + 7) // 8 * 8 + (16 if ldd == "more" else 0)
+    offsets = split(rng, rows, experts, "all")
+    qa, sa = ox.quant_rows(rng.standard_normal((rows, k)) * np.exp2(rng.integers(-6, 7, (rows, 1))))
+    a = ox.dequant_rows(qa, sa)[:, :k]
+    D = gpu(rng.standard_normal((rows, ld)).astype(np.float32)).bfloat16()
+    D[:, n:] = float("nan")
+    D = D[:, :n]
+    ref, terms = ox.wgrad(host(D), a, offsets)
+    counts = (offsets[1:] - offsets[:-1])[:, None, None]
+    bound = (counts / 32 + 2) * 2.0 ** -22 * terms
+    dB = torch.full((experts, n, k), 3.0, dtype=TYPES[out], device="cuda:0")
+    pg.pgemm_run_experts_wgrad(config(), D, gpu(qa), dB, rows, n, k, gpu(sa), experts=experts, offsets=gpu(offsets))
+    sync()
+    bound = bound + (np.abs(ref) + bound) * torch.finfo(TYPES[out]).eps / 2
+    assert np.all(np.abs(host(dB) - ref) <= bound)
+
+
 def test_wgrad_without_rows():
     """No rows at all: zeros, or the base."""
     offsets = torch.zeros(4, dtype=torch.int32, device="cuda:0")

@@ -118,8 +118,9 @@ struct Slab {
   __device__ __forceinline__ void aim(int64_t r, int left, const void* mat, int64_t ld, int c0, int cols) {
     const int rows = left < BR ? left : BR;
     x = reinterpret_cast<unsigned long long>(mat) + (unsigned long long)(r * ld + c0) * ESZ;
-    // up to the last column of the last row
+    // up to the last column of the last row; what is loaded by words ends with a word
     xr = rows > 0 ? ((unsigned)(rows - 1) * (unsigned)ld + (unsigned)(cols - c0)) * ESZ : 0u;
+    if (FORM == kWide) xr = (xr + 3u) & ~3u;
   }
   // Scale bytes of the stretch of rows r .. (left of them, the others zero) and groups
   // g0 .. of `groups`, and what they stand for into half `half`.
