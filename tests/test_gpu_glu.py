@@ -144,6 +144,26 @@ def test_rows_behind_the_valid_ones_are_left(valid):
         assert bool((t.view(4, rows)[:, n:] == 0x55).all()) and bool((t.view(4, rows)[:, :n] != 0x55).all())
 
 
+@pytest.mark.parametrize("kept", [True, False])
+def test_gates_whose_exponential_is_past_fp32(kept):
+    """silu(g) is a normal number down to g = -91 or so, where exp(-g) is infinite."""
+    rows, cols = 3, 128
+    X = torch.ones((rows, 2 * cols), device="cuda:0")
+    X[:, :cols] = -torch.linspace(80, 104, rows * cols, device="cuda:0").reshape(rows, cols)
+    Y, dY, dX = torch.empty((rows, cols), device="cuda:0"), torch.ones((rows, cols), device="cuda:0"), torch.empty_like(X)
+    K, KS = u8(rows * 2 * cols), u8(2 * rows)
+    pg.pglu_run(config(), X, Y, rows, cols, kept=K, kept_scale=KS)
+    src, kw, used = (K, dict(x_scale=KS), host(X)) if kept else (X, {}, host(X))
+    if kept:
+        used = ox.dequant_rows(K.cpu().numpy().reshape(rows, -1), KS.cpu().numpy().reshape(2, rows))
+    pg.pglu_grad_run(config(), dY, src, dX, rows, cols, **kw)
+    sync()
+    want = ox.glu(host(X))
+    near(Y, want, 8 * U * np.abs(want) + 2.0 ** -126, torch.float32)
+    want, terms = ox.glu_grad(host(dY), used)
+    near(dX, want, 16 * U * terms + 2.0 ** -126, torch.float32)
+
+
 def test_infinities_and_nan_stay_in_their_block():
     rows, cols = 4, 384
     X = inputs(rows, cols, "f32", 4)

@@ -14,8 +14,12 @@
 namespace pgk {
 namespace {
 
-// 1 / (1 + exp(-g)): exp past fp32's range gives infinity and so zero.
-__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + expf(-g)); }
+// 1 / (1 + exp(-g)) with an exponential that cannot overflow: of a large one the
+// reciprocal is zero where the value is not (g below -87.3).
+__device__ __forceinline__ float sigmoid(float g) {
+  const float t = expf(-fabsf(g));
+  return __builtin_amdgcn_rcpf(1.0f + t) * (g < 0.0f ? t : 1.0f);
+}
 
 __device__ __forceinline__ int64_t used_rows(const int* valid, int64_t rows) {
   if (!valid) return rows;
