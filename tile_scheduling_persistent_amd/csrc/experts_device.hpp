@@ -18,6 +18,12 @@ __device__ __forceinline__ ExpertRows expert_rows(const int* offsets, int e, int
   return {lo, hi > lo ? hi - lo : 0};
 }
 
+// Tiles are counted up to here: a program's tile and one stride of the grid more fit in
+// an int.  Offsets that rise have fewer; ones that rise and fall, whose ranges share
+// rows, may have more, which then no program takes.
+constexpr unsigned kMaxTiles = 0x7effffffu;
+__device__ __forceinline__ unsigned add_tiles(unsigned a, unsigned b) { return a + b < kMaxTiles ? a + b : kMaxTiles; }
+
 // s_lo[e], s_n[e]: the experts' rows; s_tile[e]: output tiles of the experts
 // before e, at `per` tiles for each `bm` rows begun (s_tile[experts]: all of them).
 // By the whole workgroup; ends with a barrier.
@@ -31,20 +37,20 @@ __device__ __forceinline__ void expert_tiles(const int* offsets, int experts, in
   __syncthreads();
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
-    int before = 0;
+    unsigned before = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
       const int e = e0 + lane;
-      const int t = e < experts ? (s_n[e] + bm - 1) / bm * per : 0;
-      int x = t;
+      unsigned x = e < experts ? (unsigned)((s_n[e] + bm - 1) / bm * per) : 0u;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
-        const int y = __shfl_up(x, d);
-        if (lane >= d) x += y;
+        const unsigned y = __shfl_up(x, d);
+        if (lane >= d) x = add_tiles(x, y);
       }
-      if (e < experts) s_tile[e] = before + x - t;
-      before += __shfl(x, 63);
+      const unsigned up = __shfl_up(x, 1);
+      if (e < experts) s_tile[e] = (int)add_tiles(before, lane > 0 ? up : 0u);
+      before = add_tiles(before, __shfl(x, 63));
     }
-    if (lane == 0) s_tile[experts] = before;
+    if (lane == 0) s_tile[experts] = (int)before;
   }
   __syncthreads();
 }

@@ -253,14 +253,14 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
       a.load(i - PD, (unsigned)kp, at);
   };
   auto aim = [&]() {
-    const int r0 = at * BR;
-    d.aim(lo + r0, n_rows - r0, p.D, p.ldd, n0, DFORM == kCodes ? np : p.N);
-    a.aim(lo + r0, n_rows - r0, p.A, kp, k0, kp);
+    const int64_t r0 = (int64_t)at * BR;
+    d.aim(lo + r0, (int)(n_rows - r0), p.D, p.ldd, n0, DFORM == kCodes ? np : p.N);
+    a.aim(lo + r0, (int)(n_rows - r0), p.A, kp, k0, kp);
   };
   auto fetch = [&](int stretch) {
-    const int r0 = stretch * kScaleRows;
-    d.fetch(p.sd, p.rows, lo + r0, n_rows - r0, n0 >> 7, np >> 7);
-    a.fetch(p.sa, p.rows, lo + r0, n_rows - r0, k0 >> 7, kp >> 7);
+    const int64_t r0 = (int64_t)stretch * kScaleRows;
+    d.fetch(p.sd, p.rows, lo + r0, (int)(n_rows - r0), n0 >> 7, np >> 7);
+    a.fetch(p.sa, p.rows, lo + r0, (int)(n_rows - r0), k0 >> 7, kp >> 7);
   };
   auto keep = [&](int stretch) {
     d.keep(stretch & 1);
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
     // slab s + 3, `at`, is loaded.  Where that is the second of a stretch, the scales of
     // the stretch after take the place of those of the one before, which the slab before
     // it was the last to read in another period.
-    for (int s = 0; (s + 1) * BR < n_rows; ++s) {
+    for (int s = 0; (int64_t)(s + 1) * BR < n_rows; ++s) {
       unsigned char* now = s & 1 ? stage1 : stage0;
       unsigned char* next = s & 1 ? stage0 : stage1;
       ++at;
