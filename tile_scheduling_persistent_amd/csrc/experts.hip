@@ -236,7 +236,7 @@ __device__ __forceinline__ int slot_of(const int* order, int64_t row, int64_t sl
 // XCD's workgroups then read the same 256 bytes of every token (16 bits), 2 MiB of
 // 8192 tokens, which stay in its L2 although a token is read for each of its slots in
 // the order of the experts (8192 x 8 x 4096 to e4m3, with the sort: a row's columns side
-// by side 105.6 us, XX).  The output is written in whole lines, past the caches where it
+// by side 105.6 us, so 83).  The output is written in whole lines, past the caches where it
 // would fill them (NT).
 template <int T, int R, bool QUANT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
