@@ -9,11 +9,12 @@
 // LDS as they do in memory, rows r of columns, and are read transposed
 // (ds_read_b64_tr_b16).
 //
-// Measured: 8192^3 811 us (1.36 PFLOP/s; a library product of bf16 reaches 1.41), 32768
-// rows of 16 experts x 4096 x 2048 530 us, with e4m3 D 504; 5000 rows of 8 x 1000 x 1408
-// with a base 43.  Bound by the matrix cores together with LDS, which takes 512 cycles of
-// writes and 1024 of reads for a slab's 2048 of MFMAs: without the conversions the time
-// stays, without the LDS writes it falls by 5 to 10%, without the loads by 11 to 19%.
+// Measured: 8192^3 802 us (1.37 PFLOP/s; a library product of bf16 reaches 1.41), with
+// e4m3 D 817; 32768 rows of 16 experts x 4096 x 2048 525 and 500; 5000 rows of 8 x 1000 x
+// 1408 with e4m3 D and a base 42.  Bound by the matrix cores together with LDS, which
+// takes 512 cycles of writes and 1024 of reads for a slab's 2048 of MFMAs: without the
+// conversions the time stays, without the LDS writes it falls by 5 to 10%, without the
+// loads by 11 to 19%.
 #include <atomic>
 #include <type_traits>
 #include <utility>
@@ -76,10 +77,11 @@ __device__ __forceinline__ void acc_written() {
 // Physical 16-byte chunk of logical chunk c in row r.  A transposing read of 32
 // lanes touches rows r .. r + 3 and r + 8 .. r + 11 at two adjacent chunks: bits 2-3
 // from r & 3 and bit 1 from bit 3 of r put those 16 chunks in distinct slots of a
-// 256-byte window.  Bit 0 does the same for the writes of every second chunk that
-// the conversion makes.
+// 256-byte window.  Bit 0 lets eight lanes, which the conversion has write every
+// second chunk, meet the eight slots of a 128-byte one (bit 0 from bit 4 of the chunk: 8192^3
+// of two e4m3 operands 827 us, so 817).
 __device__ __forceinline__ int swz(int r, int c) {
-  return c ^ (4 * (r & 3)) ^ (2 * ((r >> 3) & 1)) ^ (((c >> 4) ^ r) & 1);
+  return c ^ (4 * (r & 3)) ^ (2 * ((r >> 3) & 1)) ^ (((c >> 3) ^ r) & 1);
 }
 
 // How an operand lies in memory: bf16 whose rows start on 16 bytes, bf16 of any
@@ -193,7 +195,7 @@ struct Slab {
 // barrier per slab, between its two steps: behind it the second step's fragments are in
 // registers already and the next slab's first are read.  Scales come by stretches of 512
 // rows, a byte or two per thread, and lie in LDS as floats: a byte load beside every
-// part's own cost as much as the conversions and the LDS writes (8192^3 863 us, so 811).
+// part's own cost as much as the conversions and the LDS writes (8192^3 863 us, without 811).
 //
 // A workgroup takes one tile: a tile's time goes with its expert's rows, which only
 // the device knows, and the hardware hands the next workgroup to the next free CU.
