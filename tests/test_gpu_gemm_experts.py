@@ -205,6 +205,34 @@ def test_wgrad_rows_on_vectors(rows, n, k, experts, out, ldd):
     assert np.all(np.abs(host(dB) - ref) <= bound)
 
 
+@pytest.mark.parametrize("d", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,k", [(260, 390), (2064, 2050)])
+def test_wgrad_nan_rows_stay_in_their_expert(n, k, d):
+    """A row whose block is NaN makes its expert's gradient NaN in that block's columns
+    and leaves the experts before and after it, which share slabs of 64 rows."""
+    note(f"wgrad nan {n} {k} {d}")
+    rng = np.random.default_rng(9)
+    rows, experts = 640, 5
+    offsets = np.array([0, 100, 230, 500, 540, 640], np.int32)
+    qa, sa = ox.quant_rows(rng.standard_normal((rows, k)))
+    sa[1, 230] = 255  # expert 2's first row, columns 128 .. 255
+    qa[539, 0] = 0x7f  # expert 3's last row
+    kw = {}
+    D = gpu(rng.standard_normal((rows, n)).astype(np.float32)).bfloat16()
+    if d == "bf16":
+        D[99, 5] = float("nan")  # expert 0's last row
+    else:
+        qd, sd = ox.quant_rows(host(D))
+        qd[99, 5] = 0x7f
+        D, kw["d_scale"] = gpu(qd), gpu(sd)
+    dB = torch.zeros((experts, n, k), device="cuda:0")
+    pg.pgemm_run_experts_wgrad(config(), D, gpu(qa), dB, rows, n, k, gpu(sa), experts=experts, offsets=gpu(offsets), **kw)
+    sync()
+    want = np.zeros((experts, n, k), bool)
+    want[0, 5] = want[2, :, 128:256] = want[3, :, 0] = True
+    assert np.array_equal(np.isnan(host(dB)), want)
+
+
 def test_wgrad_without_rows():
     """No rows at all: zeros, or the base."""
     offsets = torch.zeros(4, dtype=torch.int32, device="cuda:0")

@@ -206,6 +206,11 @@ __global__ void __launch_bounds__(WAVES * 64) gemm_experts_stream_kernel(Experts
 // (SN-th) row, from row b on, so that a lane reads the scale words of all its blocks
 // at once and stores SN consecutive columns.  Which k an MFMA's lanes take is free
 // too, as long as both operands agree and a scale covers them all.
+//
+// Measured: 8192^3 385 us (2.85 PFLOP/s), to fp32 765; 65536 rows of 64 experts x 4096 x
+// 4096 1003 us.  Bound by the matrix cores (in use 0.65 of the time), the loads' arrival,
+// the tiles that an expert's last rows leave part empty (there an eighth) and the stores
+// (7% there).
 template <int BM, int BN, int NST_, int WN_>
 struct Shape {
   static constexpr int NST = NST_;
