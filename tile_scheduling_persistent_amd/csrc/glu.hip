@@ -5,7 +5,7 @@
 //   dg = dy u s (1 + g (1 - s)),  du = dy g s
 //
 // One pass each, row by row, bound by memory: 32768 x 2048 bf16 to e4m3 and back, both
-// with everything quantised, 876 MB in 164 us (5.3 TB/s).  Inputs that fill most of the
+// with everything quantised, 876 MB in 164 to 170 us (5.2 TB/s).  Inputs that fill most of the
 // Infinity Cache are loaded past the caches (169 us through them; smaller ones are
 // there from the product that made them).  Four rows to a wave: two 172 us, eight 184.
 #include "common.hpp"
