@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "../../include/pgemm.h"
+#include "call_buffers.hpp"
 #include "common.hpp"
 
 // A program numbering choose_order made, by the scheduler parameters, the
@@ -161,11 +162,7 @@ size_t span_bytes(int64_t rows, int64_t cols, size_t esz) {
   return b > (unsigned __int128)SIZE_MAX ? SIZE_MAX : (size_t)b;
 }
 
-bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
-  const char* x = (const char*)a;
-  const char* y = (const char*)b;
-  return an > 0 && bn > 0 && x < y + bn && y < x + an;
-}
+using pgk::overlaps;
 
 bool validate_only(const pgemm_args* args) {
   return args && (args->debug_flags & PGEMM_DEBUG_VALIDATE_ONLY);
@@ -1393,35 +1390,17 @@ pgemm_status prms_grad_run(pgemm_config* cfg, const void* dY, int y_type, int64_
 namespace {
 
 // The buffers of a call: each must lie in one allocation and start on its
-// elements' alignment, and no output may overlap another buffer, but for pairs
-// that may be the same exactly.
+// elements' alignment, and they must be apart (CallBuffers).
 struct CallBuffersCheck {
-  struct Buffer {
-    const void* p;
-    size_t bytes;
-    bool out;
-    const void* same;  // an input that an output may be
-  };
   CallRanges in;
-  int n = 0;
+  pgk::CallBuffers all;
   bool ok = true;
-  Buffer b[10];
   explicit CallBuffersCheck(int dev) : in(dev) {}
-  void add(const void* p, size_t bytes, size_t align, bool out, const void* same = nullptr) {
-    if (bytes == 0) return;
+  int add(const void* p, size_t bytes, size_t align, bool out, int same = -1) {
     ok = ok && buffer_ok(p, bytes, align, in);
-    b[n++] = {p, bytes, out, same};
+    return all.add(p, bytes, out, same);
   }
-  bool good() const {
-    if (!ok) return false;
-    for (int i = 0; i < n; ++i)
-      for (int j = i + 1; j < n; ++j) {
-        if (!b[i].out && !b[j].out) continue;
-        if (b[i].p == b[j].p && (b[i].same == b[j].p || b[j].same == b[i].p)) continue;
-        if (overlaps(b[i].p, b[i].bytes, b[j].p, b[j].bytes)) return false;
-      }
-    return true;
-  }
+  bool good() const { return ok && all.apart(); }
 };
 
 // Bytes of an e4m3 operand and of its scales.
@@ -1499,8 +1478,8 @@ pgemm_status pmoe_combine_run(pgemm_config* cfg, const void* X, int x_type, int6
   in.add(X, matrix_bytes(slots, cols, ldx, xs), xs, false);
   in.add(place, sb, 4, false);
   in.add(weights, weights ? sb : 0, 4, false);
-  in.add(R, R ? matrix_bytes(tokens, cols, ldr, ys) : 0, ys, false);
-  in.add(Y, matrix_bytes(tokens, cols, ldy, ys), ys, true, ldr == ldy ? R : nullptr);
+  const int r = in.add(R, R ? matrix_bytes(tokens, cols, ldr, ys) : 0, ys, false);
+  in.add(Y, matrix_bytes(tokens, cols, ldy, ys), ys, true, ldr == ldy ? r : -1);
   if (!in.good()) return PGEMM_ERR_INVALID;
   DeviceGuard g(cfg->device);
   if (!g.ok) return PGEMM_ERR_DEVICE;
@@ -1628,8 +1607,8 @@ pgemm_status pgemm_run_experts_wgrad(pgemm_config* cfg, const void* D, int d_typ
   in.add(A, fp8_bytes(rows, K), 1, false);
   in.add(a_scale, fp8_scale_bytes(rows, K), 1, false);
   in.add(offsets, offsets ? ((size_t)experts + 1) * 4 : 0, 4, false);
-  in.add(base, base ? bb : 0, bs, false);
-  in.add(dB, bb, bs, true, base);
+  const int from = in.add(base, base ? bb : 0, bs, false);
+  in.add(dB, bb, bs, true, from);
   if (!in.good()) return PGEMM_ERR_INVALID;
   if ((fp8 && !aligned(D, 16)) || !aligned(A, 16)) return PGEMM_ERR_UNSUPPORTED;
   DeviceGuard g(cfg->device);
