@@ -632,9 +632,9 @@ PGEMM_API pgemm_status pfp8_quant_weights_run(pgemm_config* cfg, const void* W, 
  * offsets as pmoe_sort_run writes them, on the device (NULL with experts == 1: one
  * matrix and all rows); rows outside of every expert's are left as they were.  K must
  * be a multiple of 128 (PGEMM_ERR_INVALID otherwise); A and B 16-byte aligned, K below
- * 2^22, experts at most PMOE_MAX_EXPERTS, rows and blocks of 16 x 16 of C, with one
- * row of blocks more per expert, countable in 31 bits (PGEMM_ERR_UNSUPPORTED
- * otherwise); any N.  The kernel follows from rows / experts: the sums' order, and so
+ * 2^22, experts at most PMOE_MAX_EXPERTS, rows and N at most 2^31 - 257, blocks of 16 x
+ * 16 of C, with one row of blocks more per expert, countable in 31 bits
+ * (PGEMM_ERR_UNSUPPORTED otherwise); any N below that.  The kernel follows from rows / experts: the sums' order, and so
  * the last bits of C, depend on the sizes of the call. */
 PGEMM_API pgemm_status pgemm_run_experts(pgemm_config* cfg, const uint8_t* A, const uint8_t* a_scale, const uint8_t* B,
                                const uint8_t* b_scale, void* C, int c_type, int64_t rows, int64_t N, int64_t K,

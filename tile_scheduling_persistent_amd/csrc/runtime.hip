@@ -20,6 +20,7 @@
 #include "../../include/pgemm.h"
 #include "call_buffers.hpp"
 #include "common.hpp"
+#include "experts_limits.hpp"
 
 // A program numbering choose_order made, by the scheduler parameters, the
 // tile and (several problems per launch) each problem's first tile id and
@@ -1567,8 +1568,7 @@ pgemm_status pgemm_run_experts(pgemm_config* cfg, const uint8_t* A, const uint8_
       K % 128 != 0 || experts < 1 || (!offsets && experts != 1))
     return PGEMM_ERR_INVALID;
   if (c_type == PMX_F16 || experts > PMOE_MAX_EXPERTS || K >= 1 << 22) return PGEMM_ERR_UNSUPPORTED;
-  // rows, with a tile more, and tiles of 16 x 16 are counted in 31 bits
-  if (rows > kMaxDim - 256 || (rows / 16 + experts) * ((N + 15) / 16) > kMaxDim) return PGEMM_ERR_UNSUPPORTED;
+  if (!pgk::product_countable(rows, N, experts)) return PGEMM_ERR_UNSUPPORTED;
   if (rows == 0) return PGEMM_OK;
   const size_t cs = type_size(c_type);
   CallBuffersCheck in(cfg->device);
