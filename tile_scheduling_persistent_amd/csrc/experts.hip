@@ -236,8 +236,8 @@ __device__ __forceinline__ int slot_of(const int* order, int64_t row, int64_t sl
 // XCD's workgroups then read the same 256 bytes of every token (16 bits), 2 MiB of
 // 8192 tokens, which stay in its L2 although a token is read for each of its slots in
 // the order of the experts (8192 x 8 x 4096 to e4m3, with the sort: a row's columns side
-// by side 105.6 us, so 83).  The output is written in whole lines, past the caches where it
-// would fill them (NT).
+// by side 105.6 us, so 83).  NT: the output goes past the caches, where the tokens stay for
+// their other slots (gather_typed has the rule).
 template <int T, int R, bool QUANT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
   constexpr int ROWS = 16 * R;
@@ -413,16 +413,27 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradPa
 
 constexpr int64_t kPastCaches = 128ll << 20;
 
+// Past the caches go codes of any size, which 16 lanes write by whole lines, and rows of 16
+// bits that would fill most of the Infinity Cache, where they start on lines.  us, past them
+// / through them.  Codes, with the product that reads them next: 16 MB 61 / 72, 256 MB 404
+// / 448; alone 8.0 / 12.3 and 76 / 167.  bf16, 8192 x 8 x 4096: 128 / 173; rows that start
+// on 16 bytes (a stride of 4104) 250 / 248, of 5000 columns 321 / 289, of 4095 305 / 280.  An
+// access of fp32 covers half of each line: 4096 x 8 x 4096 259 / 163, 4095 columns 317 / 239.
 template <int T, bool QUANT>
 void gather_typed(const GatherParams& p, hipStream_t stream) {
   const int64_t slots = p.tokens * p.topk, groups = (p.cols + 127) / 128, tall = (slots + 127) / 128 * groups;
   const dim3 block(kRowThreads);
-  if (tall >= 4 * p.cus && (QUANT || slots * p.cols * size_of(T) >= kPastCaches))
-    hipLaunchKernelGGL((gather_kernel<T, 8, QUANT, true>), row_grid(tall), block, 0, stream, p);
-  else if (!QUANT && tall >= 4 * p.cus)
-    hipLaunchKernelGGL((gather_kernel<T, 8, false, false>), row_grid(tall), block, 0, stream, p);
-  else
+  if (tall < 4 * p.cus) {
     hipLaunchKernelGGL((gather_kernel<T, 1, QUANT, false>), row_grid((slots + 15) / 16 * groups), block, 0, stream, p);
+    return;
+  }
+  if constexpr (QUANT || T != kTypeF32) {
+    if (QUANT || (slots * p.cols * size_of(T) >= kPastCaches && rows_at(p.Y, p.ldy, size_of(T), 128))) {
+      hipLaunchKernelGGL((gather_kernel<T, 8, QUANT, true>), row_grid(tall), block, 0, stream, p);
+      return;
+    }
+  }
+  if constexpr (!QUANT) hipLaunchKernelGGL((gather_kernel<T, 8, false, false>), row_grid(tall), block, 0, stream, p);
 }
 template <int T>
 void gather_out(const GatherParams& p, hipStream_t stream) {
