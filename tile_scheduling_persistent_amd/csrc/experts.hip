@@ -337,8 +337,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {
 
 // A wave takes RW rows, all of their columns: dx = w dy, and the dot product of
 // dy with the row for dw.  NT: rows in and out past the caches, which leaves those to dy
-// that is read for each slot (us: 8192 x 8 x 4096 to e4m3 215 -> 208, 5000 x 2 x 7000 46.8
-// -> 43.0; rows that fit in the Infinity Cache, 512 x 8 x 4096, 15.3 -> 17.0).
+// that is read for each slot (combine_grad_typed has the rule).
 template <int T, int RW, bool QUANT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradParams p) {
   constexpr int ROWS = 4 * RW;
@@ -453,13 +452,20 @@ void combine_out(const CombineParams& p, hipStream_t stream) {
   p.y_type == T ? combine_typed<T, T>(p, stream) : combine_typed<T, kTypeF32>(p, stream);
 }
 
+// Rows that fill most of the Infinity Cache go past the caches, but for fp32 results that
+// start on lines, of which an access covers half of each.  us, past them / through them:
+// 8192 x 8 x 4096 bf16 241 / 250, without dw 159 / 169, to e4m3 207 / 214; 4095 columns 286 /
+// 314, 168 / 226 and 265 / 270; rows that fit, 512 x 8 x 4096, 17.0 / 15.3.  fp32, 4096 x 8 x
+// 4096 294 / 274 and 210 / 173, to e4m3 192 / 199; rows off lines, 4095 columns 297 / 295 and
+// 204 / 230, a stride of 4100 293 / 294 and 207 / 226.
 template <int T, bool QUANT>
 void combine_grad_typed(const CombineGradParams& p, hipStream_t stream) {
   const int64_t slots = p.tokens * p.topk;
   const dim3 block(kRowThreads);
+  const bool half_lines = T == kTypeF32 && !QUANT && rows_at(p.dX, p.lddx, size_of(T), 128);
   if ((slots + 15) / 16 < 2 * p.cus)
     hipLaunchKernelGGL((combine_grad_kernel<T, 1, QUANT, false>), row_grid((slots + 3) / 4), block, 0, stream, p);
-  else if (slots * p.cols * size_of(T) < kPastCaches)
+  else if (slots * p.cols * size_of(T) < kPastCaches || half_lines)
     hipLaunchKernelGGL((combine_grad_kernel<T, 4, QUANT, false>), row_grid((slots + 15) / 16), block, 0, stream, p);
   else
     hipLaunchKernelGGL((combine_grad_kernel<T, 4, QUANT, true>), row_grid((slots + 15) / 16), block, 0, stream, p);
