@@ -128,7 +128,7 @@ def test_gather_and_combine_grad(routed, cols, ldx, ldy, x, out):
         assert torch.equal(got[4][lo:lo + PART], want[4]), lo
 
 
-@pytest.mark.parametrize("rows,cols,extra", [(9000, 2048, 0), (8900, 2055, 3), (9000, 4104, 8)])
+@pytest.mark.parametrize("rows,cols,extra", [(9000, 2048, 0), (8900, 2055, 3), (9000, 4104, 8), (33000, 2048, 64)])
 @pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("out", ["same", "fp8_b128"])
 def test_glu(rows, cols, extra, x, out):

@@ -5,9 +5,8 @@
 //   dg = dy u s (1 + g (1 - s)),  du = dy g s
 //
 // One pass each, row by row, bound by memory: 32768 x 2048 bf16 to e4m3 and back, both
-// with everything quantised, 876 MB in 164 to 170 us (5.2 TB/s).  Inputs that fill most of the
-// Infinity Cache are loaded past the caches (169 us through them; smaller ones are
-// there from the product that made them).  Four rows to a wave: two 172 us, eight 184.
+// with everything quantised, 876 MB in 164 to 173 us (5.1 to 5.3 TB/s).  Four rows to a wave:
+// two 172 us, eight 184.
 #include "common.hpp"
 #include "fp8_rows.hpp"
 
@@ -197,23 +196,47 @@ void glu_grad_sized(const GluGradParams& p, hipStream_t stream) {
   }
 }
 
+// Inputs that fill most of the Infinity Cache are loaded past the caches where a load
+// covers whole lines: 16 bits, rows (and u's half of X) that start on them; smaller ones
+// are there from the product that made them.  us, past them / through them.  32768 x 2048
+// bf16: forward 92.7 / 93.3, backward from X 119 / 122, to e4m3 87 / 87 to 90; 17000 rows
+// forward 48.2 / 50.3; 8192 x 8192 forward, rows not quantised, 94.6 / 96.9, backward 92.4 /
+// 94.4.  Rows on 16 bytes only, 2040 columns: forward 127 / 121, without what is kept 100 /
+// 97.8; rows that start anywhere, 2047 columns, 231 / 216 and 204 / 189 (backward level).
+// fp32, of which a load covers half of each line, 16384 x 2048: forward 95 / 90 and 81 / 76,
+// backward 106 / 103; 2047 columns 123 / 112 and 106 / 98.
+template <int T>
+bool past_caches(const void* x, int64_t ld, int64_t rows, int64_t cols) {
+  return rows * cols * size_of(T) >= kPastCaches && rows_at(x, ld, size_of(T), 128);
+}
+
 template <int T>
 void glu_typed(const GluParams& p, hipStream_t stream) {
-  if (row_tiles(p.rows, p.cols, kTall) < 2 * p.cus)
+  if (row_tiles(p.rows, p.cols, kTall) < 2 * p.cus) {
     glu_sized<T, 1, false>(p, stream);
-  else if (p.rows * p.cols * 2 * size_of(T) < kPastCaches)
-    glu_sized<T, kTall, false>(p, stream);
-  else
-    glu_sized<T, kTall, true>(p, stream);
+    return;
+  }
+  if constexpr (T != kTypeF32) {
+    if (past_caches<T>(p.X, p.ldx, p.rows, 2 * p.cols) && p.cols * size_of(T) % 128 == 0) {
+      glu_sized<T, kTall, true>(p, stream);
+      return;
+    }
+  }
+  glu_sized<T, kTall, false>(p, stream);
 }
 template <int T>
 void glu_grad_typed(const GluGradParams& p, hipStream_t stream) {
-  if (row_tiles(p.rows, p.cols, kTall) < 2 * p.cus)
+  if (row_tiles(p.rows, p.cols, kTall) < 2 * p.cus) {
     glu_grad_sized<T, 1, false>(p, stream);
-  else if (p.rows * p.cols * size_of(T) < kPastCaches)
-    glu_grad_sized<T, kTall, false>(p, stream);
-  else
-    glu_grad_sized<T, kTall, true>(p, stream);
+    return;
+  }
+  if constexpr (T != kTypeF32) {
+    if (past_caches<T>(p.dY, p.ldy, p.rows, p.cols)) {
+      glu_grad_sized<T, kTall, true>(p, stream);
+      return;
+    }
+  }
+  glu_grad_sized<T, kTall, false>(p, stream);
 }
 
 }  // namespace
