@@ -472,6 +472,13 @@ Instance tiled() {
 
 }  // namespace
 
+// Tiles of 256 x 256 where they give every CU one and do not cover half as much again as
+// tiles of 128 x 128 (of 128 columns they leave half empty).  us, 256 x 256 / 128 x 128, whole
+// tiles: 32768 rows of 16 experts x 4096 x 2048 523 / 678, 8192 of 4 x 2048 x 2048 69 / 91, of 64 x
+// 256 x 2048 44 / 49.  A third more: 32768 of 16 x 300 x 2048 70 / 74, 8192 of 64 x 300 x 1024 42 /
+// 37, of 32 x 1152 x 640 (e4m3) 45 / 39.  Twice as much: 8192 of 64 x 128 x 2048 40 / 26, 32768
+// (e4m3) 60 / 42.  Fewer tiles than CUs: 8192 of 3 x 2048 x 2048 76 / 83, of 8 x 1000 x 1408 39 /
+// 40, 5000 (e4m3) 31.3 / 30.7.
 hipError_t launch_gemm_experts_wgrad(const WgradParams& p, int cus, hipStream_t stream) {
   static const Instance big[2][2] = {{tiled<256, 256, kWide, false>(), tiled<256, 256, kWide, true>()},
                                      {tiled<256, 256, kCodes, false>(), tiled<256, 256, kCodes, true>()}};
@@ -479,9 +486,10 @@ hipError_t launch_gemm_experts_wgrad(const WgradParams& p, int cus, hipStream_t 
                                        {tiled<128, 128, kCodes, false>(), tiled<128, 128, kCodes, true>()},
                                        {tiled<128, 128, kNarrow, false>(), tiled<128, 128, kNarrow, true>()}};
   const int64_t tiles = (int64_t)p.experts * ((p.N + 255) / 256) * ((p.K + 255) / 256);
+  const int64_t quarters = (int64_t)p.experts * ((p.N + 127) / 128) * ((p.K + 127) / 128);
   const int f32 = p.out_f32 ? 1 : 0;
   if (!p.sd && ((reinterpret_cast<uintptr_t>(p.D) & 15) != 0 || (p.ldd & 7) != 0)) return small[2][f32].launch(p, stream);
-  return (tiles >= cus ? big : small)[p.sd ? 1 : 0][f32].launch(p, stream);
+  return (tiles >= cus && 8 * tiles < 3 * quarters ? big : small)[p.sd ? 1 : 0][f32].launch(p, stream);
 }
 
 }  // namespace pgk
