@@ -296,9 +296,13 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(GatherParams p) {
 
 // A wave takes 512 columns of a token: up to eight of its slots' rows at a time
 // are on their way together, summed in fp32 in the slots' order.
-// NT: rows and result past the caches, where the rows fill most of the Infinity Cache
-// (us, with a norm of the result: 8192 x 8 x 4096 bf16 162 -> 139, alone 130 -> 108;
-// 2048 tokens 43.2 -> 40.2; 1024 tokens, whose rows may still be there, 22.2 -> 25.0).
+// NT: rows and result past the caches, where the rows fill most of the Infinity Cache, in
+// every type and wherever rows start (a row is read once, and most of what moves is read).
+// us, past them / through them, with a norm of the result: 8192 x 8 x 4096 bf16 139 / 162,
+// alone 108 / 130; 2048 tokens 40.2 / 43.2; 1024 tokens, whose rows may still be there, 25.0
+// / 22.2.  bf16 8192 x 8, a stride of 4104 121 / 131, 5000 columns 158 / 162, 4095 columns 204
+// / 207, to fp32 137 / 151; fp32 4096 x 8 x 4096 122 / 131, 4095 columns 146 / 152, 1100 x 8 x
+// 4096 38.3 / 38.5.
 constexpr int kSlotsAtOnce = 8;
 template <int T, int YT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(CombineParams p) {

@@ -197,8 +197,9 @@ void glu_grad_sized(const GluGradParams& p, hipStream_t stream) {
 }
 
 // Inputs that fill most of the Infinity Cache are loaded past the caches where a load
-// covers whole lines: 16 bits, rows (and u's half of X) that start on them; smaller ones
-// are there from the product that made them.  us, past them / through them.  32768 x 2048
+// covers whole lines: 16 bits, rows (and u's half of X) that start on them.  Smaller ones are
+// not, behind the product that made them, 16 MB, both calls, 27.0 / 27.3 (but 64 MB 64.5 /
+// 71.3, 128 MB 128 / 128).  us, past the caches / through them.  32768 x 2048
 // bf16: forward 92.7 / 93.3, backward from X 119 / 122, to e4m3 87 / 87 to 90; 17000 rows
 // forward 48.2 / 50.3; 8192 x 8192 forward, rows not quantised, 94.6 / 96.9, backward 92.4 /
 // 94.4.  Rows on 16 bytes only, 2040 columns: forward 127 / 121, without what is kept 100 /
